@@ -19,14 +19,17 @@ LMOE_OK, LMOE_ERR_INVALID_ARG, LMOE_ERR_UNSUPPORTED, LMOE_ERR_CUDA, LMOE_ERR_OOM
 LMOE_ACT_SITU, LMOE_ACT_SWIGLU = 0, 1
 LMOE_W_MXFP4, LMOE_W_FP8_BLOCK128 = 0, 1
 
-# Every symbol include/lmoe.h declares.
+# Every symbol the headers under include/ declare.
 EXPORTS = ("lmoe_create", "lmoe_route", "lmoe_forward", "lmoe_forward_host", "lmoe_dispatch",
            "lmoe_debug_tensor", "lmoe_sync_status", "lmoe_last_launch_count", "lmoe_set_profiling",
            "lmoe_set_profiling_period",
            "lmoe_profile_get", "lmoe_last_active_experts", "lmoe_destroy", "lmoe_status_string",
            "lmoe_dispatch_noalloc", "lmoe_keep_f32_output", "lmoe_selftest_timeout", "lmoe_tc_peak",
            "lmoe_qb_update", "lmoe_qb_histogram", "lmoe_qb_update_from_histogram",
-           "lmoe_ep_dispatch", "lmoe_ep_experts", "lmoe_ep_combine")
+           "lmoe_ep_dispatch", "lmoe_ep_experts", "lmoe_ep_combine",
+           "lmoe_add_rms_norm", "lmoe_add_rms_norm_backward_workspace", "lmoe_add_rms_norm_backward",
+           "lmoe_ffn_create", "lmoe_ffn_forward", "lmoe_ffn_backward", "lmoe_ffn_forward_mx",
+           "lmoe_ffn_sync_status", "lmoe_ffn_last_launch_count", "lmoe_ffn_destroy")
 NOALLOC_MAX_ASSIGNMENTS = 65536
 NOALLOC_MAX_EXPERTS = 2048
 PROFILE_ALL_STAGES = 0x1FF
@@ -53,6 +56,19 @@ class LmoeWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in _WEIGHT_FIELDS]
 
 
+class LmoeFfnConfig(ctypes.Structure):
+    _fields_ = [("d_model", ctypes.c_int), ("d_ff", ctypes.c_int), ("act", ctypes.c_int),
+                ("situ_beta", ctypes.c_float), ("situ_linear_beta", ctypes.c_float), ("wfmt", ctypes.c_int),
+                ("max_tokens", ctypes.c_int), ("training", ctypes.c_int)]
+
+
+_FFN_WEIGHT_FIELDS = ("gate", "up", "down", "gate_s", "up_s", "down_s")
+
+
+class LmoeFfnWeights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in _FFN_WEIGHT_FIELDS]
+
+
 class LmoeError(RuntimeError):
     def __init__(self, call: str, status: int):
         super().__init__(f"{call} failed: {status_string(status)} ({status})")
@@ -72,6 +88,7 @@ def load_library(path: str = LIB_PATH):
                                "(run python -m latent_mixture_experts_gb300.build)")
         lib = ctypes.CDLL(path)
         P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        L, F = ctypes.c_int64, ctypes.c_float
         sig = {
             "lmoe_create": (I, [ctypes.POINTER(LmoeConfig), ctypes.POINTER(LmoeWeights), P, ctypes.POINTER(P)]),
             "lmoe_route": (I, [P, P, I, P, P, P]),
@@ -97,6 +114,17 @@ def load_library(path: str = LIB_PATH):
             "lmoe_ep_dispatch": (I, [P, P, I, P, P, P, P, P]),
             "lmoe_ep_experts": (I, [P, P, P, I, P, P]),
             "lmoe_ep_combine": (I, [P, P, I, P, P]),
+            "lmoe_add_rms_norm": (I, [P, L, P, L, I, I, I, P, F, P, P, I, P, P]),
+            "lmoe_add_rms_norm_backward_workspace": (I, [I, I, ctypes.POINTER(S)]),
+            "lmoe_add_rms_norm_backward": (I, [P, L, P, L, P, L, I, I, I, P, F, P, P, P, S, P]),
+            "lmoe_ffn_create": (I, [ctypes.POINTER(LmoeFfnConfig), ctypes.POINTER(LmoeFfnWeights), P,
+                                    ctypes.POINTER(P)]),
+            "lmoe_ffn_forward": (I, [P, P, L, I, P, P, P, P]),
+            "lmoe_ffn_backward": (I, [P, P, L, P, P, P, L, I, P, P, P, P, P]),
+            "lmoe_ffn_forward_mx": (I, [P, P, P, I, P, P]),
+            "lmoe_ffn_sync_status": (I, [P, P]),
+            "lmoe_ffn_last_launch_count": (I, [P]),
+            "lmoe_ffn_destroy": (I, [P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)

@@ -1,0 +1,310 @@
+// C ABI of the norm and of the dense feed-forward block: argument checks,
+// workspace, tensor maps, launch sequences.
+//
+//   forward:  gate/up products + activation -> hid;  hid x down
+//   backward: dy x down + activation gradient -> dg, du, hid;
+//             dg x gate + du x up -> dx;  dg^T x, du^T x, dy^T hid in one launch
+#include <cmath>
+#include <new>
+
+#include "../../include/lmoe_ffn.h"
+#include "ffn_internal.h"
+#include "lmoe_internal.h"
+#include "tmap.h"
+
+using namespace lmoe;
+
+struct lmoe_ffn_ctx {
+  lmoe_ffn_config cfg;
+  lmoe_ffn_weights w;
+  int ctas = 0;                 // resident CTAs of the pair kernels
+  void* pool = nullptr;
+  int* err = nullptr;
+  void *hid = nullptr, *dg = nullptr, *du = nullptr;
+  CUtensorMap gate, up, down;         // K contiguous, boxes of 64 x 128 rows
+  CUtensorMap gate_n, up_n, down_n;   // the same memory as N contiguous operands, boxes of 64 x 64
+  int launches = 0;
+};
+
+namespace {
+
+lmoe_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return LMOE_OK;
+  return e == cudaErrorMemoryAllocation ? LMOE_ERR_OOM : LMOE_ERR_CUDA;
+}
+#define FFN_TRY(expr)                              \
+  do {                                             \
+    const cudaError_t e_ = (expr);                 \
+    if (e_ != cudaSuccess) return cuda_status(e_); \
+  } while (0)
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool usable(const void* p) { return p && aligned16(p); }
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// K-contiguous bf16 operand [rows][K]: boxes of 64 K values x 128 rows.
+bool map_k(CUtensorMap* m, const void* base, int K, int rows, long long ld) {
+  return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, K, rows, 2 * ld, 64, 128,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// The transposed use of [K][N]: boxes of 64 N values x 64 K rows.
+bool map_n(CUtensorMap* m, const void* base, int N, int K, long long ld) {
+  return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, N, K, 2 * ld, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+lmoe_status norm_args(int T, int d, const void* w, float eps, bool mx) {
+  if (T < 0 || d < 1 || !usable(w) || !(eps >= 0.0f) || std::isinf(eps)) return LMOE_ERR_INVALID_ARG;
+  if (d % (mx ? 32 : 8) != 0 || d > kNormMaxWidth) return LMOE_ERR_UNSUPPORTED;
+  return LMOE_OK;
+}
+lmoe_status row_args(const void* p, int64_t ld, int d) {
+  if (!usable(p) || ld < d) return LMOE_ERR_INVALID_ARG;
+  return ld % 8 == 0 ? LMOE_OK : LMOE_ERR_UNSUPPORTED;
+}
+#define FFN_TRY_STATUS(expr)            \
+  do {                                  \
+    const lmoe_status s_ = (expr);      \
+    if (s_ != LMOE_OK) return s_;       \
+  } while (0)
+
+}  // namespace
+
+extern "C" {
+
+lmoe_status lmoe_add_rms_norm(const void* x, int64_t ldx, const void* r, int64_t ldr, lmoe_stream_type stream_type,
+                              int T, int d, const void* w, float eps, void* h, void* y, lmoe_norm_out fmt,
+                              uint8_t* scale, cudaStream_t stream) {
+  if ((fmt != LMOE_NORM_OUT_BF16 && fmt != LMOE_NORM_OUT_MXFP8) ||
+      (stream_type != LMOE_STREAM_BF16 && stream_type != LMOE_STREAM_FP32))
+    return LMOE_ERR_INVALID_ARG;
+  const bool mx = fmt == LMOE_NORM_OUT_MXFP8;
+  FFN_TRY_STATUS(norm_args(T, d, w, eps, mx));
+  if (T == 0) return LMOE_OK;
+  FFN_TRY_STATUS(row_args(x, ldx, d));
+  if (r) {
+    FFN_TRY_STATUS(row_args(r, ldr, d));
+    if (!usable(h)) return LMOE_ERR_INVALID_ARG;
+  }
+  if (!usable(y) || (mx && !scale)) return LMOE_ERR_INVALID_ARG;
+  return cuda_status(launch_add_rms_norm(x, ldx, r, ldr, stream_type == LMOE_STREAM_FP32, T, d, w, eps, h, y,
+                                         mx ? scale : nullptr, stream));
+}
+
+lmoe_status lmoe_add_rms_norm_backward_workspace(int T, int d, size_t* bytes) {
+  if (!bytes || T < 0 || d < 1) return LMOE_ERR_INVALID_ARG;
+  if (d % 8 != 0 || d > kNormMaxWidth) return LMOE_ERR_UNSUPPORTED;
+  *bytes = T == 0 ? 0 : 4 * rms_norm_bwd_partials(T, d);
+  return LMOE_OK;
+}
+
+lmoe_status lmoe_add_rms_norm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* dh,
+                                       int64_t lddh, lmoe_stream_type stream_type, int T, int d, const void* w,
+                                       float eps, void* dx, float* dw, void* ws, size_t ws_bytes,
+                                       cudaStream_t stream) {
+  if (stream_type != LMOE_STREAM_BF16 && stream_type != LMOE_STREAM_FP32) return LMOE_ERR_INVALID_ARG;
+  FFN_TRY_STATUS(norm_args(T, d, w, eps, false));
+  if (!usable(dw)) return LMOE_ERR_INVALID_ARG;
+  if (T == 0) return cuda_status(cudaMemsetAsync(dw, 0, 4 * static_cast<size_t>(d), stream));
+  FFN_TRY_STATUS(row_args(dy, lddy, d));
+  FFN_TRY_STATUS(row_args(h, ldh, d));
+  if (dh) FFN_TRY_STATUS(row_args(dh, lddh, d));
+  if (!usable(dx) || !usable(ws) || ws_bytes < 4 * rms_norm_bwd_partials(T, d)) return LMOE_ERR_INVALID_ARG;
+  return cuda_status(launch_rms_norm_bwd(dy, lddy, h, ldh, dh, lddh, stream_type == LMOE_STREAM_FP32, T, d, w, eps,
+                                         dx, static_cast<float*>(ws), dw, stream));
+}
+
+lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* w, cudaStream_t stream,
+                            lmoe_ffn_handle* out) {
+  (void)stream;
+  if (!out) return LMOE_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!cfg || !w) return LMOE_ERR_INVALID_ARG;
+  const int d = cfg->d_model, F = cfg->d_ff;
+  if (d < 1 || F < 1 || cfg->max_tokens < 1 || (cfg->act != LMOE_ACT_SITU && cfg->act != LMOE_ACT_SWIGLU) ||
+      (cfg->wfmt != LMOE_FFN_W_BF16 && cfg->wfmt != LMOE_FFN_W_MXFP8) || (cfg->training != 0 && cfg->training != 1))
+    return LMOE_ERR_INVALID_ARG;
+  if (cfg->act == LMOE_ACT_SITU && !(cfg->situ_beta > 0.0f && cfg->situ_linear_beta > 0.0f &&
+                                     std::isfinite(cfg->situ_beta) && std::isfinite(cfg->situ_linear_beta)))
+    return LMOE_ERR_INVALID_ARG;
+  const bool mx = cfg->wfmt == LMOE_FFN_W_MXFP8;
+  if (!usable(w->gate) || !usable(w->up) || !usable(w->down)) return LMOE_ERR_INVALID_ARG;
+  if (mx && (!usable(w->gate_s) || !usable(w->up_s) || !usable(w->down_s))) return LMOE_ERR_INVALID_ARG;
+  if (d % (mx ? 32 : 8) || F % (mx ? 32 : 8) || (mx && cfg->training)) return LMOE_ERR_UNSUPPORTED;
+  if (mx) return LMOE_ERR_UNSUPPORTED;
+  int dev = 0, major = 0, minor = 0;
+  FFN_TRY(cudaGetDevice(&dev));
+  FFN_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
+  FFN_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
+  if (major != 10 || minor != 3) return LMOE_ERR_UNSUPPORTED;
+  lmoe_ffn_ctx* h = new (std::nothrow) lmoe_ffn_ctx;
+  if (!h) return LMOE_ERR_OOM;
+  h->cfg = *cfg;
+  h->w = *w;
+  const size_t act_bytes = (static_cast<size_t>(cfg->max_tokens) * F * 2 + 255) / 256 * 256;
+  const size_t bytes = 256 + act_bytes * (cfg->training ? 3 : 1);
+  cudaError_t e = ffn_pair_ctas(&h->ctas);
+  if (e == cudaSuccess) e = cudaMalloc(&h->pool, bytes);
+  if (e == cudaSuccess) e = cudaMemset(h->pool, 0, 256);
+  if (e != cudaSuccess) {
+    lmoe_ffn_destroy(h);
+    return cuda_status(e);
+  }
+  uint8_t* base = static_cast<uint8_t*>(h->pool);
+  h->err = reinterpret_cast<int*>(base);
+  h->hid = base + 256;
+  h->dg = base + 256 + act_bytes;
+  h->du = base + 256 + 2 * act_bytes;
+  const bool ok = map_k(&h->gate, w->gate, d, F, d) && map_k(&h->up, w->up, d, F, d) &&
+                  map_k(&h->down, w->down, F, d, F) && map_n(&h->gate_n, w->gate, d, F, d) &&
+                  map_n(&h->up_n, w->up, d, F, d) && map_n(&h->down_n, w->down, F, d, F);
+  if (!ok) {
+    lmoe_ffn_destroy(h);
+    return LMOE_ERR_CUDA;
+  }
+  *out = h;
+  return LMOE_OK;
+}
+
+lmoe_status lmoe_ffn_destroy(lmoe_ffn_handle h) {
+  if (!h) return LMOE_OK;
+  cudaError_t e = cudaSuccess;
+  if (h->pool) e = cudaFree(h->pool);   // waits for the device
+  delete h;
+  return cuda_status(e);
+}
+
+lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int T, void* out, void* gate, void* up,
+                             cudaStream_t stream) {
+  if (!h || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
+  if (h->cfg.wfmt != LMOE_FFN_W_BF16) return LMOE_ERR_UNSUPPORTED;
+  h->launches = 0;
+  if (T == 0) return LMOE_OK;
+  const int d = h->cfg.d_model, F = h->cfg.d_ff;
+  FFN_TRY_STATUS(row_args(x, ldx, d));
+  if (!usable(out) || (gate == nullptr) != (up == nullptr) || !aligned16(gate) || !aligned16(up))
+    return LMOE_ERR_INVALID_ARG;
+  FfnPairParams p = {};
+  p.b1 = h->cfg.situ_beta;
+  p.b2 = h->cfg.situ_linear_beta;
+  p.act = h->cfg.act == LMOE_ACT_SWIGLU;
+  p.err = h->err;
+  p.nprod = 1;
+  p.b[0] = h->gate;
+  p.b[1] = h->up;
+  p.M[0] = T;
+  p.N[0] = F;
+  p.tiles_n[0] = ceil_div(F, 128);
+  p.tile_end[0] = ceil_div(T, 256) * p.tiles_n[0];
+  p.nkb = p.nkb0 = ceil_div(d, 64);
+  p.out[0] = h->hid;
+  p.out[1] = gate;
+  p.out[2] = up;
+  if (!map_k(&p.a[0], x, d, T, ldx)) return LMOE_ERR_CUDA;
+  FFN_TRY(launch_ffn_pair(kFfnGateUp, p, h->ctas, stream));
+  p.b[0] = h->down;
+  p.N[0] = d;
+  p.tiles_n[0] = ceil_div(d, 256);
+  p.tile_end[0] = ceil_div(T, 256) * p.tiles_n[0];
+  p.nkb = p.nkb0 = ceil_div(F, 64);
+  p.out[0] = out;
+  if (!map_k(&p.a[0], h->hid, F, T, F)) return LMOE_ERR_CUDA;
+  FFN_TRY(launch_ffn_pair(kFfnPlain, p, h->ctas, stream));
+  h->launches = 2;
+  return LMOE_OK;
+}
+
+lmoe_status lmoe_ffn_backward(lmoe_ffn_handle h, const void* x, int64_t ldx, const void* gate, const void* up,
+                              const void* dy, int64_t lddy, int T, void* dx, void* dwg, void* dwu, void* dwd,
+                              cudaStream_t stream) {
+  if (!h || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
+  if (h->cfg.wfmt != LMOE_FFN_W_BF16 || !h->cfg.training) return LMOE_ERR_UNSUPPORTED;
+  h->launches = 0;
+  const int d = h->cfg.d_model, F = h->cfg.d_ff;
+  if (!aligned16(dx) || !aligned16(dwg) || !aligned16(dwu) || !aligned16(dwd)) return LMOE_ERR_INVALID_ARG;
+  if (T == 0) {
+    for (void* w : {dwg, dwu, dwd})
+      if (w) FFN_TRY(cudaMemsetAsync(w, 0, 2 * static_cast<size_t>(d) * F, stream));
+    return LMOE_OK;
+  }
+  FFN_TRY_STATUS(row_args(x, ldx, d));
+  FFN_TRY_STATUS(row_args(dy, lddy, d));
+  if (!usable(gate) || !usable(up)) return LMOE_ERR_INVALID_ARG;
+  if (!dx && !dwg && !dwu && !dwd) return LMOE_OK;
+
+  FfnPairParams p = {};
+  p.b1 = h->cfg.situ_beta;
+  p.b2 = h->cfg.situ_linear_beta;
+  p.act = h->cfg.act == LMOE_ACT_SWIGLU;
+  p.err = h->err;
+  // dhid = dy down, and its activation gradient
+  p.nprod = 1;
+  p.b[0] = h->down_n;
+  p.in_g = gate;
+  p.in_u = up;
+  p.out[0] = h->dg;
+  p.out[1] = h->du;
+  p.out[2] = h->hid;
+  p.M[0] = T;
+  p.N[0] = F;
+  p.tiles_n[0] = ceil_div(F, 256);
+  p.tile_end[0] = ceil_div(T, 256) * p.tiles_n[0];
+  p.nkb = p.nkb0 = ceil_div(d, 64);
+  if (!map_k(&p.a[0], dy, d, T, lddy)) return LMOE_ERR_CUDA;
+  FFN_TRY(launch_ffn_pair(kFfnDHid, p, h->ctas, stream));
+  h->launches = 1;
+  if (dx) {   // dx = [dg | du] [gate ; up]
+    p.b[0] = h->gate_n;
+    p.b[1] = h->up_n;
+    p.out[0] = dx;
+    p.N[0] = d;
+    p.tiles_n[0] = ceil_div(d, 256);
+    p.tile_end[0] = ceil_div(T, 256) * p.tiles_n[0];
+    p.nkb0 = ceil_div(F, 64);
+    p.nkb = 2 * p.nkb0;
+    if (!map_k(&p.a[0], h->dg, F, T, F) || !map_k(&p.a[1], h->du, F, T, F)) return LMOE_ERR_CUDA;
+    FFN_TRY(launch_ffn_pair(kFfnDx, p, h->ctas, stream));
+    ++h->launches;
+  }
+  if (dwg || dwu || dwd) {
+    p.nprod = 0;
+    int tiles = 0;
+    auto add = [&](const void* a, long long lda, int M, const void* b, long long ldb, int N, void* out) {
+      const int i = p.nprod++;
+      p.out[i] = out;
+      p.M[i] = M;
+      p.N[i] = N;
+      p.tiles_n[i] = ceil_div(N, 256);
+      tiles += ceil_div(M, 256) * p.tiles_n[i];
+      p.tile_end[i] = tiles;
+      return map_n(&p.a[i], a, M, T, lda) && map_n(&p.b[i], b, N, T, ldb);
+    };
+    bool ok = true;
+    if (dwg) ok = ok && add(h->dg, F, F, x, ldx, d, dwg);
+    if (dwu) ok = ok && add(h->du, F, F, x, ldx, d, dwu);
+    if (dwd) ok = ok && add(dy, lddy, d, h->hid, F, F, dwd);
+    if (!ok) return LMOE_ERR_CUDA;
+    p.nkb = p.nkb0 = ceil_div(T, 64);
+    FFN_TRY(launch_ffn_pair(kFfnDw, p, h->ctas, stream));
+    ++h->launches;
+  }
+  return LMOE_OK;
+}
+
+lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t*, const uint8_t*, int T, void*, cudaStream_t) {
+  if (!h || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
+  return LMOE_ERR_UNSUPPORTED;
+}
+
+lmoe_status lmoe_ffn_sync_status(lmoe_ffn_handle h, cudaStream_t stream) {
+  if (!h) return LMOE_ERR_INVALID_ARG;
+  FFN_TRY(cudaStreamSynchronize(stream));
+  int flag = 0;
+  FFN_TRY(cudaMemcpy(&flag, h->err, sizeof(flag), cudaMemcpyDeviceToHost));
+  if (flag == 0) return LMOE_OK;
+  FFN_TRY(cudaMemset(h->err, 0, sizeof(flag)));
+  return LMOE_ERR_TIMEOUT;
+}
+
+int lmoe_ffn_last_launch_count(lmoe_ffn_handle h) { return h ? h->launches : 0; }
+
+}  // extern "C"

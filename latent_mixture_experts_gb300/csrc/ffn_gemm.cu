@@ -1,0 +1,324 @@
+// The products of the dense feed-forward block on large batches: bf16, fp32
+// accumulation in tensor memory, one 256 x 256 output tile per pair of CTAs.
+//
+// A pair shares one tcgen05.mma (cta_group::2, M = 256, N = 256): each CTA
+// stages 128 rows of A and 128 of B, so a 64-wide K block costs 32 KB of
+// shared memory per CTA for 256 x 256 x 64 products - two thirds of the
+// bytes per product of a single CTA's 128 x 256 tile, which the
+// shared-memory fill would bound.  The ring holds six such blocks; two
+// 256-column accumulators fill tensor memory, so the epilogue of one tile
+// runs under the products of the next.  Grid: one CTA per SM, tiles handed
+// out statically, eight tile rows at a time so that concurrent tiles share
+// their operands in L2.
+//
+// Operands reach shared memory by TMA in the order they have in memory: rows
+// along K ("K contiguous") or, for the backward products, along M or N,
+// which the MMA descriptors express, so nothing is transposed or copied.
+//
+// Warps: 0 = TMA, 1 = MMA (even CTA), 2..5 = epilogue (TMEM lane quarter
+// warp % 4).
+#include "ffn_act.cuh"
+#include "ffn_internal.h"
+#include "lmoe_internal.h"
+#include "pair.cuh"
+
+namespace lmoe {
+namespace {
+
+constexpr int kStages = 6;
+constexpr int kOperand = 16384;              // 128 rows x 64 bf16
+constexpr int kStage = 2 * kOperand;
+constexpr int kPairSmem = kStages * kStage + 1024;
+constexpr int kPairThreads = 192;
+constexpr int kTileRows = 8;                 // tile rows of one raster group
+
+struct Tile {
+  int prod, m, n;
+};
+__device__ __forceinline__ Tile tile_of(const FfnPairParams& p, int i) {
+  Tile t;
+  t.prod = 0;
+  while (t.prod + 1 < p.nprod && i >= p.tile_end[t.prod]) ++t.prod;
+  const int first = t.prod ? p.tile_end[t.prod - 1] : 0;
+  const int tn = p.tiles_n[t.prod], tm = (p.tile_end[t.prod] - first) / tn;
+  i -= first;
+  const int g = i / (kTileRows * tn), r = i - g * kTileRows * tn;
+  const int rows = min(kTileRows, tm - g * kTileRows);
+  t.m = g * kTileRows + r % rows;
+  t.n = r / rows;
+  return t;
+}
+
+__device__ __forceinline__ void store16(__nv_bfloat16* dst, const uint32_t (&w)[8], int left) {
+  if (left >= 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (left >= 16) *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* src, uint32_t (&w)[8], int left) {
+  uint4 a = make_uint4(0, 0, 0, 0), b = a;
+  if (left >= 8) a = *reinterpret_cast<const uint4*>(src);
+  if (left >= 16) b = *reinterpret_cast<const uint4*>(src + 8);
+  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+}
+
+// One row (this thread's) of the tile: columns of the CTA's 256-column
+// accumulator at `acc`.  N is a multiple of 8, so a row ends on a 16-byte
+// boundary.
+template <int MODE, int ACT>
+__device__ __forceinline__ void epilogue_row(const FfnPairParams& p, const Tile& t, uint32_t acc, int row,
+                                             bool row_ok) {
+  const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
+  if constexpr (MODE == kFfnGateUp) {
+    const int n0 = t.n * 128, N = p.N[0];
+    const size_t at = static_cast<size_t>(row) * N + n0;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 16) {
+      if (n0 + c >= N) break;
+      uint32_t g[16], u[16], h[8];
+      tmem_ld16(acc + c, g);
+      tmem_ld16(acc + 128 + c, u);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        h[j] = pack_bf16(glu_hidden<ACT>(__uint_as_float(g[2 * j]), __uint_as_float(u[2 * j]), caps),
+                         glu_hidden<ACT>(__uint_as_float(g[2 * j + 1]), __uint_as_float(u[2 * j + 1]), caps));
+      if (row_ok) {
+        const int left = N - n0 - c;
+        store16(static_cast<__nv_bfloat16*>(p.out[0]) + at + c, h, left);
+        if (p.out[1]) {
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j] = pack_bf16(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
+          store16(static_cast<__nv_bfloat16*>(p.out[1]) + at + c, w, left);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j] = pack_bf16(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+          store16(static_cast<__nv_bfloat16*>(p.out[2]) + at + c, w, left);
+        }
+      }
+    }
+  } else {
+    const int n0 = t.n * 256, N = p.N[t.prod];
+    const size_t at = static_cast<size_t>(row) * N + n0;
+#pragma unroll 1
+    for (int c = 0; c < 256; c += 16) {
+      if (n0 + c >= N) break;
+      const int left = N - n0 - c;
+      uint32_t v[16];
+      if constexpr (MODE == kFfnDHid) {
+        uint32_t g[8], u[8], dg[8], du[8], h[8];
+        const int have = row_ok ? left : 0;
+        load16(static_cast<const __nv_bfloat16*>(p.in_g) + at + c, g, have);
+        load16(static_cast<const __nv_bfloat16*>(p.in_u) + at + c, u, have);
+        tmem_ld16(acc + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const GluGrad x = glu_grad<ACT>(bf16_lo(g[j]), bf16_lo(u[j]), __uint_as_float(v[2 * j]), caps);
+          const GluGrad y = glu_grad<ACT>(bf16_hi(g[j]), bf16_hi(u[j]), __uint_as_float(v[2 * j + 1]), caps);
+          dg[j] = pack_bf16(x.dg, y.dg);
+          du[j] = pack_bf16(x.du, y.du);
+          h[j] = pack_bf16(x.hid, y.hid);
+        }
+        if (row_ok) {
+          store16(static_cast<__nv_bfloat16*>(p.out[0]) + at + c, dg, left);
+          store16(static_cast<__nv_bfloat16*>(p.out[1]) + at + c, du, left);
+          store16(static_cast<__nv_bfloat16*>(p.out[2]) + at + c, h, left);
+        }
+      } else {
+        uint32_t w[8];
+        tmem_ld16(acc + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+        if (row_ok) store16(static_cast<__nv_bfloat16*>(p.out[t.prod]) + at + c, w, left);
+      }
+    }
+  }
+}
+
+template <int MODE, int ACT>
+__global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_constant__ FfnPairParams p) {
+  constexpr bool kAMn = MODE == kFfnDw;
+  constexpr bool kBMn = MODE == kFfnDHid || MODE == kFfnDx || MODE == kFfnDw;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = align1024(smem_raw);
+  __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+  __shared__ uint32_t tmem_base;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 8);      // four epilogue warps of both CTAs
+    }
+    fence_mbar_init();
+  }
+  cluster_sync();
+  if (warp == 1) {
+    tmem_alloc_pair(&tmem_base, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  griddep_launch();
+  griddep_wait();
+  const uint32_t tbase = tmem_base;
+  const int pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
+  const int total = p.tile_end[p.nprod - 1];
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int i = first; i < total && ok; i += pairs) {
+        const Tile t = tile_of(p, i);
+        const int m0 = t.m * 256 + 128 * static_cast<int>(rank);
+        for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+          const uint32_t s = it % kStages;
+          if (it >= kStages && !mbar_wait_cluster(&empty[s], ((it / kStages) - 1) & 1, p.err, kErrTimeout)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
+          const uint32_t bar = map_rank(&full[s], 0);
+          uint8_t* sa = sm + s * kStage;
+          uint8_t* sb = sa + kOperand;
+          int src = t.prod, k0 = kb * 64;
+          if (MODE == kFfnDx && kb >= p.nkb0) {
+            src = 1;
+            k0 = (kb - p.nkb0) * 64;
+          }
+          if constexpr (kAMn) {
+            tma_load_2d_pair(sa, &p.a[src], bar, m0, k0);
+            tma_load_2d_pair(sa + 8192, &p.a[src], bar, m0 + 64, k0);
+          } else {
+            tma_load_2d_pair(sa, &p.a[src], bar, k0, m0);
+          }
+          if constexpr (MODE == kFfnGateUp) {   // gate rows in the even CTA, up rows in the odd one
+            tma_load_2d_pair(sb, &p.b[rank], bar, k0, t.n * 128);
+          } else if constexpr (kBMn) {
+            const int n0 = t.n * 256 + 128 * static_cast<int>(rank);
+            tma_load_2d_pair(sb, &p.b[src], bar, n0, k0);
+            tma_load_2d_pair(sb + 8192, &p.b[src], bar, n0 + 64, k0);
+          } else {
+            tma_load_2d_pair(sb, &p.b[src], bar, k0, t.n * 256 + 128 * static_cast<int>(rank));
+          }
+        }
+      }
+      // Every stage has been read by the MMAs (and so every copy has landed)
+      // before the pair may leave; if a wait ran out, the copies in flight
+      // get a millisecond to land.
+      const uint32_t used = it < kStages ? it : kStages;
+      for (uint32_t j = it - used; j < it && ok; ++j)
+        ok = mbar_wait_cluster(&empty[j % kStages], (j / kStages) & 1, p.err, kErrTimeout);
+      if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16(256, 256) | (kAMn ? kIdescAMajorMn : 0u) | (kBMn ? kIdescBMajorMn : 0u);
+      uint32_t it = 0, n = 0;
+      bool ok = true;
+      for (int i = first; i < total && ok; i += pairs, ++n) {
+        const uint32_t b = n & 1, use = n >> 1;
+        if (use > 0 && !mbar_wait_cluster(&acc_empty[b], (use - 1) & 1, p.err, kErrTimeout)) break;
+        tc_fence_after();
+        const uint32_t d = tbase + b * 256;
+        for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+          const uint32_t s = it % kStages;
+          if (!mbar_wait_cluster(&full[s], (it / kStages) & 1, p.err, kErrTimeout)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(sm + s * kStage), sb = sa + kOperand;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t ad = kAMn ? sdesc_sw128_mn(sa + 2048 * k, 8192) : sdesc_sw128(sa + 32 * k);
+            const uint64_t bd = kBMn ? sdesc_sw128_mn(sb + 2048 * k, 8192) : sdesc_sw128(sb + 32 * k);
+            mma_bf16_pair(d, ad, bd, idesc, (kb | k) != 0);
+          }
+          mma_commit_pair(&empty[s]);
+        }
+        if (ok) mma_commit_pair(&acc_full[b]);
+      }
+    }
+  } else {
+    const int q = warp & 3;
+    const uint32_t remote_empty[2] = {map_rank(&acc_empty[0], 0), map_rank(&acc_empty[1], 0)};
+    uint32_t n = 0;
+    for (int i = first; i < total; i += pairs, ++n) {
+      const uint32_t b = n & 1;
+      if (!mbar_wait_cluster(&acc_full[b], (n >> 1) & 1, p.err, kErrTimeout)) break;
+      tc_fence_after();
+      const Tile t = tile_of(p, i);
+      const int row0 = t.m * 256 + 128 * static_cast<int>(rank) + 32 * q;
+      if (row0 < p.M[t.prod])
+        epilogue_row<MODE, ACT>(p, t, tbase + b * 256 + (static_cast<uint32_t>(32 * q) << 16), row0 + lane,
+                                row0 + lane < p.M[t.prod]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(b ? remote_empty[1] : remote_empty[0]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) tmem_dealloc_pair(tbase, 512);
+  cluster_sync();      // neither CTA leaves while the other still frees the pair's columns
+}
+
+template <int MODE, int ACT>
+cudaError_t launch(const FfnPairParams& p, int ctas, cudaStream_t s) {
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      ffn_pair_kernel<MODE, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  if (attr != cudaSuccess) return attr;
+  const int tiles = p.tile_end[p.nprod - 1];
+  return launch_pdl_cluster(ffn_pair_kernel<MODE, ACT>, dim3(2 * tiles < ctas ? 2 * tiles : ctas), dim3(kPairThreads),
+                            kPairSmem, 2, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_ffn_pair(FfnMode mode, const FfnPairParams& p, int ctas, cudaStream_t s) {
+  const bool sw = p.act == 1;
+  switch (mode) {
+    case kFfnGateUp: return sw ? launch<kFfnGateUp, 1>(p, ctas, s) : launch<kFfnGateUp, 0>(p, ctas, s);
+    case kFfnPlain: return launch<kFfnPlain, 0>(p, ctas, s);
+    case kFfnDHid: return sw ? launch<kFfnDHid, 1>(p, ctas, s) : launch<kFfnDHid, 0>(p, ctas, s);
+    case kFfnDx: return launch<kFfnDx, 0>(p, ctas, s);
+    case kFfnDw: return launch<kFfnDw, 0>(p, ctas, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t ffn_pair_ctas(int* ctas) {
+  cudaError_t e = cudaFuncSetAttribute(ffn_pair_kernel<kFfnPlain, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kPairSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, ffn_pair_kernel<kFfnPlain, 0>, &cfg);
+  if (e != cudaSuccess) return e;
+  *ctas = 2 * (n > 0 ? n : 1);
+  return cudaSuccess;
+}
+
+}  // namespace lmoe

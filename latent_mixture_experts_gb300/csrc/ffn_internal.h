@@ -1,0 +1,46 @@
+// Interfaces between the feed-forward block's C ABI and its kernels, and of
+// the norm kernels.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace lmoe {
+
+// ---------------------------------------------------------------- RMS norm
+constexpr int kNormMaxWidth = 16384;
+// Floats of `part` that launch_rms_norm_bwd needs.
+size_t rms_norm_bwd_partials(int T, int d);
+// r null: h = x is not written.  scale set: y is E4M3 codes with E8M0 scales.
+cudaError_t launch_add_rms_norm(const void* x, long long ldx, const void* r, long long ldr, bool r_fp32, int T, int d,
+                                const void* w, float eps, void* h, void* y, uint8_t* scale, cudaStream_t s);
+cudaError_t launch_rms_norm_bwd(const void* dy, long long lddy, const void* h, long long ldh, const void* dh,
+                                long long lddh, bool h_fp32, int T, int d, const void* w, float eps, void* dx,
+                                float* part, float* dw, cudaStream_t s);
+
+// ------------------------------------------------------ pair-tile bf16 GEMM
+// C[M][N] (bf16) = A B^T on 256 x 256 tiles of CTA pairs.
+enum FfnMode {
+  kFfnGateUp = 0,   // A = x, B = gate | up rows of 128 features; out0 = act(g, u), out1/out2 = g, u when set
+  kFfnPlain = 1,    // A, B stored K contiguous; out0
+  kFfnDHid = 2,     // B stored N contiguous; out0 = dg, out1 = du, out2 = hid from in_g, in_u
+  kFfnDx = 3,       // B stored N contiguous, K concatenated over two (A, B); out0
+  kFfnDw = 4        // A and B stored M / N contiguous; up to three products out[i] = A[i]^T B[i]
+};
+struct FfnPairParams {
+  CUtensorMap a[3], b[3];
+  void* out[3];
+  const void *in_g, *in_u;
+  int M[3], N[3];             // output rows and columns of each product
+  int tiles_n[3], tile_end[3], nprod;
+  int nkb, nkb0;              // 64-wide K blocks in all; of the first (A, B) of a concatenation
+  float b1, b2;
+  int act;
+  int* err;
+};
+cudaError_t launch_ffn_pair(FfnMode mode, const FfnPairParams& p, int ctas, cudaStream_t s);
+// Largest number of CTAs (an even number) of the pair kernels that run at once.
+cudaError_t ffn_pair_ctas(int* ctas);
+
+}  // namespace lmoe
