@@ -224,6 +224,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       constexpr uint32_t idesc = idesc_bf16(256, 256) | (kAMn ? kIdescAMajorMn : 0u) | (kBMn ? kIdescBMajorMn : 0u);
+      const uint32_t base = smem_u32(sm);
+      const uint64_t a_desc = kAMn ? sdesc_sw128_mn(base, 8192) : sdesc_sw128(base);
+      const uint64_t b_desc = kBMn ? sdesc_sw128_mn(base + kOperand, 8192) : sdesc_sw128(base + kOperand);
       uint32_t it = 0, n = 0;
       bool ok = true;
       for (int i = first; i < total && ok; i += pairs, ++n) {
@@ -238,13 +241,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(sm + s * kStage), sb = sa + kOperand;
+          // descriptors count 16-byte units: a step of 16 along K is 32 bytes of
+          // a K-contiguous row, or 16 rows of 128 bytes
+          const uint64_t ad = a_desc + s * (kStage >> 4), bd = b_desc + s * (kStage >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t ad = kAMn ? sdesc_sw128_mn(sa + 2048 * k, 8192) : sdesc_sw128(sa + 32 * k);
-            const uint64_t bd = kBMn ? sdesc_sw128_mn(sb + 2048 * k, 8192) : sdesc_sw128(sb + 32 * k);
-            mma_bf16_pair(d, ad, bd, idesc, (kb | k) != 0);
-          }
+          for (int k = 0; k < 4; ++k)
+            mma_bf16_pair(d, ad + k * (kAMn ? 128 : 2), bd + k * (kBMn ? 128 : 2), idesc, (kb | k) != 0);
           mma_commit_pair(&empty[s]);
         }
         if (ok) mma_commit_pair(&acc_full[b]);

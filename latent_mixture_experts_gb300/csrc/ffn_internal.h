@@ -43,4 +43,33 @@ cudaError_t launch_ffn_pair(FfnMode mode, const FfnPairParams& p, int ctas, cuda
 // Largest number of CTAs (an even number) of the pair kernels that run at once.
 cudaError_t ffn_pair_ctas(int* ctas);
 
+// ------------------------------------------------------ small-batch passes
+// out[t][f] over all tokens of a batch of at most kSkinnyMaxTokens.
+constexpr int kSkinnyMaxTokens = 128;
+constexpr int kSkinnyMaxStages = 16;
+constexpr int kSkinnyMaxSplits = 8;    // K splits: the portable cluster size
+constexpr int kSkinnySmem = 110 * 1024;
+struct FfnSkinnyParams {
+  // whole (K a multiple of 64): a (64, T, K/64), b (64, features, K/64) or, gate/up, (64, features, 2, K/64),
+  // boxes of tb / rows and kc chunks; else a (K, T), b (K, features[, 2]), one box per 64-wide chunk
+  // apart: gate and up too far apart for one map (2^40 bytes): b, b_up (K, features), one box per chunk each
+  CUtensorMap a, b, b_up;
+  void *out, *save_g, *save_u;
+  int T, M;            // tokens; features of the output
+  int rows;            // features of a cluster
+  int tb;              // token rows loaded: T rounded up to 8
+  int chunks, kc;      // 64-wide K chunks; chunks of a stage
+  int stages;
+  int splits;          // CTAs of a cluster, over K
+  int recv, reuse_ring;   // where in shared memory the partial sums meet: behind the ring, or over it
+  int whole, apart;
+  int swapped;         // swapped: the up matrix lies below the gate matrix in memory
+  float b1, b2;
+  int* err;
+};
+// Fills rows, splits, tb, kc and stages from T, M and chunks; false where the
+// kernel does not take the shape.
+bool ffn_skinny_plan(FfnSkinnyParams& p, bool gate_up);
+cudaError_t launch_ffn_skinny(const FfnSkinnyParams& p, bool gate_up, int act, cudaStream_t s);
+
 }  // namespace lmoe

@@ -1,0 +1,285 @@
+// The feed-forward block's two forward passes on small batches (bf16), where
+// streaming the weights once from HBM bounds the time.
+//
+// Tokens are the MMA's M rows (up to 128; rows past the batch are whatever
+// shared memory holds, and only reach output rows that nobody reads), weight
+// rows its N columns.  A cluster of up to 8 CTAs owns `rows` consecutive
+// output features and splits K; its partial sums are joined through
+// distributed shared memory, in rank order, by all of its CTAs.  An MMA costs
+// about the same for 32 columns as for 100 (it reads its 128 token rows either
+// way), so wide tiles with a split K keep up with HBM where one wave of narrow
+// tiles over the whole of K does not: one token at widths 7168 and 6144 takes
+// 48.4 us against 63.0 us, at 7168 and 2048 23.7 us against 32.1 us.  The gate and up rows of
+// the same features arrive side by side, through one tensor map whose third
+// dimension steps from one matrix to the other.  A ring of about 100 KB per
+// CTA puts two CTAs on an SM, and lets the down pass's CTAs load their first
+// weights while the gate/up pass's last ones finish.
+#include "ffn_act.cuh"
+#include "ffn_internal.h"
+#include "lmoe_internal.h"
+#include "pair.cuh"
+
+namespace lmoe {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kCols = 128;       // MMA columns: weight rows of a tile
+constexpr int kMinCtas = 150;    // about one CTA per SM at least
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+__device__ __forceinline__ void st_cluster4(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// GU: gate and up rows of 64 features -> act(g, u); else 128 output features
+// of one matrix.
+template <bool GU, int ACT>
+__global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_constant__ FfnSkinnyParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = align1024(smem_raw);
+  __shared__ uint64_t full[kSkinnyMaxStages], empty[kSkinnyMaxStages], done;
+  __shared__ uint32_t tmem_base;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int N = kCols;
+  constexpr int kRows = GU ? N / 2 : N;               // features of the cluster
+  const int rank = static_cast<int>(cluster_rank());  // K split of this CTA
+  const int f0 = static_cast<int>(blockIdx.x) / p.splits * kRows;   // first feature
+  const int a_chunk = p.tb * 128, b_chunk = N * 128;  // bytes of one 64-wide K chunk
+  const int a_slot = a_chunk * p.kc, b_slot = b_chunk * p.kc;
+  uint8_t* sb = sm + p.stages * a_slot;
+  const int all = (p.chunks + p.kc - 1) / p.kc;
+  const int first = rank * all / p.splits, steps = (rank + 1) * all / p.splits - first;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_base, N);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // Every CTA of the cluster runs (and, where the partial sums go into the
+  // ring, has finished with it) before another one writes to it.
+  if (!p.reuse_ring) cluster_arrive();
+  const uint32_t tacc = tmem_base;
+  const bool producer = warp == 0 && lane == 0;
+  // The dependents are let in only after everything before this kernel has
+  // finished: the down pass may then read its weights at once.
+  if (GU || !producer) {
+    griddep_wait();
+    griddep_launch();
+  }
+
+  if (producer) {
+    auto load_b = [&](int i, int s) {
+      i += first;
+      uint8_t* dst = sb + s * b_slot;
+      if (GU && p.apart) {
+        for (int c = 0; c < p.kc; ++c) {
+          tma_load_2d(dst + c * b_chunk, &p.b, &full[s], (i * p.kc + c) * 64, f0);
+          tma_load_2d(dst + c * b_chunk + (b_chunk >> 1), &p.b_up, &full[s], (i * p.kc + c) * 64, f0);
+        }
+      } else if (p.whole) {
+        if constexpr (GU)
+          tma_load_4d(dst, &p.b, &full[s], 0, f0, 0, i * p.kc);
+        else
+          tma_load_3d(dst, &p.b, &full[s], 0, f0, i * p.kc);
+      } else {
+        for (int c = 0; c < p.kc; ++c) {
+          if constexpr (GU)
+            tma_load_3d(dst + c * b_chunk, &p.b, &full[s], (i * p.kc + c) * 64, f0, 0);
+          else
+            tma_load_2d(dst + c * b_chunk, &p.b, &full[s], (i * p.kc + c) * 64, f0);
+        }
+      }
+    };
+    auto load_a = [&](int i, int s) {
+      i += first;
+      uint8_t* dst = sm + s * a_slot;
+      if (p.whole) {
+        tma_load_3d(dst, &p.a, &full[s], 0, 0, i * p.kc);
+      } else {
+        for (int c = 0; c < p.kc; ++c) tma_load_2d(dst + c * a_chunk, &p.a, &full[s], (i * p.kc + c) * 64, 0);
+      }
+    };
+    const int pre = steps < p.stages ? steps : p.stages;
+    for (int i = 0; i < pre; ++i) {
+      mbar_arrive_expect_tx(&full[i], a_slot + b_slot);
+      load_b(i, i);
+      if (GU) load_a(i, i);
+    }
+    if (!GU) {                     // the tokens come from the kernel before
+      griddep_wait();
+      griddep_launch();
+      for (int i = 0; i < pre; ++i) load_a(i, i);
+    }
+    int s = pre == p.stages ? 0 : pre;
+    uint32_t phase = 0;
+    for (int i = pre; i < steps; ++i) {
+      if (!mbar_wait(&empty[s], phase, p.err, kErrTimeout)) break;
+      mbar_arrive_expect_tx(&full[s], a_slot + b_slot);
+      load_b(i, s);
+      load_a(i, s);
+      if (++s == p.stages) s = 0, phase ^= 1;
+    }
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_bf16(128, N);
+    const uint64_t a_desc = sdesc_sw128(smem_u32(sm)), b_desc = sdesc_sw128(smem_u32(sb));
+    int s = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int i = 0; i < steps; ++i) {
+      if (!(ok = mbar_wait(&full[s], phase, p.err, kErrTimeout))) break;
+      tc_fence_after();
+      // descriptors count 16-byte units: one addition each per MMA, as this
+      // single thread's instructions would otherwise take longer than the MMAs
+      uint64_t ad = a_desc + static_cast<uint32_t>(s * a_slot >> 4), bd = b_desc + static_cast<uint32_t>(s * b_slot >> 4);
+      for (int c = 0; c < p.kc; ++c) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_bf16(tacc, ad + 2 * k, bd + 2 * k, idesc, (i | c | k) != 0);
+        ad += a_chunk >> 4;
+        bd += b_chunk >> 4;
+      }
+      mma_commit(&empty[s]);
+      if (++s == p.stages) s = 0, phase ^= 1;
+    }
+    mma_commit(&done);
+  }
+  __syncwarp();
+
+  // Each CTA of the cluster finishes fs = rows / splits of the features: the
+  // partial sums (lane = token) go straight into its shared memory, one block
+  // [token][fs columns, GU: gate then up] per source rank, and are added in
+  // rank order by all of its threads, features along threads.
+  const bool ok = mbar_wait(&done, 0, p.err, kErrTimeout);
+  tc_fence_after();
+  __syncwarp();
+  if (p.reuse_ring) cluster_arrive();
+  cluster_wait();
+  const int fs = kRows / p.splits, pitch = N / p.splits + 4;   // 16-byte rows, four banks apart
+  float* recv = reinterpret_cast<float*>(sm + p.recv);
+  const int row = 32 * warp;
+  if (row < p.T) {                  // warp-uniform
+    const uint32_t at = 4 * ((rank * p.T + row + lane) * pitch);
+#pragma unroll 1
+    for (int o = 0; o < p.splits; ++o) {
+      const uint32_t dst = map_rank(recv, o) + at;
+      for (int c = 0; c < fs; c += 8) {
+        uint32_t v[8], w[8];
+        tmem_ld8(tmem_addr(tacc, 32 * warp, o * fs + c), v);
+        if constexpr (GU) tmem_ld8(tmem_addr(tacc, 32 * warp, kRows + o * fs + c), w);
+        tmem_ld_wait();
+        if (row + lane < p.T) {
+          st_cluster4(dst + 4 * c, v);
+          st_cluster4(dst + 4 * c + 16, v + 4);
+          if constexpr (GU) {
+            st_cluster4(dst + 4 * (fs + c), w);
+            st_cluster4(dst + 4 * (fs + c) + 16, w + 4);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tacc, N);
+  cluster_arrive();
+  cluster_wait();
+  const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
+  const int shift = 30 - __clz(fs);   // log2 of the pairs of features (fs is a power of two)
+  const int f1 = f0 + rank * fs, left = p.M - f1;
+  for (int e = threadIdx.x; e < p.T << shift; e += kThreads) {
+    const int t = e >> shift, f = 2 * (e - (t << shift));
+    if (f >= left) continue;
+    float2 v = make_float2(0.f, 0.f), w = v;
+    for (int r = 0; r < p.splits; ++r) {
+      const float* src = recv + (r * p.T + t) * pitch + f;
+      const float2 a = *reinterpret_cast<const float2*>(src);
+      v.x += a.x, v.y += a.y;
+      if constexpr (GU) {
+        const float2 b = *reinterpret_cast<const float2*>(src + fs);
+        w.x += b.x, w.y += b.y;
+      }
+    }
+    if (!ok) v = w = make_float2(0.f, 0.f);
+    const size_t at = static_cast<size_t>(t) * p.M + f1 + f;
+    if constexpr (GU) {
+      const float2 g = p.swapped ? w : v, u = p.swapped ? v : w;
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+          pack_bf16(glu_hidden<ACT>(g.x, u.x, caps), glu_hidden<ACT>(g.y, u.y, caps));
+      if (p.save_g) {
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.save_g) + at) = pack_bf16(g.x, g.y);
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.save_u) + at) = pack_bf16(u.x, u.y);
+      }
+    } else {
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at) = pack_bf16(v.x, v.y);
+    }
+  }
+}
+
+template <bool GU, int ACT>
+cudaError_t launch(const FfnSkinnyParams& p, cudaStream_t s) {
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(ffn_skinny_kernel<GU, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSkinnySmem);
+  if (attr != cudaSuccess) return attr;
+  return launch_pdl_cluster(ffn_skinny_kernel<GU, ACT>, dim3((p.M + p.rows - 1) / p.rows * p.splits), dim3(kThreads),
+                            kSkinnySmem, p.splits, s, p);
+}
+
+}  // namespace
+
+bool ffn_skinny_plan(FfnSkinnyParams& p, bool gate_up) {
+  if (p.T > kSkinnyMaxTokens) return false;
+  constexpr int N = kCols;
+  p.rows = gate_up ? N / 2 : N;
+  const int tiles = (p.M + p.rows - 1) / p.rows;
+  p.tb = (p.T + 7) / 8 * 8;
+  const int chunk = (p.tb + N) * 128;
+  // K chunks per stage: up to about 24 KB a stage
+  p.kc = chunk <= 6 * 1024 ? 4 : chunk <= 12 * 1024 ? 2 : 1;
+  const int all = (p.chunks + p.kc - 1) / p.kc;
+  p.splits = 1;
+  while (p.splits < kSkinnyMaxSplits && tiles * p.splits < kMinCtas && 2 * p.splits <= all)
+    p.splits *= 2;
+  const int budget = kSkinnySmem - 1024;
+  const int recv = 4 * p.T * (N + 4 * p.splits);
+  p.reuse_ring = recv > budget / 3;
+  const int ring = p.reuse_ring ? budget : (budget - recv) / 1024 * 1024;
+  p.recv = p.reuse_ring ? 0 : ring;
+  p.stages = ring / (chunk * p.kc);
+  if (p.stages > kSkinnyMaxStages) p.stages = kSkinnyMaxStages;
+  // the joined sums, and the MMA's reads of up to 128 rows from the last chunk, stay inside
+  const int a_end = p.stages * p.kc * p.tb * 128 + (128 - p.tb) * 128;
+  return p.stages >= 2 && recv <= budget && a_end <= budget;
+}
+
+cudaError_t launch_ffn_skinny(const FfnSkinnyParams& p, bool gate_up, int act, cudaStream_t s) {
+  if (!gate_up) return launch<false, 0>(p, s);
+  return act == 1 ? launch<true, 1>(p, s) : launch<true, 0>(p, s);
+}
+
+}  // namespace lmoe

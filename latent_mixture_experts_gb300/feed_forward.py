@@ -8,8 +8,8 @@ contiguous, rows may be strided.  Outputs are allocated on the stream the
 call runs on."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -17,6 +17,7 @@ from . import binding as B
 
 _OUT_FORMATS = {"bf16": 0, "mxfp8": 1}
 _STREAM_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+_BF16, _U8, _F32 = torch.bfloat16, torch.uint8, torch.float32
 
 
 def _rows(name: str, t: torch.Tensor, dtypes, shape) -> int:
@@ -25,12 +26,12 @@ def _rows(name: str, t: torch.Tensor, dtypes, shape) -> int:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-    if t.shape[0] <= 1:
+    if t.is_contiguous() or t.shape[0] <= 1 and t.stride(1) == 1:
         return t.shape[1]
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
     return t.stride(0)
 
 
@@ -39,84 +40,114 @@ def _packed(name: str, t: torch.Tensor, dtype, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _same_device(ref: torch.Tensor, **others):
-    if ref.device.index != torch.cuda.current_device():
+def _on_device(dev: int, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, not on CUDA device {dev}")
+
+
+def _on_stream(f):
+    """With stream=..., run the call and its allocations on that stream; otherwise on the current one."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
+# The current stream's handle without building a Stream object: a call on one token takes a few microseconds.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _device_of(t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
         raise ValueError("tensors must be on the current CUDA device")
-    for name, t in others.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, not {ref.device}")
-
-
-def _on(stream):
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return dev
 
 
 def _norm_weight(w: torch.Tensor, d: int):
-    if not w.is_cuda or w.dtype != torch.bfloat16 or tuple(w.shape) != (d,) or not w.is_contiguous():
+    if w.dtype is not _BF16 or w.shape != (d,) or not w.is_contiguous():
         raise ValueError(f"norm_w must be a contiguous CUDA bfloat16 tensor of shape ({d},)")
 
 
+@_on_stream
 def lmoe_add_rms_norm(x: torch.Tensor, norm_w: torch.Tensor, eps: float, residual: torch.Tensor | None = None,
-                      out_format: str = "bf16", h_out: torch.Tensor | None = None, stream=None):
+                      out_format: str = "bf16", h_out: torch.Tensor | None = None):
     """h = residual + x (in residual's dtype, bf16 or fp32; h = x without a
     residual), y = norm_w * h / sqrt(mean(h^2) + eps).
 
     Returns (y, scales, h): y bf16 [T][d] and scales None, or with
     out_format="mxfp8" E4M3 codes uint8 [T][d] and E8M0 scales uint8
-    [T][d/32]; h None without a residual.  h_out may be the residual itself."""
+    [T][d/32]; h None without a residual.  h_out may be the residual itself.
+    stream=...: the stream to run on."""
     if out_format not in _OUT_FORMATS:
         raise ValueError(f"out_format must be one of {sorted(_OUT_FORMATS)}")
     if x.dim() != 2:
         raise ValueError("x must be [T][d]")
-    T, d = x.shape
-    ldx = _rows("x", x, (torch.bfloat16,), (T, d))
+    shape = x.shape
+    T, d = shape
+    ldx = _rows("x", x, (_BF16,), shape)
+    dev = _device_of(x)
     _norm_weight(norm_w, d)
-    ldr, st, h = d, 0, None
-    _same_device(x, norm_w=norm_w, residual=residual, h_out=h_out)
+    _on_device(dev, norm_w=norm_w)
+    mx = out_format == "mxfp8"
+    y = torch.empty(shape, dtype=_U8 if mx else _BF16, device=x.device)
+    s = torch.empty(T, d // 32, dtype=_U8, device=x.device) if mx else None
+    rp = hp = h = None
+    ldr, st = d, 0
     if residual is not None:
-        ldr = _rows("residual", residual, tuple(_STREAM_TYPES), (T, d))
+        ldr = _rows("residual", residual, (_BF16, _F32), shape)
         st = _STREAM_TYPES[residual.dtype]
-        if h_out is not None:
-            _packed("h_out", h_out, residual.dtype, (T, d))
+        _on_device(dev, residual=residual, h_out=h_out)
+        if h_out is None:
+            h = torch.empty(shape, dtype=residual.dtype, device=x.device)
+        else:
+            h = h_out
+            _packed("h_out", h, residual.dtype, shape)
+        rp, hp = residual.data_ptr(), h.data_ptr()
     elif h_out is not None:
         raise ValueError("h_out needs a residual")
-    mx = out_format == "mxfp8"
-    with _on(stream):
-        y = torch.empty(T, d, dtype=torch.uint8 if mx else torch.bfloat16, device=x.device)
-        s = torch.empty(T, d // 32, dtype=torch.uint8, device=x.device) if mx else None
-        if residual is not None:
-            h = h_out if h_out is not None else torch.empty(T, d, dtype=residual.dtype, device=x.device)
-    B._check("lmoe_add_rms_norm", B.load_library().lmoe_add_rms_norm(
-        B._ptr(x), ldx, B._ptr(residual), ldr, st, T, d, B._ptr(norm_w), float(eps), B._ptr(h), B._ptr(y),
-        _OUT_FORMATS[out_format], B._ptr(s), B._stream(stream)))
+    status = B.load_library().lmoe_add_rms_norm(
+        x.data_ptr(), ldx, rp, ldr, st, T, d, norm_w.data_ptr(), eps, hp, y.data_ptr(), _OUT_FORMATS[out_format],
+        s.data_ptr() if mx else None, _raw_stream(dev))
+    if status:
+        raise B.LmoeError("lmoe_add_rms_norm", status)
     return y, s, h
 
 
+@_on_stream
 def lmoe_add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, norm_w: torch.Tensor, eps: float,
-                               dh: torch.Tensor | None = None, stream=None):
+                               dh: torch.Tensor | None = None):
     """Gradients of lmoe_add_rms_norm from dy bf16 [T][d] and its h (bf16 or
     fp32); dh (h's dtype): the gradient along the residual stream.  Returns
     (dx in h's dtype, the gradient of x and of the residual alike; d norm_w
-    fp32 [d])."""
+    fp32 [d]).  stream=...: the stream to run on."""
     if h.dim() != 2:
         raise ValueError("h must be [T][d]")
-    T, d = h.shape
-    ldh = _rows("h", h, tuple(_STREAM_TYPES), (T, d))
-    lddy = _rows("dy", dy, (torch.bfloat16,), (T, d))
-    lddh = d if dh is None else _rows("dh", dh, (h.dtype,), (T, d))
+    shape = h.shape
+    T, d = shape
+    ldh = _rows("h", h, (_BF16, _F32), shape)
+    lddy = _rows("dy", dy, (_BF16,), shape)
+    lddh = d if dh is None else _rows("dh", dh, (h.dtype,), shape)
+    dev = _device_of(h)
     _norm_weight(norm_w, d)
-    _same_device(h, dy=dy, norm_w=norm_w, dh=dh)
+    _on_device(dev, dy=dy, norm_w=norm_w, dh=dh)
     lib = B.load_library()
     n = ctypes.c_size_t()
     B._check("lmoe_add_rms_norm_backward_workspace",
              lib.lmoe_add_rms_norm_backward_workspace(T, d, ctypes.byref(n)))
-    with _on(stream):
-        dx = torch.empty(T, d, dtype=h.dtype, device=h.device)
-        dw = torch.empty(d, dtype=torch.float32, device=h.device)
-        ws = torch.empty(n.value, dtype=torch.uint8, device=h.device)
-    B._check("lmoe_add_rms_norm_backward", lib.lmoe_add_rms_norm_backward(
-        B._ptr(dy), lddy, B._ptr(h), ldh, B._ptr(dh), lddh, _STREAM_TYPES[h.dtype], T, d, B._ptr(norm_w), float(eps),
-        B._ptr(dx), B._ptr(dw), B._ptr(ws), n.value, B._stream(stream)))
+    dx = torch.empty(shape, dtype=h.dtype, device=h.device)
+    dw = torch.empty(d, dtype=_F32, device=h.device)
+    ws = torch.empty(n.value, dtype=_U8, device=h.device)
+    status = lib.lmoe_add_rms_norm_backward(
+        dy.data_ptr(), lddy, h.data_ptr(), ldh, None if dh is None else dh.data_ptr(), lddh, _STREAM_TYPES[h.dtype],
+        T, d, norm_w.data_ptr(), eps, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), n.value, _raw_stream(dev))
+    if status:
+        raise B.LmoeError("lmoe_add_rms_norm_backward", status)
     return dx, dw
 
 
@@ -151,7 +182,7 @@ class GatedFFN:
         for n, shape in shapes.items():
             t = weights[n]
             _packed(n, t, gate.dtype, shape)
-            _same_device(t)
+            _on_device(_device_of(gate), **{n: t})
             self._weights[n] = t
         self.d_model, self.d_ff, self.max_tokens, self.act = d, F, int(max_tokens), act
         self.training = bool(training)
@@ -159,74 +190,75 @@ class GatedFFN:
                             situ_beta=situ_beta, situ_linear_beta=situ_linear_beta, wfmt=int(self.mx),
                             max_tokens=int(max_tokens), training=int(self.training))
         w = B.LmoeFfnWeights(**{n: t.data_ptr() for n, t in self._weights.items()})
-        self._device = gate.device
+        self._device, self._dev = gate.device, gate.get_device()
         h = ctypes.c_void_p()
         B._check("lmoe_ffn_create", lib.lmoe_ffn_create(ctypes.byref(c), ctypes.byref(w), B._stream(stream),
                                                         ctypes.byref(h)))
         self._h, self._lib = h, lib
 
-    def _tokens(self, t: torch.Tensor, name: str, dtype=torch.bfloat16):
-        ld = _rows(name, t, (dtype,), (t.shape[0], self.d_model))
-        if t.device != self._device:
+    def _tokens(self, t: torch.Tensor, name: str, T: int) -> int:
+        ld = _rows(name, t, (_BF16,), (T, self.d_model))
+        if t.get_device() != self._dev:
             raise ValueError(f"{name} is on {t.device}, the block on {self._device}")
         return ld
 
-    def lmoe_ffn_forward(self, x: torch.Tensor, save: bool = False, out: torch.Tensor | None = None, stream=None):
+    def _out(self, T: int, out):
+        if out is None:
+            return torch.empty(T, self.d_model, dtype=_BF16, device=self._device)
+        _packed("out", out, _BF16, (T, self.d_model))
+        _on_device(self._dev, out=out)
+        return out
+
+    @_on_stream
+    def lmoe_ffn_forward(self, x: torch.Tensor, save: bool = False, out: torch.Tensor | None = None):
         """x bf16 [T][d_model] -> y bf16; with save=True (y, g, u): the
         pre-activations bf16 [T][d_ff] that lmoe_ffn_backward takes."""
-        ldx, T = self._tokens(x, "x"), x.shape[0]
-        g = u = None
-        with _on(stream):
-            if out is None:
-                out = torch.empty(T, self.d_model, dtype=torch.bfloat16, device=x.device)
-            else:
-                _packed("out", out, torch.bfloat16, (T, self.d_model))
-            if save:
-                g = torch.empty(T, self.d_ff, dtype=torch.bfloat16, device=x.device)
-                u = torch.empty_like(g)
-        B._check("lmoe_ffn_forward", self._lib.lmoe_ffn_forward(
-            self._h, B._ptr(x), ldx, T, B._ptr(out), B._ptr(g), B._ptr(u), B._stream(stream)))
+        T = x.shape[0]
+        ldx = self._tokens(x, "x", T)
+        out = self._out(T, out)
+        g = u = gp = up = None
+        if save:
+            g = torch.empty(T, self.d_ff, dtype=_BF16, device=self._device)
+            u = torch.empty(T, self.d_ff, dtype=_BF16, device=self._device)
+            gp, up = g.data_ptr(), u.data_ptr()
+        status = self._lib.lmoe_ffn_forward(self._h, x.data_ptr(), ldx, T, out.data_ptr(), gp, up,
+                                            _raw_stream(self._dev))
+        if status:
+            raise B.LmoeError("lmoe_ffn_forward", status)
         return (out, g, u) if save else out
 
+    @_on_stream
     def lmoe_ffn_backward(self, x: torch.Tensor, g: torch.Tensor, u: torch.Tensor, dy: torch.Tensor,
-                          need_dx: bool = True, need_dw: bool = True, stream=None):
+                          need_dx: bool = True, need_dw: bool = True):
         """-> (dx, dw_gate, dw_up, dw_down), bf16; None for those not asked for."""
-        ldx, T = self._tokens(x, "x"), x.shape[0]
-        lddy = self._tokens(dy, "dy")
-        if dy.shape[0] != T:
-            raise ValueError("x and dy must have the same number of rows")
-        _packed("g", g, torch.bfloat16, (T, self.d_ff))
-        _packed("u", u, torch.bfloat16, (T, self.d_ff))
-        _same_device(x, g=g, u=u, dy=dy)
-        dx = dwg = dwu = dwd = None
-        with _on(stream):
-            if need_dx:
-                dx = torch.empty(T, self.d_model, dtype=torch.bfloat16, device=x.device)
-            if need_dw:
-                dwg = torch.empty(self.d_ff, self.d_model, dtype=torch.bfloat16, device=x.device)
-                dwu = torch.empty_like(dwg)
-                dwd = torch.empty(self.d_model, self.d_ff, dtype=torch.bfloat16, device=x.device)
-        B._check("lmoe_ffn_backward", self._lib.lmoe_ffn_backward(
-            self._h, B._ptr(x), ldx, B._ptr(g), B._ptr(u), B._ptr(dy), lddy, T, B._ptr(dx), B._ptr(dwg), B._ptr(dwu),
-            B._ptr(dwd), B._stream(stream)))
-        return dx, dwg, dwu, dwd
+        T, d, F = x.shape[0], self.d_model, self.d_ff
+        ldx = self._tokens(x, "x", T)
+        lddy = self._tokens(dy, "dy", T)
+        _packed("g", g, _BF16, (T, F))
+        _packed("u", u, _BF16, (T, F))
+        _on_device(self._dev, g=g, u=u)
+        grads = [torch.empty(s, dtype=_BF16, device=self._device) if need else None
+                 for s, need in (((T, d), need_dx), ((F, d), need_dw), ((F, d), need_dw), ((d, F), need_dw))]
+        status = self._lib.lmoe_ffn_backward(
+            self._h, x.data_ptr(), ldx, g.data_ptr(), u.data_ptr(), dy.data_ptr(), lddy, T,
+            *(None if t is None else t.data_ptr() for t in grads), _raw_stream(self._dev))
+        if status:
+            raise B.LmoeError("lmoe_ffn_backward", status)
+        return tuple(grads)
 
-    def lmoe_ffn_forward_mx(self, x_codes: torch.Tensor, x_scales: torch.Tensor, out: torch.Tensor | None = None,
-                            stream=None):
+    @_on_stream
+    def lmoe_ffn_forward_mx(self, x_codes: torch.Tensor, x_scales: torch.Tensor, out: torch.Tensor | None = None):
         """MXFP8 x (codes uint8 [T][d_model], scales uint8 [T][d_model/32],
         as lmoe_add_rms_norm(out_format="mxfp8") returns them) -> y bf16."""
         T = x_codes.shape[0]
-        _packed("x_codes", x_codes, torch.uint8, (T, self.d_model))
-        _packed("x_scales", x_scales, torch.uint8, (T, self.d_model // 32))
-        self._tokens(x_codes, "x_codes", torch.uint8)
-        _same_device(x_codes, x_scales=x_scales)
-        with _on(stream):
-            if out is None:
-                out = torch.empty(T, self.d_model, dtype=torch.bfloat16, device=x_codes.device)
-            else:
-                _packed("out", out, torch.bfloat16, (T, self.d_model))
-        B._check("lmoe_ffn_forward_mx", self._lib.lmoe_ffn_forward_mx(
-            self._h, B._ptr(x_codes), B._ptr(x_scales), T, B._ptr(out), B._stream(stream)))
+        _packed("x_codes", x_codes, _U8, (T, self.d_model))
+        _packed("x_scales", x_scales, _U8, (T, self.d_model // 32))
+        _on_device(self._dev, x_codes=x_codes, x_scales=x_scales)
+        out = self._out(T, out)
+        status = self._lib.lmoe_ffn_forward_mx(self._h, x_codes.data_ptr(), x_scales.data_ptr(), T, out.data_ptr(),
+                                               _raw_stream(self._dev))
+        if status:
+            raise B.LmoeError("lmoe_ffn_forward_mx", status)
         return out
 
     def lmoe_ffn_sync_status(self, stream=None):
