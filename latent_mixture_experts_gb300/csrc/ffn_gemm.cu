@@ -15,8 +15,9 @@
 // along K ("K contiguous") or, for the backward products, along M or N,
 // which the MMA descriptors express, so nothing is transposed or copied.
 //
-// Warps: 0 = TMA, 1 = MMA (even CTA), 2..5 = epilogue (TMEM lane quarter
-// warp % 4).
+// Warps: 0 = TMA, 1 = MMA (even CTA), 2..9 = epilogue (TMEM lane quarter
+// warp % 4; the first four take the left half of the columns, the others the
+// right half).
 #include "ffn_act.cuh"
 #include "ffn_internal.h"
 #include "lmoe_internal.h"
@@ -29,7 +30,8 @@ constexpr int kStages = 6;
 constexpr int kOperand = 16384;              // 128 rows x 64 bf16
 constexpr int kStage = 2 * kOperand;
 constexpr int kPairSmem = kStages * kStage + 1024;
-constexpr int kPairThreads = 192;
+constexpr int kEpiPairWarps = 8;             // two for each TMEM lane quarter
+constexpr int kPairThreads = 64 + 32 * kEpiPairWarps;
 constexpr int kTileRows = 8;                 // tile rows of one raster group
 
 struct Tile {
@@ -60,18 +62,20 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* src, uint32_t (&w)[8
   w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
 }
 
-// One row (this thread's) of the tile: columns of the CTA's 256-column
-// accumulator at `acc`.  N is a multiple of 8, so a row ends on a 16-byte
-// boundary.
-template <int MODE, int ACT>
-__device__ __forceinline__ void epilogue_row(const FfnPairParams& p, const Tile& t, uint32_t acc, int row,
-                                             bool row_ok) {
+// One row (this thread's) of half a tile's columns, from the CTA's
+// 256-column accumulator at `acc`.  N is a multiple of 8, so a row ends on a
+// 16-byte boundary.  `ready`: waits for the accumulator; what the epilogue
+// reads from memory is requested before, and then one step ahead.
+template <int MODE, int ACT, class Ready>
+__device__ __forceinline__ bool epilogue_row(const FfnPairParams& p, const Tile& t, uint32_t acc, int row,
+                                             bool row_ok, int half, Ready ready) {
   const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
   if constexpr (MODE == kFfnGateUp) {
     const int n0 = t.n * 128, N = p.N[0];
     const size_t at = static_cast<size_t>(row) * N + n0;
+    if (!ready()) return false;
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 16) {
+    for (int c = 64 * half; c < 64 * half + 64; c += 16) {
       if (n0 + c >= N) break;
       uint32_t g[16], u[16], h[8];
       tmem_ld16(acc + c, g);
@@ -96,20 +100,25 @@ __device__ __forceinline__ void epilogue_row(const FfnPairParams& p, const Tile&
       }
     }
   } else {
-    const int n0 = t.n * 256, N = p.N[t.prod];
+    const int n0 = t.n * 256, N = p.N[t.prod], c0 = 128 * half;
     const size_t at = static_cast<size_t>(row) * N + n0;
+    if constexpr (MODE == kFfnDHid) {
+      const __nv_bfloat16* gp = static_cast<const __nv_bfloat16*>(p.in_g) + at;
+      const __nv_bfloat16* up = static_cast<const __nv_bfloat16*>(p.in_u) + at;
+      uint32_t g[8], u[8], g1[8], u1[8], v[16];
+      load16(gp + c0, g, row_ok ? N - n0 - c0 : 0);
+      load16(up + c0, u, row_ok ? N - n0 - c0 : 0);
+      if (!ready()) return false;
 #pragma unroll 1
-    for (int c = 0; c < 256; c += 16) {
-      if (n0 + c >= N) break;
-      const int left = N - n0 - c;
-      uint32_t v[16];
-      if constexpr (MODE == kFfnDHid) {
-        uint32_t g[8], u[8], dg[8], du[8], h[8];
-        const int have = row_ok ? left : 0;
-        load16(static_cast<const __nv_bfloat16*>(p.in_g) + at + c, g, have);
-        load16(static_cast<const __nv_bfloat16*>(p.in_u) + at + c, u, have);
+      for (int c = c0; c < c0 + 128; c += 16) {
+        const int left = N - n0 - c;
+        if (left <= 0) break;
+        const int next = row_ok && c + 16 < c0 + 128 ? left - 16 : 0;
+        load16(gp + c + 16, g1, next);
+        load16(up + c + 16, u1, next);
         tmem_ld16(acc + c, v);
         tmem_ld_wait();
+        uint32_t dg[8], du[8], h[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const GluGrad x = glu_grad<ACT>(bf16_lo(g[j]), bf16_lo(u[j]), __uint_as_float(v[2 * j]), caps);
@@ -117,14 +126,22 @@ __device__ __forceinline__ void epilogue_row(const FfnPairParams& p, const Tile&
           dg[j] = pack_bf16(x.dg, y.dg);
           du[j] = pack_bf16(x.du, y.du);
           h[j] = pack_bf16(x.hid, y.hid);
+          g[j] = g1[j];
+          u[j] = u1[j];
         }
         if (row_ok) {
           store16(static_cast<__nv_bfloat16*>(p.out[0]) + at + c, dg, left);
           store16(static_cast<__nv_bfloat16*>(p.out[1]) + at + c, du, left);
           store16(static_cast<__nv_bfloat16*>(p.out[2]) + at + c, h, left);
         }
-      } else {
-        uint32_t w[8];
+      }
+    } else {
+      if (!ready()) return false;
+#pragma unroll 1
+      for (int c = c0; c < c0 + 128; c += 16) {
+        const int left = N - n0 - c;
+        if (left <= 0) break;
+        uint32_t v[16], w[8];
         tmem_ld16(acc + c, v);
         tmem_ld_wait();
 #pragma unroll
@@ -133,6 +150,7 @@ __device__ __forceinline__ void epilogue_row(const FfnPairParams& p, const Tile&
       }
     }
   }
+  return true;
 }
 
 template <int MODE, int ACT>
@@ -153,7 +171,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);      // four epilogue warps of both CTAs
+      mbar_init(&acc_empty[i], 2 * kEpiPairWarps);      // the epilogue warps of both CTAs
     }
     fence_mbar_init();
   }
@@ -258,13 +276,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
     uint32_t n = 0;
     for (int i = first; i < total; i += pairs, ++n) {
       const uint32_t b = n & 1;
-      if (!mbar_wait_cluster(&acc_full[b], (n >> 1) & 1, p.err, kErrTimeout)) break;
-      tc_fence_after();
+      const auto ready = [&] {
+        const bool ok = mbar_wait_cluster(&acc_full[b], (n >> 1) & 1, p.err, kErrTimeout);
+        tc_fence_after();
+        return __all_sync(0xFFFFFFFFu, ok) != 0;
+      };
       const Tile t = tile_of(p, i);
       const int row0 = t.m * 256 + 128 * static_cast<int>(rank) + 32 * q;
-      if (row0 < p.M[t.prod])
-        epilogue_row<MODE, ACT>(p, t, tbase + b * 256 + (static_cast<uint32_t>(32 * q) << 16), row0 + lane,
-                                row0 + lane < p.M[t.prod]);
+      const bool ok = row0 < p.M[t.prod]
+                          ? epilogue_row<MODE, ACT>(p, t, tbase + b * 256 + (static_cast<uint32_t>(32 * q) << 16),
+                                                    row0 + lane, row0 + lane < p.M[t.prod], (warp - 2) >> 2, ready)
+                          : ready();
+      if (!ok) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(b ? remote_empty[1] : remote_empty[0]);
