@@ -84,9 +84,10 @@ typedef struct {
 } lmoe_ffn_config;
 
 /* gate, up [d_ff][d_model], down [d_model][d_ff]: bf16, or MXFP8 codes with
- * *_s scales.  Borrowed: they stay valid while the handle lives.  Their values are
- * read anew by every call, so an optimizer may update them in place between
- * calls (in stream order). */
+ * *_s scales.  Borrowed: they stay valid while the handle lives.  bf16
+ * weights are read anew by every call, so an optimizer may update them in
+ * place between calls (in stream order); MXFP8 scales are laid out for the
+ * tensor cores once, by lmoe_ffn_create, and must not change. */
 typedef struct {
   const void* gate;
   const void* up;
@@ -100,7 +101,7 @@ typedef struct lmoe_ffn_ctx* lmoe_ffn_handle;
 
 /* Errors: INVALID_ARG (NULL, misaligned, sizes < 1, bad enum, caps not
  * positive), UNSUPPORTED (shapes above; training with MXFP8; not an sm_103
- * GPU), OOM, CUDA.  *out is NULL on error.  One handle is used by one
+ * GPU), OOM, CUDA.  Synchronises `stream`.  *out is NULL on error.  One handle is used by one
  * stream at a time. */
 LMOE_API lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* w, cudaStream_t stream,
                                      lmoe_ffn_handle* out);

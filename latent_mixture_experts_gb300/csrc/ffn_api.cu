@@ -23,6 +23,8 @@ struct lmoe_ffn_ctx {
   void *hid = nullptr, *dg = nullptr, *du = nullptr;
   CUtensorMap gate, up, down;         // K contiguous, boxes of 64 x 128 rows
   CUtensorMap gate_n, up_n, down_n;   // the same memory as N contiguous operands, boxes of 64 x 64
+  // MXFP8 blocks: hid holds codes; scale atoms of x, hid and the weights
+  uint8_t *x_sf = nullptr, *hid_sf = nullptr, *gu_sf = nullptr, *down_sf = nullptr;
   int launches = 0;
 };
 
@@ -50,6 +52,11 @@ bool map_k(CUtensorMap* m, const void* base, int K, int rows, long long ld) {
 // The transposed use of [K][N]: boxes of 64 N values x 64 K rows.
 bool map_n(CUtensorMap* m, const void* base, int N, int K, long long ld) {
   return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, N, K, 2 * ld, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// MXFP8 codes [rows][K]: boxes of 128 K values x `box` rows.
+bool map_mx(CUtensorMap* m, const void* base, int K, int rows, int box) {
+  return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, K, rows, K, 128, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Weight-streaming passes: x (or hid) and the weights of one pass.  `whole`
@@ -149,7 +156,6 @@ lmoe_status lmoe_add_rms_norm_backward(const void* dy, int64_t lddy, const void*
 
 lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* w, cudaStream_t stream,
                             lmoe_ffn_handle* out) {
-  (void)stream;
   if (!out) return LMOE_ERR_INVALID_ARG;
   *out = nullptr;
   if (!cfg || !w) return LMOE_ERR_INVALID_ARG;
@@ -164,7 +170,6 @@ lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* 
   if (!usable(w->gate) || !usable(w->up) || !usable(w->down)) return LMOE_ERR_INVALID_ARG;
   if (mx && (!usable(w->gate_s) || !usable(w->up_s) || !usable(w->down_s))) return LMOE_ERR_INVALID_ARG;
   if (d % (mx ? 32 : 8) || F % (mx ? 32 : 8) || (mx && cfg->training)) return LMOE_ERR_UNSUPPORTED;
-  if (mx) return LMOE_ERR_UNSUPPORTED;
   int dev = 0, major = 0, minor = 0;
   FFN_TRY(cudaGetDevice(&dev));
   FFN_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
@@ -174,11 +179,21 @@ lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* 
   if (!h) return LMOE_ERR_OOM;
   h->cfg = *cfg;
   h->w = *w;
-  const size_t act_bytes = (static_cast<size_t>(cfg->max_tokens) * F * 2 + 255) / 256 * 256;
-  const size_t bytes = 256 + act_bytes * (cfg->training ? 3 : 1);
+  const size_t Tm = cfg->max_tokens, T256 = (Tm + 255) / 256 * 256;
+  const auto pad = [](size_t v) { return (v + 255) / 256 * 256; };
+  const size_t act_bytes = pad(Tm * F * (mx ? 1 : 2));
+  // scale atoms: 512 bytes for 128 rows x 128 values
+  const size_t kd = ceil_div(d, 128), kf = ceil_div(F, 128);
+  const size_t x_sf = T256 / 128 * kd * 512, hid_sf = T256 / 128 * kf * 512;
+  const size_t gu_tiles = ceil_div(F, kMxTileN / 2), down_tiles = ceil_div(d, kMxTileN);
+  const size_t gu_sf = gu_tiles * kd * 1024, down_sf = down_tiles * kf * 1024;
+  const size_t bytes = 256 + act_bytes * (cfg->training ? 3 : 1) + (mx ? x_sf + hid_sf + gu_sf + down_sf : 0);
   cudaError_t e = ffn_pair_ctas(&h->ctas);
   if (e == cudaSuccess) e = cudaMalloc(&h->pool, bytes);
-  if (e == cudaSuccess) e = cudaMemset(h->pool, 0, 256);
+  // the error flag, and the bytes of the scale atoms that nothing writes
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->pool, 0, 256, stream);
+  if (e == cudaSuccess && mx)
+    e = cudaMemsetAsync(static_cast<uint8_t*>(h->pool) + 256 + act_bytes, 0, x_sf + hid_sf, stream);
   if (e != cudaSuccess) {
     lmoe_ffn_destroy(h);
     return cuda_status(e);
@@ -186,14 +201,29 @@ lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* 
   uint8_t* base = static_cast<uint8_t*>(h->pool);
   h->err = reinterpret_cast<int*>(base);
   h->hid = base + 256;
-  h->dg = base + 256 + act_bytes;
-  h->du = base + 256 + 2 * act_bytes;
-  const bool ok = map_k(&h->gate, w->gate, d, F, d) && map_k(&h->up, w->up, d, F, d) &&
-                  map_k(&h->down, w->down, F, d, F) && map_n(&h->gate_n, w->gate, d, F, d) &&
-                  map_n(&h->up_n, w->up, d, F, d) && map_n(&h->down_n, w->down, F, d, F);
-  if (!ok) {
+  bool ok;
+  if (mx) {
+    h->x_sf = base + 256 + act_bytes;
+    h->hid_sf = h->x_sf + x_sf;
+    h->gu_sf = h->hid_sf + hid_sf;
+    h->down_sf = h->gu_sf + gu_sf;
+    e = launch_mx_weight_atoms(w->gate_s, w->up_s, F, d, static_cast<int>(gu_tiles), h->gu_sf, stream);
+    if (e == cudaSuccess)
+      e = launch_mx_weight_atoms(w->down_s, nullptr, d, F, static_cast<int>(down_tiles), h->down_sf, stream);
+    ok = map_mx(&h->gate, w->gate, d, F, kMxTileN / 2) && map_mx(&h->up, w->up, d, F, kMxTileN / 2) &&
+         map_mx(&h->down, w->down, F, d, kMxTileN / 2);
+  } else {
+    h->dg = base + 256 + act_bytes;
+    h->du = base + 256 + 2 * act_bytes;
+    ok = map_k(&h->gate, w->gate, d, F, d) && map_k(&h->up, w->up, d, F, d) && map_k(&h->down, w->down, F, d, F) &&
+         map_n(&h->gate_n, w->gate, d, F, d) && map_n(&h->up_n, w->up, d, F, d) &&
+         map_n(&h->down_n, w->down, F, d, F);
+  }
+  // calls on other streams may follow: the workspace is ready when this returns
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess || !ok) {
     lmoe_ffn_destroy(h);
-    return LMOE_ERR_CUDA;
+    return e != cudaSuccess ? cuda_status(e) : LMOE_ERR_CUDA;
   }
   *out = h;
   return LMOE_OK;
@@ -350,9 +380,46 @@ lmoe_status lmoe_ffn_backward(lmoe_ffn_handle h, const void* x, int64_t ldx, con
   return LMOE_OK;
 }
 
-lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t*, const uint8_t*, int T, void*, cudaStream_t) {
+lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8_t* x_scales, int T, void* out,
+                                cudaStream_t stream) {
   if (!h || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
-  return LMOE_ERR_UNSUPPORTED;
+  if (h->cfg.wfmt != LMOE_FFN_W_MXFP8) return LMOE_ERR_UNSUPPORTED;
+  h->launches = 0;
+  if (T == 0) return LMOE_OK;
+  if (!usable(x) || !x_scales || !usable(out)) return LMOE_ERR_INVALID_ARG;
+  const int d = h->cfg.d_model, F = h->cfg.d_ff;
+  FFN_TRY(launch_mx_row_atoms(x_scales, T, d, h->x_sf, stream));
+  FfnMxParams p = {};
+  p.b1 = h->cfg.situ_beta;
+  p.b2 = h->cfg.situ_linear_beta;
+  p.act = h->cfg.act == LMOE_ACT_SWIGLU;
+  p.err = h->err;
+  p.b[0] = h->gate;
+  p.b[1] = h->up;
+  p.sfa = h->x_sf;
+  p.sfb = h->gu_sf;
+  p.out = h->hid;
+  p.out_sf = h->hid_sf;
+  p.out_nkb = ceil_div(F, 128);
+  p.M = T;
+  p.N = F;
+  p.tiles_n = ceil_div(F, kMxTileN / 2);
+  p.tiles = ceil_div(T, 256) * p.tiles_n;
+  p.nkb = ceil_div(d, 128);
+  if (!map_mx(&p.a, x, d, T, 128)) return LMOE_ERR_CUDA;
+  FFN_TRY(launch_ffn_mx_pair(p, true, h->ctas, stream));
+  p.b[0] = h->down;
+  p.sfa = h->hid_sf;
+  p.sfb = h->down_sf;
+  p.out = out;
+  p.N = d;
+  p.tiles_n = ceil_div(d, kMxTileN);
+  p.tiles = ceil_div(T, 256) * p.tiles_n;
+  p.nkb = ceil_div(F, 128);
+  if (!map_mx(&p.a, h->hid, F, T, 128)) return LMOE_ERR_CUDA;
+  FFN_TRY(launch_ffn_mx_pair(p, false, h->ctas, stream));
+  h->launches = 3;
+  return LMOE_OK;
 }
 
 lmoe_status lmoe_ffn_sync_status(lmoe_ffn_handle h, cudaStream_t stream) {

@@ -72,4 +72,26 @@ struct FfnSkinnyParams {
 bool ffn_skinny_plan(FfnSkinnyParams& p, bool gate_up);
 cudaError_t launch_ffn_skinny(const FfnSkinnyParams& p, bool gate_up, int act, cudaStream_t s);
 
+// ------------------------------------------------------------ MXFP8 passes
+constexpr int kMxTileN = 192;   // weight rows of a tile: 96 gate and 96 up rows, or 192 output features
+struct FfnMxParams {
+  CUtensorMap a, b[2];          // codes, boxes of 128 K values x 128 (a) or 96 (b) rows
+  const uint8_t *sfa, *sfb;     // scale atoms [row / 128][nkb][512], [tile][nkb][2][512]
+  void* out;                    // gate/up: hidden codes [M][N]; else bf16 [M][N]
+  uint8_t* out_sf;              // gate/up: the hidden activation's atoms
+  int out_nkb;
+  int M, N;                     // tokens, output features
+  int tiles_n, tiles, nkb;      // nkb: 128-wide K blocks
+  float b1, b2;
+  int act;
+  int* err;
+};
+cudaError_t launch_ffn_mx_pair(const FfnMxParams& p, bool gate_up, int ctas, cudaStream_t s);
+// Scales [T][K/32] -> atoms; bytes of blocks past K/32 keep the zeros that the
+// buffer is created with where a group of four is not begun.
+cudaError_t launch_mx_row_atoms(const uint8_t* s, int T, int K, uint8_t* out, cudaStream_t stream);
+// Weight scales [rows][K/32] (with `up`: gate and up) -> atoms of `tiles` tiles.
+cudaError_t launch_mx_weight_atoms(const uint8_t* a, const uint8_t* up, int rows, int K, int tiles, uint8_t* out,
+                                   cudaStream_t stream);
+
 }  // namespace lmoe

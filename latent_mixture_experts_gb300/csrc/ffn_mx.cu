@@ -1,0 +1,353 @@
+// The feed-forward block on MXFP8 operands (E4M3 codes, one E8M0 scale per 32
+// values along K): kind::mxf8f6f4 block-scaled tcgen05, scales applied by the
+// tensor cores, fp32 accumulation, on 256 x 192 tiles of CTA pairs.
+//
+// The structure is that of the bf16 pair tiles.  N = 192 rather than 256: two
+// accumulators and seven stages' scales (12 columns each) fit tensor memory,
+// so the epilogue still runs under the next tile's products; 96 gate and 96
+// up rows keep the hidden activation's 32-value blocks inside a tile, and the
+// thread that holds a row encodes them without talking to others.
+//
+// Scales live in memory in the image that the block-scaled MMA wants
+// ("atoms": 512 bytes for 128 rows x 4 blocks), one bulk copy per stage and
+// operand; four warps move them from shared to tensor memory (tcgen05.st), so
+// that the tensor pipe runs products only.  The weights' atoms are laid out
+// once, when the handle is made; the hidden activation's are written by the
+// gate/up epilogue; x's by a small kernel in front.
+#include "ffn_act.cuh"
+#include "ffn_internal.h"
+#include "lmoe_internal.h"
+#include "moe_common.cuh"
+#include "pair.cuh"
+
+namespace lmoe {
+namespace {
+
+constexpr int kHalfN = kMxTileN / 2;                 // B rows of each CTA
+constexpr int kOperandA = 128 * 128, kOperandB = kHalfN * 128;
+constexpr int kStage = kOperandA + kOperandB;
+constexpr int kSf = 512 + 1024;                      // A atom, two B atoms
+constexpr int kStages = 7;
+constexpr int kSmem = kStages * (kStage + kSf) + 1024;
+constexpr int kThreads = 320;                        // TMA, MMA, 4 scale warps, 4 epilogue warps
+constexpr int kSfCols = 12, kSfBase = 2 * kMxTileN;
+constexpr int kTileRows = 8;
+static_assert(kStage % 1024 == 0 && kSmem <= 227 * 1024 && kSfBase + kStages * kSfCols <= 512, "budgets");
+
+__device__ __forceinline__ void mma_mx_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tile_of(const FfnMxParams& p, int i, int& m, int& n) {
+  const int tm = p.tiles / p.tiles_n;
+  const int g = i / (kTileRows * p.tiles_n), r = i - g * kTileRows * p.tiles_n;
+  const int rows = min(kTileRows, tm - g * kTileRows);
+  m = g * kTileRows + r % rows;
+  n = r / rows;
+}
+
+// One 32-value block of the hidden activation: codes to memory, scale byte
+// to its place in the atom.
+__device__ __forceinline__ void store_hidden_block(const float (&h)[32], uint8_t* codes, uint8_t* scale) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) m = max(m, __float_as_uint(fabsf(h[j])));
+  const uint32_t s = m >= 0x7F800000u ? 255u : e4m3_block_scale(__uint_as_float(m));
+  const float inv = s == 255u ? 1.0f : e8m0_to_f32(254u - s);
+  uint32_t q[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(h[4 * j] * inv, h[4 * j + 1] * inv), __NV_SATFINITE,
+                                                 __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(h[4 * j + 2] * inv, h[4 * j + 3] * inv), __NV_SATFINITE,
+                                                 __NV_E4M3);
+    q[j] = lo | (hi << 16);
+  }
+  reinterpret_cast<uint4*>(codes)[0] = make_uint4(q[0], q[1], q[2], q[3]);
+  reinterpret_cast<uint4*>(codes)[1] = make_uint4(q[4], q[5], q[6], q[7]);
+  *scale = static_cast<uint8_t>(s);
+}
+
+// Byte of block `kblk` of `row` in scale atoms [row / 128][nkb][512].
+__device__ __forceinline__ size_t atom_byte(int row, int kblk, int nkb) {
+  return (static_cast<size_t>(row >> 7) * nkb + (kblk >> 2)) * 512 + sf_atom_offset(row & 127, kblk & 3);
+}
+
+template <bool GU, int ACT>
+__global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_constant__ FfnMxParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = align1024(smem_raw);
+  uint8_t* sf = sm + kStages * kStage;
+  // full, sf_ready, acc_empty: used in the even CTA; the others in both
+  __shared__ uint64_t full[kStages], empty[kStages], sf_full[kStages], sf_ready[kStages], acc_full[2], acc_empty[2];
+  __shared__ uint32_t tmem_base;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+      mbar_init(&sf_full[i], 1);
+      mbar_init(&sf_ready[i], 8);       // the scale warps of both CTAs
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 8);      // the epilogue warps of both CTAs
+    }
+    fence_mbar_init();
+  }
+  cluster_sync();
+  if (warp == 1) {
+    tmem_alloc_pair(&tmem_base, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  griddep_launch();
+  griddep_wait();
+  const uint32_t tbase = tmem_base;
+  const int pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int i = first; i < p.tiles && ok; i += pairs) {
+        int m, n;
+        tile_of(p, i, m, n);
+        const int m0 = m * 256 + 128 * rank;
+        const uint8_t* sa_src = p.sfa + static_cast<size_t>(2 * m + rank) * p.nkb * 512;
+        const uint8_t* sb_src = p.sfb + static_cast<size_t>(n) * p.nkb * 1024;
+        for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+          const uint32_t s = it % kStages;
+          if (it >= kStages && !mbar_wait_cluster(&empty[s], ((it / kStages) - 1) & 1, p.err, kErrTimeout)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
+          const uint32_t bar = map_rank(&full[s], 0);
+          uint8_t* sa = sm + s * kStage;
+          tma_load_2d_pair(sa, &p.a, bar, kb * 128, m0);
+          if constexpr (GU)      // gate rows in the even CTA, up rows in the odd one
+            tma_load_2d_pair(sa + kOperandA, &p.b[rank], bar, kb * 128, n * kHalfN);
+          else
+            tma_load_2d_pair(sa + kOperandA, &p.b[0], bar, kb * 128, n * kMxTileN + rank * kHalfN);
+          mbar_arrive_expect_tx(&sf_full[s], kSf);
+          bulk_g2s(sf + s * kSf, sa_src + kb * 512, 512, &sf_full[s]);
+          bulk_g2s(sf + s * kSf + 512, sb_src + kb * 1024, 1024, &sf_full[s]);
+        }
+      }
+      // every stage has been read before the pair may leave; after a wait
+      // that ran out, the copies in flight get a millisecond to land
+      const uint32_t used = it < kStages ? it : kStages;
+      for (uint32_t j = it - used; j < it && ok; ++j)
+        ok = mbar_wait_cluster(&empty[j % kStages], (j / kStages) & 1, p.err, kErrTimeout);
+      if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      const uint64_t a_desc = sdesc_sw128(smem_u32(sm)), b_desc = sdesc_sw128(smem_u32(sm) + kOperandA);
+      uint32_t it = 0, n = 0;
+      bool ok = true;
+      for (int i = first; i < p.tiles && ok; i += pairs, ++n) {
+        const uint32_t b = n & 1, use = n >> 1;
+        if (use > 0 && !mbar_wait_cluster(&acc_empty[b], (use - 1) & 1, p.err, kErrTimeout)) break;
+        tc_fence_after();
+        const uint32_t d = tbase + b * kMxTileN;
+        for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+          const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+          if (!mbar_wait_cluster(&full[s], ph, p.err, kErrTimeout) ||
+              !mbar_wait_cluster(&sf_ready[s], ph, p.err, kErrTimeout)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = a_desc + s * (kStage >> 4), bd = b_desc + s * (kStage >> 4);
+          const uint32_t sfa = tbase + kSfBase + s * kSfCols;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_mx_pair(d, ad + 2 * k, bd + 2 * k, idesc_mxf8f6f4(256, kMxTileN, 0, 0, k, k), sfa, sfa + 4,
+                        (kb | k) != 0);
+          mma_commit_pair(&empty[s]);
+        }
+        if (ok) mma_commit_pair(&acc_full[b]);
+      }
+    }
+  } else if (warp < 6) {
+    // Scale warps: lane r of quarter q writes line r of each atom (the four
+    // k-block scales of rows r, r + 32, r + 64, r + 96) to the quarter's lanes.
+    const uint32_t col0 = tbase + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kSfBase;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int i = first; i < p.tiles && ok; i += pairs)
+      for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+        const uint32_t s = it % kStages;
+        ok = mbar_wait(&sf_full[s], (it / kStages) & 1, p.err, kErrTimeout);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        const uint4* at = reinterpret_cast<const uint4*>(sf + s * kSf) + lane;
+        const uint4 a = at[0], b0 = at[32], b1 = at[64];
+        const uint32_t dst = col0 + s * kSfCols;
+        tmem_st4(dst, a.x, a.y, a.z, a.w);
+        tmem_st4(dst + 4, b0.x, b0.y, b0.z, b0.w);
+        tmem_st4(dst + 8, b1.x, b1.y, b1.z, b1.w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_rank(&sf_ready[s], 0));
+      }
+  } else {
+    const int q = warp & 3;
+    const uint32_t remote_empty[2] = {map_rank(&acc_empty[0], 0), map_rank(&acc_empty[1], 0)};
+    const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
+    uint32_t cnt = 0;
+    for (int i = first; i < p.tiles; i += pairs, ++cnt) {
+      const uint32_t b = cnt & 1;
+      const bool ok = mbar_wait_cluster(&acc_full[b], (cnt >> 1) & 1, p.err, kErrTimeout);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      int m, n;
+      tile_of(p, i, m, n);
+      const int row0 = m * 256 + 128 * rank + 32 * q, row = row0 + lane;
+      const uint32_t acc = tbase + b * kMxTileN + (static_cast<uint32_t>(32 * q) << 16);
+      if (row0 < p.M) {
+        if constexpr (GU) {
+#pragma unroll 1
+          for (int c = 0; c < kHalfN; c += 32) {
+            const int f = n * kHalfN + c;
+            if (f >= p.N) break;
+            uint32_t g[32], u[32];
+            tmem_ld16(acc + c, *reinterpret_cast<uint32_t(*)[16]>(&g[0]));
+            tmem_ld16(acc + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&g[16]));
+            tmem_ld16(acc + kHalfN + c, *reinterpret_cast<uint32_t(*)[16]>(&u[0]));
+            tmem_ld16(acc + kHalfN + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&u[16]));
+            tmem_ld_wait();
+            float h[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) h[j] = glu_hidden<ACT>(__uint_as_float(g[j]), __uint_as_float(u[j]), caps);
+            if (row < p.M)
+              store_hidden_block(h, static_cast<uint8_t*>(p.out) + static_cast<size_t>(row) * p.N + f,
+                                 p.out_sf + atom_byte(row, f >> 5, p.out_nkb));
+          }
+        } else {
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(row) * p.N + n * kMxTileN;
+#pragma unroll 1
+          for (int c = 0; c < kMxTileN; c += 32) {
+            if (n * kMxTileN + c >= p.N) break;      // widths are multiples of 32
+            uint32_t v[32];
+            tmem_ld16(acc + c, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+            tmem_ld16(acc + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+            tmem_ld_wait();
+            if (row < p.M)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(dst + c + 8 * j) =
+                    make_uint4(pack_bf16(__uint_as_float(v[8 * j]), __uint_as_float(v[8 * j + 1])),
+                               pack_bf16(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3])),
+                               pack_bf16(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5])),
+                               pack_bf16(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7])));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(b ? remote_empty[1] : remote_empty[0]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) tmem_dealloc_pair(tbase, 512);
+  cluster_sync();
+}
+
+// x's scales [T][K/32] -> atoms.  One thread per row and group of 4 blocks.
+__global__ void mx_row_atoms_kernel(const uint8_t* __restrict__ s, int T, int kblks, int nkb, uint8_t* __restrict__ out) {
+  griddep_launch();
+  griddep_wait();
+  const long long n = static_cast<long long>(T) * nkb;
+  for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < n;
+       i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const int row = static_cast<int>(i / nkb), g = static_cast<int>(i - static_cast<long long>(row) * nkb);
+    const uint8_t* src = s + static_cast<size_t>(row) * kblks + 4 * g;
+    uint32_t w = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (4 * g + k < kblks) w |= static_cast<uint32_t>(src[k]) << (8 * k);
+    *reinterpret_cast<uint32_t*>(out + atom_byte(row, 4 * g, nkb)) = w;
+  }
+}
+
+// Weight scales -> atoms [tile][nkb][2][512].  Tile row n of 192: with `up`,
+// gate row 96 tile + n, then up row 96 tile + n - 96; else row 192 tile + n of
+// the one matrix.  Rows past the end and blocks past kblks get zeros.
+__global__ void mx_weight_atoms_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ up, int rows,
+                                       int kblks, int nkb, int tiles, uint8_t* __restrict__ out) {
+  const long long n = static_cast<long long>(tiles) * nkb * 256;
+  for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < n;
+       i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const int r = static_cast<int>(i & 255);
+    const long long tk = i >> 8;
+    const int g = static_cast<int>(tk % nkb), t = static_cast<int>(tk / nkb);
+    const uint8_t* src = a;
+    int row = t * kMxTileN + r;
+    if (up) {
+      row = t * kHalfN + (r < kHalfN ? r : r - kHalfN);
+      if (r >= kHalfN) src = up;
+    }
+    uint32_t w = 0;
+    if (r < kMxTileN && row < rows)
+      for (int k = 0; k < 4; ++k)
+        if (4 * g + k < kblks) w |= static_cast<uint32_t>(src[static_cast<size_t>(row) * kblks + 4 * g + k]) << (8 * k);
+    *reinterpret_cast<uint32_t*>(out + tk * 1024 + (r >> 7) * 512 + sf_atom_offset(r & 127, 0)) = w;
+  }
+}
+
+template <bool GU, int ACT>
+cudaError_t launch(const FfnMxParams& p, int ctas, cudaStream_t s) {
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(ffn_mx_pair_kernel<GU, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (attr != cudaSuccess) return attr;
+  return launch_pdl_cluster(ffn_mx_pair_kernel<GU, ACT>, dim3(2 * p.tiles < ctas ? 2 * p.tiles : ctas), dim3(kThreads),
+                            kSmem, 2, s, p);
+}
+
+int ew_blocks(long long n) {
+  const long long b = (n + 255) / 256;
+  return static_cast<int>(b < 152 * 8 ? (b ? b : 1) : 152 * 8);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_row_atoms(const uint8_t* s, int T, int K, uint8_t* out, cudaStream_t stream) {
+  const int nkb = (K + 127) / 128;
+  return launch_pdl(mx_row_atoms_kernel, dim3(ew_blocks(static_cast<long long>(T) * nkb)), dim3(256), 0, stream, s, T,
+                    K / 32, nkb, out);
+}
+
+cudaError_t launch_mx_weight_atoms(const uint8_t* a, const uint8_t* up, int rows, int K, int tiles, uint8_t* out,
+                                   cudaStream_t stream) {
+  const int nkb = (K + 127) / 128;
+  mx_weight_atoms_kernel<<<ew_blocks(256ll * tiles * nkb), 256, 0, stream>>>(a, up, rows, K / 32, nkb, tiles, out);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_ffn_mx_pair(const FfnMxParams& p, bool gate_up, int ctas, cudaStream_t s) {
+  if (!gate_up) return launch<false, 0>(p, ctas, s);
+  return p.act == 1 ? launch<true, 1>(p, ctas, s) : launch<true, 0>(p, ctas, s);
+}
+
+}  // namespace lmoe
