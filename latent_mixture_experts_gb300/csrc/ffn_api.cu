@@ -25,6 +25,7 @@ struct lmoe_ffn_ctx {
   CUtensorMap gate_n, up_n, down_n;   // the same memory as N contiguous operands, boxes of 64 x 64
   // MXFP8 blocks: hid holds codes; scale atoms of x, hid and the weights
   uint8_t *x_sf = nullptr, *hid_sf = nullptr, *gu_sf = nullptr, *down_sf = nullptr;
+  CUtensorMap m_x_sf, m_hid_sf, m_gu_sf, m_down_sf;
   int launches = 0;
 };
 
@@ -57,6 +58,12 @@ bool map_n(CUtensorMap* m, const void* base, int N, int K, long long ld) {
 // MXFP8 codes [rows][K]: boxes of 128 K values x `box` rows.
 bool map_mx(CUtensorMap* m, const void* base, int K, int rows, int box) {
   return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, K, rows, K, 128, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Scale atoms (512 bytes each), `box` at a time.
+bool map_atoms(CUtensorMap* m, const void* base, size_t bytes, int box) {
+  return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, base, 128, bytes / 512, 512, 128, box,
+                      CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // Weight-streaming passes: x (or hid) and the weights of one pass.  `whole`
@@ -211,7 +218,9 @@ lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* 
     if (e == cudaSuccess)
       e = launch_mx_weight_atoms(w->down_s, nullptr, d, F, static_cast<int>(down_tiles), h->down_sf, stream);
     ok = map_mx(&h->gate, w->gate, d, F, kMxTileN / 2) && map_mx(&h->up, w->up, d, F, kMxTileN / 2) &&
-         map_mx(&h->down, w->down, F, d, kMxTileN / 2);
+         map_mx(&h->down, w->down, F, d, kMxTileN / 2) && map_atoms(&h->m_x_sf, h->x_sf, x_sf, 1) &&
+         map_atoms(&h->m_hid_sf, h->hid_sf, hid_sf, 1) && map_atoms(&h->m_gu_sf, h->gu_sf, gu_sf, 2) &&
+         map_atoms(&h->m_down_sf, h->down_sf, down_sf, 2);
   } else {
     h->dg = base + 256 + act_bytes;
     h->du = base + 256 + 2 * act_bytes;
@@ -396,8 +405,8 @@ lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8
   p.err = h->err;
   p.b[0] = h->gate;
   p.b[1] = h->up;
-  p.sfa = h->x_sf;
-  p.sfb = h->gu_sf;
+  p.sfa = h->m_x_sf;
+  p.sfb = h->m_gu_sf;
   p.out = h->hid;
   p.out_sf = h->hid_sf;
   p.out_nkb = ceil_div(F, 128);
@@ -409,8 +418,8 @@ lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8
   if (!map_mx(&p.a, x, d, T, 128)) return LMOE_ERR_CUDA;
   FFN_TRY(launch_ffn_mx_pair(p, true, h->ctas, stream));
   p.b[0] = h->down;
-  p.sfa = h->hid_sf;
-  p.sfb = h->down_sf;
+  p.sfa = h->m_hid_sf;
+  p.sfb = h->m_down_sf;
   p.out = out;
   p.N = d;
   p.tiles_n = ceil_div(d, kMxTileN);

@@ -76,7 +76,7 @@ cudaError_t launch_ffn_skinny(const FfnSkinnyParams& p, bool gate_up, int act, c
 constexpr int kMxTileN = 192;   // weight rows of a tile: 96 gate and 96 up rows, or 192 output features
 struct FfnMxParams {
   CUtensorMap a, b[2];          // codes, boxes of 128 K values x 128 (a) or 96 (b) rows
-  const uint8_t *sfa, *sfb;     // scale atoms [row / 128][nkb][512], [tile][nkb][2][512]
+  CUtensorMap sfa, sfb;         // scale atoms [row / 128][nkb], [tile][nkb][2] of 128 32-bit words; boxes of 1 and 2
   void* out;                    // gate/up: hidden codes [M][N]; else bf16 [M][N]
   uint8_t* out_sf;              // gate/up: the hidden activation's atoms
   int out_nkb;

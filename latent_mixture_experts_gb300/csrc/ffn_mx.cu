@@ -9,15 +9,15 @@
 // thread that holds a row encodes them without talking to others.
 //
 // Scales live in memory in the image that the block-scaled MMA wants
-// ("atoms": 512 bytes for 128 rows x 4 blocks), one bulk copy per stage and
-// operand; four warps move them from shared to tensor memory (tcgen05.st), so
-// that the tensor pipe runs products only.  The weights' atoms are laid out
-// once, when the handle is made; the hidden activation's are written by the
-// gate/up epilogue; x's by a small kernel in front.
+// ("atoms": 512 bytes for 128 rows x 4 blocks) and come with the operands;
+// the MMA thread copies them on to tensor memory (tcgen05.cp) ahead of each
+// stage's products.  CPCOMMENT
+// The weights' atoms are laid out once, when the handle is made; the hidden
+// activation's are written by the gate/up epilogue; x's by a small kernel in
+// front.
 #include "ffn_act.cuh"
 #include "ffn_internal.h"
 #include "lmoe_internal.h"
-#include "moe_common.cuh"
 #include "pair.cuh"
 
 namespace lmoe {
@@ -29,7 +29,7 @@ constexpr int kStage = kOperandA + kOperandB;
 constexpr int kSf = 512 + 1024;                      // A atom, two B atoms
 constexpr int kStages = 7;
 constexpr int kSmem = kStages * (kStage + kSf) + 1024;
-constexpr int kThreads = 320;                        // TMA, MMA, 4 scale warps, 4 epilogue warps
+constexpr int kThreads = 192;                        // TMA, MMA, 4 epilogue warps
 constexpr int kSfCols = 12, kSfBase = 2 * kMxTileN;
 constexpr int kTileRows = 8;
 static_assert(kStage % 1024 == 0 && kSmem <= 227 * 1024 && kSfBase + kStages * kSfCols <= 512, "budgets");
@@ -42,6 +42,11 @@ __device__ __forceinline__ void mma_mx_pair(uint32_t d_tmem, uint64_t adesc, uin
           d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
+}
+
+// A 512-byte scale atom of each CTA's shared memory to its own tensor memory.
+__device__ __forceinline__ void copy_atom_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
 __device__ __forceinline__ void tile_of(const FfnMxParams& p, int i, int& m, int& n) {
@@ -84,8 +89,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   uint8_t* sf = sm + kStages * kStage;
-  // full, sf_ready, acc_empty: used in the even CTA; the others in both
-  __shared__ uint64_t full[kStages], empty[kStages], sf_full[kStages], sf_ready[kStages], acc_full[2], acc_empty[2];
+  // full, acc_empty: used in the even CTA; the others in both
+  __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_base;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -94,8 +99,6 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
-      mbar_init(&sf_full[i], 1);
-      mbar_init(&sf_ready[i], 8);       // the scale warps of both CTAs
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -124,15 +127,14 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
         int m, n;
         tile_of(p, i, m, n);
         const int m0 = m * 256 + 128 * rank;
-        const uint8_t* sa_src = p.sfa + static_cast<size_t>(2 * m + rank) * p.nkb * 512;
-        const uint8_t* sb_src = p.sfb + static_cast<size_t>(n) * p.nkb * 1024;
+        const int atom_a = (2 * m + rank) * p.nkb, atom_b = 2 * n * p.nkb;
         for (int kb = 0; kb < p.nkb; ++kb, ++it) {
           const uint32_t s = it % kStages;
           if (it >= kStages && !mbar_wait_cluster(&empty[s], ((it / kStages) - 1) & 1, p.err, kErrTimeout)) {
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kStage + kSf));
           const uint32_t bar = map_rank(&full[s], 0);
           uint8_t* sa = sm + s * kStage;
           tma_load_2d_pair(sa, &p.a, bar, kb * 128, m0);
@@ -140,9 +142,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
             tma_load_2d_pair(sa + kOperandA, &p.b[rank], bar, kb * 128, n * kHalfN);
           else
             tma_load_2d_pair(sa + kOperandA, &p.b[0], bar, kb * 128, n * kMxTileN + rank * kHalfN);
-          mbar_arrive_expect_tx(&sf_full[s], kSf);
-          bulk_g2s(sf + s * kSf, sa_src + kb * 512, 512, &sf_full[s]);
-          bulk_g2s(sf + s * kSf + 512, sb_src + kb * 1024, 1024, &sf_full[s]);
+          tma_load_2d_pair(sf + s * kSf, &p.sfa, bar, 0, atom_a + kb);
+          tma_load_2d_pair(sf + s * kSf + 512, &p.sfb, bar, 0, atom_b + 2 * kb);   // both CTAs need all N scales
         }
       }
       // every stage has been read before the pair may leave; after a wait
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       const uint64_t a_desc = sdesc_sw128(smem_u32(sm)), b_desc = sdesc_sw128(smem_u32(sm) + kOperandA);
+      const uint64_t sf_desc = sdesc_noswz(smem_u32(sf), 16, 128);
       uint32_t it = 0, n = 0;
       bool ok = true;
       for (int i = first; i < p.tiles && ok; i += pairs, ++n) {
@@ -167,14 +169,16 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
         const uint32_t d = tbase + b * kMxTileN;
         for (int kb = 0; kb < p.nkb; ++kb, ++it) {
           const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-          if (!mbar_wait_cluster(&full[s], ph, p.err, kErrTimeout) ||
-              !mbar_wait_cluster(&sf_ready[s], ph, p.err, kErrTimeout)) {
+          if (!mbar_wait_cluster(&full[s], ph, p.err, kErrTimeout)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t ad = a_desc + s * (kStage >> 4), bd = b_desc + s * (kStage >> 4);
           const uint32_t sfa = tbase + kSfBase + s * kSfCols;
+          const uint64_t sd = sf_desc + s * (kSf >> 4);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) copy_atom_pair(sfa + 4 * k, sd + 32 * k);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_mx_pair(d, ad + 2 * k, bd + 2 * k, idesc_mxf8f6f4(256, kMxTileN, 0, 0, k, k), sfa, sfa + 4,
@@ -184,31 +188,6 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
         if (ok) mma_commit_pair(&acc_full[b]);
       }
     }
-  } else if (warp < 6) {
-    // Scale warps: lane r of quarter q writes line r of each atom (the four
-    // k-block scales of rows r, r + 32, r + 64, r + 96) to the quarter's lanes.
-    const uint32_t col0 = tbase + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kSfBase;
-    uint32_t it = 0;
-    bool ok = true;
-    for (int i = first; i < p.tiles && ok; i += pairs)
-      for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-        const uint32_t s = it % kStages;
-        ok = mbar_wait(&sf_full[s], (it / kStages) & 1, p.err, kErrTimeout);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
-        }
-        const uint4* at = reinterpret_cast<const uint4*>(sf + s * kSf) + lane;
-        const uint4 a = at[0], b0 = at[32], b1 = at[64];
-        const uint32_t dst = col0 + s * kSfCols;
-        tmem_st4(dst, a.x, a.y, a.z, a.w);
-        tmem_st4(dst + 4, b0.x, b0.y, b0.z, b0.w);
-        tmem_st4(dst + 8, b1.x, b1.y, b1.z, b1.w);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_rank(&sf_ready[s], 0));
-      }
   } else {
     const int q = warp & 3;
     const uint32_t remote_empty[2] = {map_rank(&acc_empty[0], 0), map_rank(&acc_empty[1], 0)};
