@@ -21,7 +21,7 @@
 #include "ffn_act.cuh"
 #include "ffn_internal.h"
 #include "lmoe_internal.h"
-#include "pair.cuh"
+#include "issue.cuh"
 
 namespace lmoe {
 namespace {
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
   __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_base;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known uniform
   const uint32_t rank = cluster_rank();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -190,57 +190,54 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
   const int total = p.tile_end[p.nprod - 1];
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int i = first; i < total && ok; i += pairs) {
-        const Tile t = tile_of(p, i);
-        const int m0 = t.m * 256 + 128 * static_cast<int>(rank);
-        for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-          const uint32_t s = it % kStages;
-          if (it >= kStages && !mbar_wait_cluster(&empty[s], ((it / kStages) - 1) & 1, p.err, kErrTimeout)) {
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
-          const uint32_t bar = map_rank(&full[s], 0);
-          uint8_t* sa = sm + s * kStage;
-          uint8_t* sb = sa + kOperand;
-          int src = t.prod, k0 = kb * 64;
-          if (MODE == kFfnDx && kb >= p.nkb0) {
-            src = 1;
-            k0 = (kb - p.nkb0) * 64;
-          }
-          if constexpr (kAMn) {
-            tma_load_2d_pair(sa, &p.a[src], bar, m0, k0);
-            tma_load_2d_pair(sa + 8192, &p.a[src], bar, m0 + 64, k0);
-          } else {
-            tma_load_2d_pair(sa, &p.a[src], bar, k0, m0);
-          }
-          if constexpr (MODE == kFfnGateUp) {   // gate rows in the even CTA, up rows in the odd one
-            tma_load_2d_pair(sb, &p.b[rank], bar, k0, t.n * 128);
-          } else if constexpr (kBMn) {
-            const int n0 = t.n * 256 + 128 * static_cast<int>(rank);
-            tma_load_2d_pair(sb, &p.b[src], bar, n0, k0);
-            tma_load_2d_pair(sb + 8192, &p.b[src], bar, n0 + 64, k0);
-          } else {
-            tma_load_2d_pair(sb, &p.b[src], bar, k0, t.n * 256 + 128 * static_cast<int>(rank));
-          }
+    uint32_t it = 0;
+    bool ok = true;
+    for (int i = first; i < total && ok; i += pairs) {
+      const Tile t = tile_of(p, i);
+      const int m0 = t.m * 256 + 128 * static_cast<int>(rank);
+      for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+        const uint32_t s = it % kStages;
+        if (it >= kStages && !warp_wait(&empty[s], ((it / kStages) - 1) & 1, p.err)) {
+          ok = false;
+          break;
+        }
+        if (rank == 0) w_arrive_expect_tx(&full[s], 2 * kStage);
+        const uint32_t bar = map_rank(&full[s], 0);
+        uint8_t* sa = sm + s * kStage;
+        uint8_t* sb = sa + kOperand;
+        int src = t.prod, k0 = kb * 64;
+        if (MODE == kFfnDx && kb >= p.nkb0) {
+          src = 1;
+          k0 = (kb - p.nkb0) * 64;
+        }
+        if constexpr (kAMn) {
+          w_load_2d_pair(sa, &p.a[src], bar, m0, k0);
+          w_load_2d_pair(sa + 8192, &p.a[src], bar, m0 + 64, k0);
+        } else {
+          w_load_2d_pair(sa, &p.a[src], bar, k0, m0);
+        }
+        if constexpr (MODE == kFfnGateUp) {   // gate rows in the even CTA, up rows in the odd one
+          w_load_2d_pair(sb, &p.b[rank], bar, k0, t.n * 128);
+        } else if constexpr (kBMn) {
+          const int n0 = t.n * 256 + 128 * static_cast<int>(rank);
+          w_load_2d_pair(sb, &p.b[src], bar, n0, k0);
+          w_load_2d_pair(sb + 8192, &p.b[src], bar, n0 + 64, k0);
+        } else {
+          w_load_2d_pair(sb, &p.b[src], bar, k0, t.n * 256 + 128 * static_cast<int>(rank));
         }
       }
-      // Every stage has been read by the MMAs (and so every copy has landed)
-      // before the pair may leave; if a wait ran out, the copies in flight
-      // get a millisecond to land.
-      const uint32_t used = it < kStages ? it : kStages;
-      for (uint32_t j = it - used; j < it && ok; ++j)
-        ok = mbar_wait_cluster(&empty[j % kStages], (j / kStages) & 1, p.err, kErrTimeout);
-      if (!ok) {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
-      }
+    }
+    // Every stage has been read by the MMAs (and so every copy has landed)
+    // before the pair may leave; if a wait ran out, the copies in flight get a
+    // millisecond to land.
+    const uint32_t used = it < kStages ? it : kStages;
+    for (uint32_t j = it - used; j < it && ok; ++j) ok = warp_wait(&empty[j % kStages], (j / kStages) & 1, p.err);
+    if (!ok) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t idesc = idesc_bf16(256, 256) | (kAMn ? kIdescAMajorMn : 0u) | (kBMn ? kIdescBMajorMn : 0u);
       const uint32_t base = smem_u32(sm);
       const uint64_t a_desc = kAMn ? sdesc_sw128_mn(base, 8192) : sdesc_sw128(base);
@@ -249,12 +246,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
       bool ok = true;
       for (int i = first; i < total && ok; i += pairs, ++n) {
         const uint32_t b = n & 1, use = n >> 1;
-        if (use > 0 && !mbar_wait_cluster(&acc_empty[b], (use - 1) & 1, p.err, kErrTimeout)) break;
+        if (use > 0 && !warp_wait(&acc_empty[b], (use - 1) & 1, p.err)) break;
         tc_fence_after();
         const uint32_t d = tbase + b * 256;
         for (int kb = 0; kb < p.nkb; ++kb, ++it) {
           const uint32_t s = it % kStages;
-          if (!mbar_wait_cluster(&full[s], (it / kStages) & 1, p.err, kErrTimeout)) {
+          if (!warp_wait(&full[s], (it / kStages) & 1, p.err)) {
             ok = false;
             break;
           }
@@ -264,10 +261,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
           const uint64_t ad = a_desc + s * (kStage >> 4), bd = b_desc + s * (kStage >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_bf16_pair(d, ad + k * (kAMn ? 128 : 2), bd + k * (kBMn ? 128 : 2), idesc, (kb | k) != 0);
-          mma_commit_pair(&empty[s]);
+            w_mma_bf16_pair(d, ad + k * (kAMn ? 128 : 2), bd + k * (kBMn ? 128 : 2), idesc, (kb | k) != 0);
+          w_commit_pair(&empty[s]);
         }
-        if (ok) mma_commit_pair(&acc_full[b]);
+        if (ok) w_commit_pair(&acc_full[b]);
       }
     }
   } else {

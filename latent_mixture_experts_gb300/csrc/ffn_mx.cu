@@ -18,7 +18,7 @@
 #include "ffn_act.cuh"
 #include "ffn_internal.h"
 #include "lmoe_internal.h"
-#include "pair.cuh"
+#include "issue.cuh"
 
 namespace lmoe {
 namespace {
@@ -33,21 +33,6 @@ constexpr int kThreads = 192;                        // TMA, MMA, 4 epilogue war
 constexpr int kSfCols = 12, kSfBase = 2 * kMxTileN;
 constexpr int kTileRows = 8;
 static_assert(kStage % 1024 == 0 && kSmem <= 227 * 1024 && kSfBase + kStages * kSfCols <= 512, "budgets");
-
-__device__ __forceinline__ void mma_mx_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-          d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
-}
-
-// A 512-byte scale atom of each CTA's shared memory to its own tensor memory.
-__device__ __forceinline__ void copy_atom_pair(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
 
 __device__ __forceinline__ void tile_of(const FfnMxParams& p, int i, int& m, int& n) {
   const int tm = p.tiles / p.tiles_n;
@@ -93,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
   __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_base;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known uniform
   const int rank = static_cast<int>(cluster_rank());
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -120,72 +105,69 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
   const int pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int i = first; i < p.tiles && ok; i += pairs) {
-        int m, n;
-        tile_of(p, i, m, n);
-        const int m0 = m * 256 + 128 * rank;
-        const int atom_a = (2 * m + rank) * p.nkb, atom_b = 2 * n * p.nkb;
-        for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-          const uint32_t s = it % kStages;
-          if (it >= kStages && !mbar_wait_cluster(&empty[s], ((it / kStages) - 1) & 1, p.err, kErrTimeout)) {
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kStage + kSf));
-          const uint32_t bar = map_rank(&full[s], 0);
-          uint8_t* sa = sm + s * kStage;
-          tma_load_2d_pair(sa, &p.a, bar, kb * 128, m0);
-          if constexpr (GU)      // gate rows in the even CTA, up rows in the odd one
-            tma_load_2d_pair(sa + kOperandA, &p.b[rank], bar, kb * 128, n * kHalfN);
-          else
-            tma_load_2d_pair(sa + kOperandA, &p.b[0], bar, kb * 128, n * kMxTileN + rank * kHalfN);
-          tma_load_2d_pair(sf + s * kSf, &p.sfa, bar, 0, atom_a + kb);
-          tma_load_2d_pair(sf + s * kSf + 512, &p.sfb, bar, 0, atom_b + 2 * kb);   // both CTAs need all N scales
+    uint32_t it = 0;
+    bool ok = true;
+    for (int i = first; i < p.tiles && ok; i += pairs) {
+      int m, n;
+      tile_of(p, i, m, n);
+      const int m0 = m * 256 + 128 * rank;
+      const int atom_a = (2 * m + rank) * p.nkb, atom_b = 2 * n * p.nkb;
+      for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+        const uint32_t s = it % kStages;
+        if (it >= kStages && !warp_wait(&empty[s], ((it / kStages) - 1) & 1, p.err)) {
+          ok = false;
+          break;
         }
-      }
-      // every stage has been read before the pair may leave; after a wait
-      // that ran out, the copies in flight get a millisecond to land
-      const uint32_t used = it < kStages ? it : kStages;
-      for (uint32_t j = it - used; j < it && ok; ++j)
-        ok = mbar_wait_cluster(&empty[j % kStages], (j / kStages) & 1, p.err, kErrTimeout);
-      if (!ok) {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+        if (rank == 0) w_arrive_expect_tx(&full[s], 2 * (kStage + kSf));
+        const uint32_t bar = map_rank(&full[s], 0);
+        uint8_t* sa = sm + s * kStage;
+        w_load_2d_pair(sa, &p.a, bar, kb * 128, m0);
+        if constexpr (GU)      // gate rows in the even CTA, up rows in the odd one
+          w_load_2d_pair(sa + kOperandA, &p.b[rank], bar, kb * 128, n * kHalfN);
+        else
+          w_load_2d_pair(sa + kOperandA, &p.b[0], bar, kb * 128, n * kMxTileN + rank * kHalfN);
+        w_load_2d_pair(sf + s * kSf, &p.sfa, bar, 0, atom_a + kb);
+        w_load_2d_pair(sf + s * kSf + 512, &p.sfb, bar, 0, atom_b + 2 * kb);   // both CTAs need all N scales
       }
     }
+    // every stage has been read before the pair may leave; after a wait that
+    // ran out, the copies in flight get a millisecond to land
+    const uint32_t used = it < kStages ? it : kStages;
+    for (uint32_t j = it - used; j < it && ok; ++j) ok = warp_wait(&empty[j % kStages], (j / kStages) & 1, p.err);
+    if (!ok) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint64_t a_desc = sdesc_sw128(smem_u32(sm)), b_desc = sdesc_sw128(smem_u32(sm) + kOperandA);
       const uint64_t sf_desc = sdesc_noswz(smem_u32(sf), 16, 128);
       uint32_t it = 0, n = 0;
       bool ok = true;
       for (int i = first; i < p.tiles && ok; i += pairs, ++n) {
         const uint32_t b = n & 1, use = n >> 1;
-        if (use > 0 && !mbar_wait_cluster(&acc_empty[b], (use - 1) & 1, p.err, kErrTimeout)) break;
+        if (use > 0 && !warp_wait(&acc_empty[b], (use - 1) & 1, p.err)) break;
         tc_fence_after();
         const uint32_t d = tbase + b * kMxTileN;
         for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-          const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-          if (!mbar_wait_cluster(&full[s], ph, p.err, kErrTimeout)) {
+          const uint32_t s = it % kStages;
+          if (!warp_wait(&full[s], (it / kStages) & 1, p.err)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t ad = a_desc + s * (kStage >> 4), bd = b_desc + s * (kStage >> 4);
-          const uint32_t sfa = tbase + kSfBase + s * kSfCols;
           const uint64_t sd = sf_desc + s * (kSf >> 4);
+          const uint32_t sfa = tbase + kSfBase + s * kSfCols;
 #pragma unroll
-          for (int k = 0; k < 3; ++k) copy_atom_pair(sfa + 4 * k, sd + 32 * k);
+          for (int k = 0; k < 3; ++k) w_copy_atom_pair(sfa + 4 * k, sd + 32 * k);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_mx_pair(d, ad + 2 * k, bd + 2 * k, idesc_mxf8f6f4(256, kMxTileN, 0, 0, k, k), sfa, sfa + 4,
-                        (kb | k) != 0);
-          mma_commit_pair(&empty[s]);
+            w_mma_mx_pair(d, ad + 2 * k, bd + 2 * k, idesc_mxf8f6f4(256, kMxTileN, 0, 0, k, k), sfa, sfa + 4,
+                          (kb | k) != 0);
+          w_commit_pair(&empty[s]);
         }
-        if (ok) mma_commit_pair(&acc_full[b]);
+        if (ok) w_commit_pair(&acc_full[b]);
       }
     }
   } else {

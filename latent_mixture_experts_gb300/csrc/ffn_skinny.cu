@@ -17,7 +17,7 @@
 #include "ffn_act.cuh"
 #include "ffn_internal.h"
 #include "lmoe_internal.h"
-#include "pair.cuh"
+#include "issue.cuh"
 
 namespace lmoe {
 namespace {
@@ -25,15 +25,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kCols = 128;       // MMA columns: weight rows of a tile
 constexpr int kMinCtas = 150;    // about one CTA per SM at least
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2,
-                                            int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
-      "[%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
 
 __device__ __forceinline__ void st_cluster4(uint32_t addr, const uint32_t* v) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -55,7 +46,7 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
   uint8_t* sm = align1024(smem_raw);
   __shared__ uint64_t full[kSkinnyMaxStages], empty[kSkinnyMaxStages], done;
   __shared__ uint32_t tmem_base;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known uniform
   constexpr int N = kCols;
   constexpr int kRows = GU ? N / 2 : N;               // features of the cluster
   const int rank = static_cast<int>(cluster_rank());  // K split of this CTA
@@ -85,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
   // ring, has finished with it) before another one writes to it.
   if (!p.reuse_ring) cluster_arrive();
   const uint32_t tacc = tmem_base;
-  const bool producer = warp == 0 && lane == 0;
+  const bool producer = warp == 0;
   // The dependents are let in only after everything before this kernel has
   // finished: the down pass may then read its weights at once.
   if (GU || !producer) {
@@ -99,20 +90,20 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
       uint8_t* dst = sb + s * b_slot;
       if (GU && p.apart) {
         for (int c = 0; c < p.kc; ++c) {
-          tma_load_2d(dst + c * b_chunk, &p.b, &full[s], (i * p.kc + c) * 64, f0);
-          tma_load_2d(dst + c * b_chunk + (b_chunk >> 1), &p.b_up, &full[s], (i * p.kc + c) * 64, f0);
+          w_load_2d(dst + c * b_chunk, &p.b, &full[s], (i * p.kc + c) * 64, f0);
+          w_load_2d(dst + c * b_chunk + (b_chunk >> 1), &p.b_up, &full[s], (i * p.kc + c) * 64, f0);
         }
       } else if (p.whole) {
         if constexpr (GU)
-          tma_load_4d(dst, &p.b, &full[s], 0, f0, 0, i * p.kc);
+          w_load_4d(dst, &p.b, &full[s], 0, f0, 0, i * p.kc);
         else
-          tma_load_3d(dst, &p.b, &full[s], 0, f0, i * p.kc);
+          w_load_3d(dst, &p.b, &full[s], 0, f0, i * p.kc);
       } else {
         for (int c = 0; c < p.kc; ++c) {
           if constexpr (GU)
-            tma_load_3d(dst + c * b_chunk, &p.b, &full[s], (i * p.kc + c) * 64, f0, 0);
+            w_load_3d(dst + c * b_chunk, &p.b, &full[s], (i * p.kc + c) * 64, f0, 0);
           else
-            tma_load_2d(dst + c * b_chunk, &p.b, &full[s], (i * p.kc + c) * 64, f0);
+            w_load_2d(dst + c * b_chunk, &p.b, &full[s], (i * p.kc + c) * 64, f0);
         }
       }
     };
@@ -120,14 +111,14 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
       i += first;
       uint8_t* dst = sm + s * a_slot;
       if (p.whole) {
-        tma_load_3d(dst, &p.a, &full[s], 0, 0, i * p.kc);
+        w_load_3d(dst, &p.a, &full[s], 0, 0, i * p.kc);
       } else {
-        for (int c = 0; c < p.kc; ++c) tma_load_2d(dst + c * a_chunk, &p.a, &full[s], (i * p.kc + c) * 64, 0);
+        for (int c = 0; c < p.kc; ++c) w_load_2d(dst + c * a_chunk, &p.a, &full[s], (i * p.kc + c) * 64, 0);
       }
     };
     const int pre = steps < p.stages ? steps : p.stages;
     for (int i = 0; i < pre; ++i) {
-      mbar_arrive_expect_tx(&full[i], a_slot + b_slot);
+      w_arrive_expect_tx(&full[i], a_slot + b_slot);
       load_b(i, i);
       if (GU) load_a(i, i);
     }
@@ -139,35 +130,34 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
     int s = pre == p.stages ? 0 : pre;
     uint32_t phase = 0;
     for (int i = pre; i < steps; ++i) {
-      if (!mbar_wait(&empty[s], phase, p.err, kErrTimeout)) break;
-      mbar_arrive_expect_tx(&full[s], a_slot + b_slot);
+      if (!warp_wait(&empty[s], phase, p.err)) break;
+      w_arrive_expect_tx(&full[s], a_slot + b_slot);
       load_b(i, s);
       load_a(i, s);
       if (++s == p.stages) s = 0, phase ^= 1;
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     const uint32_t idesc = idesc_bf16(128, N);
     const uint64_t a_desc = sdesc_sw128(smem_u32(sm)), b_desc = sdesc_sw128(smem_u32(sb));
     int s = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int i = 0; i < steps; ++i) {
-      if (!(ok = mbar_wait(&full[s], phase, p.err, kErrTimeout))) break;
+      if (!(ok = warp_wait(&full[s], phase, p.err))) break;
       tc_fence_after();
-      // descriptors count 16-byte units: one addition each per MMA, as this
-      // single thread's instructions would otherwise take longer than the MMAs
+      // descriptors count 16-byte units
       uint64_t ad = a_desc + static_cast<uint32_t>(s * a_slot >> 4), bd = b_desc + static_cast<uint32_t>(s * b_slot >> 4);
       for (int c = 0; c < p.kc; ++c) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_bf16(tacc, ad + 2 * k, bd + 2 * k, idesc, (i | c | k) != 0);
+          w_mma_bf16(tacc, ad + 2 * k, bd + 2 * k, idesc, (i | c | k) != 0);
         ad += a_chunk >> 4;
         bd += b_chunk >> 4;
       }
-      mma_commit(&empty[s]);
+      w_commit(&empty[s]);
       if (++s == p.stages) s = 0, phase ^= 1;
     }
-    mma_commit(&done);
+    w_commit(&done);
   }
   __syncwarp();
 
