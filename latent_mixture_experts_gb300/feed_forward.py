@@ -22,17 +22,17 @@ _BF16, _U8, _F32 = torch.bfloat16, torch.uint8, torch.float32
 
 def _rows(name: str, t: torch.Tensor, dtypes, shape) -> int:
     """Row stride of a 2-D tensor, after checking what the kernels rely on."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.shape == shape:
+        if t.is_contiguous() or t.shape[0] <= 1 and t.stride(1) == 1:
+            return t.shape[1]
+        if t.stride(1) == 1 or t.shape[1] <= 1:
+            return t.stride(0)
+        raise ValueError(f"{name} must be contiguous along its last dimension")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.is_contiguous() or t.shape[0] <= 1 and t.stride(1) == 1:
-        return t.shape[1]
-    if t.stride(1) != 1 and t.shape[1] > 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-    return t.stride(0)
+    raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def _packed(name: str, t: torch.Tensor, dtype, shape):
@@ -40,10 +40,123 @@ def _packed(name: str, t: torch.Tensor, dtype, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _on_device(dev: int, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, not on CUDA device {dev}")
+def _on_device(dev: int, *tensors):
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, not on CUDA device {dev}")
+
+
+# The current device and stream without building their objects: a call on one
+# token takes a few microseconds.
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _device_of(t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev != _raw_device():
+        raise ValueError("tensors must be on the current CUDA device")
+    return dev
+
+
+def _norm_weight(w: torch.Tensor, shape):
+    if w.dtype is not _BF16 or w.shape != shape or not w.is_contiguous():
+        raise ValueError(f"norm_w must be a contiguous CUDA bfloat16 tensor of shape {tuple(shape)}")
+
+
+def lmoe_add_rms_norm(x: torch.Tensor, norm_w: torch.Tensor, eps: float, residual: torch.Tensor | None = None,
+                      out_format: str = "bf16", h_out: torch.Tensor | None = None, stream=None):
+    """h = residual + x (in residual's dtype, bf16 or fp32; h = x without a
+    residual), y = norm_w * h / sqrt(mean(h^2) + eps).
+
+    Returns (y, scales, h): y bf16 [T][d] and scales None, or with
+    out_format="mxfp8" E4M3 codes uint8 [T][d] and E8M0 scales uint8
+    [T][d/32]; h None without a residual.  h_out may be the residual itself."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return lmoe_add_rms_norm(x, norm_w, eps, residual, out_format, h_out)
+    fmt = _OUT_FORMATS.get(out_format)
+    if fmt is None:
+        raise ValueError(f"out_format must be one of {sorted(_OUT_FORMATS)}")
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError("x must be [T][d]")
+    T, d = shape
+    ldx = _rows("x", x, (_BF16,), shape)
+    dev = _device_of(x)
+    _norm_weight(norm_w, shape[1:])
+    s = sp = rp = hp = h = None
+    ldr, st = d, 0
+    if residual is not None:
+        ldr = _rows("residual", residual, (_BF16, _F32), shape)
+        _on_device(dev, norm_w, residual)
+        st = _STREAM_TYPES[residual.dtype]
+        if h_out is None:
+            h = torch.empty(shape, dtype=residual.dtype, device=x.device)
+        else:
+            h = h_out
+            _packed("h_out", h, residual.dtype, shape)
+            _on_device(dev, h)
+        rp, hp = residual.data_ptr(), h.data_ptr()
+    else:
+        _on_device(dev, norm_w)
+        if h_out is not None:
+            raise ValueError("h_out needs a residual")
+    if fmt:
+        y = torch.empty(shape, dtype=_U8, device=x.device)
+        s = torch.empty(T, d // 32, dtype=_U8, device=x.device)
+        sp = s.data_ptr()
+    else:
+        y = torch.empty(shape, dtype=_BF16, device=x.device)
+    status = B.load_library().lmoe_add_rms_norm(x.data_ptr(), ldx, rp, ldr, st, T, d, norm_w.data_ptr(), eps, hp,
+                                                y.data_ptr(), fmt, sp, _raw_stream(dev))
+    if status:
+        raise B.LmoeError("lmoe_add_rms_norm", status)
+    return y, s, h
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_backward_workspace(T: int, d: int) -> int:
+    n = ctypes.c_size_t()
+    B._check("lmoe_add_rms_norm_backward_workspace",
+             B.load_library().lmoe_add_rms_norm_backward_workspace(T, d, ctypes.byref(n)))
+    return n.value
+
+
+def lmoe_add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, norm_w: torch.Tensor, eps: float,
+                               dh: torch.Tensor | None = None, stream=None):
+    """Gradients of lmoe_add_rms_norm from dy bf16 [T][d] and its h (bf16 or
+    fp32); dh (h's dtype): the gradient along the residual stream.  Returns
+    (dx in h's dtype, the gradient of x and of the residual alike; d norm_w
+    fp32 [d])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return lmoe_add_rms_norm_backward(dy, h, norm_w, eps, dh)
+    shape = h.shape
+    if len(shape) != 2:
+        raise ValueError("h must be [T][d]")
+    T, d = shape
+    ldh = _rows("h", h, (_BF16, _F32), shape)
+    lddy = _rows("dy", dy, (_BF16,), shape)
+    dev = _device_of(h)
+    _norm_weight(norm_w, shape[1:])
+    _on_device(dev, dy, norm_w)
+    lddh, ep = d, None
+    if dh is not None:
+        lddh = _rows("dh", dh, (h.dtype,), shape)
+        _on_device(dev, dh)
+        ep = dh.data_ptr()
+    n = _norm_backward_workspace(T, d)
+    dx = torch.empty(shape, dtype=h.dtype, device=h.device)
+    dw = torch.empty(d, dtype=_F32, device=h.device)
+    ws = torch.empty(n, dtype=_U8, device=h.device)
+    status = B.load_library().lmoe_add_rms_norm_backward(
+        dy.data_ptr(), lddy, h.data_ptr(), ldh, ep, lddh, _STREAM_TYPES[h.dtype], T, d, norm_w.data_ptr(), eps,
+        dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), n, _raw_stream(dev))
+    if status:
+        raise B.LmoeError("lmoe_add_rms_norm_backward", status)
+    return dx, dw
 
 
 def _on_stream(f):
@@ -55,100 +168,6 @@ def _on_stream(f):
         with torch.cuda.stream(stream):
             return f(*args, **kw)
     return call
-
-
-# The current stream's handle without building a Stream object: a call on one token takes a few microseconds.
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _device_of(t: torch.Tensor) -> int:
-    dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError("tensors must be on the current CUDA device")
-    return dev
-
-
-def _norm_weight(w: torch.Tensor, d: int):
-    if w.dtype is not _BF16 or w.shape != (d,) or not w.is_contiguous():
-        raise ValueError(f"norm_w must be a contiguous CUDA bfloat16 tensor of shape ({d},)")
-
-
-@_on_stream
-def lmoe_add_rms_norm(x: torch.Tensor, norm_w: torch.Tensor, eps: float, residual: torch.Tensor | None = None,
-                      out_format: str = "bf16", h_out: torch.Tensor | None = None):
-    """h = residual + x (in residual's dtype, bf16 or fp32; h = x without a
-    residual), y = norm_w * h / sqrt(mean(h^2) + eps).
-
-    Returns (y, scales, h): y bf16 [T][d] and scales None, or with
-    out_format="mxfp8" E4M3 codes uint8 [T][d] and E8M0 scales uint8
-    [T][d/32]; h None without a residual.  h_out may be the residual itself.
-    stream=...: the stream to run on."""
-    if out_format not in _OUT_FORMATS:
-        raise ValueError(f"out_format must be one of {sorted(_OUT_FORMATS)}")
-    if x.dim() != 2:
-        raise ValueError("x must be [T][d]")
-    shape = x.shape
-    T, d = shape
-    ldx = _rows("x", x, (_BF16,), shape)
-    dev = _device_of(x)
-    _norm_weight(norm_w, d)
-    _on_device(dev, norm_w=norm_w)
-    mx = out_format == "mxfp8"
-    y = torch.empty(shape, dtype=_U8 if mx else _BF16, device=x.device)
-    s = torch.empty(T, d // 32, dtype=_U8, device=x.device) if mx else None
-    rp = hp = h = None
-    ldr, st = d, 0
-    if residual is not None:
-        ldr = _rows("residual", residual, (_BF16, _F32), shape)
-        st = _STREAM_TYPES[residual.dtype]
-        _on_device(dev, residual=residual, h_out=h_out)
-        if h_out is None:
-            h = torch.empty(shape, dtype=residual.dtype, device=x.device)
-        else:
-            h = h_out
-            _packed("h_out", h, residual.dtype, shape)
-        rp, hp = residual.data_ptr(), h.data_ptr()
-    elif h_out is not None:
-        raise ValueError("h_out needs a residual")
-    status = B.load_library().lmoe_add_rms_norm(
-        x.data_ptr(), ldx, rp, ldr, st, T, d, norm_w.data_ptr(), eps, hp, y.data_ptr(), _OUT_FORMATS[out_format],
-        s.data_ptr() if mx else None, _raw_stream(dev))
-    if status:
-        raise B.LmoeError("lmoe_add_rms_norm", status)
-    return y, s, h
-
-
-@_on_stream
-def lmoe_add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, norm_w: torch.Tensor, eps: float,
-                               dh: torch.Tensor | None = None):
-    """Gradients of lmoe_add_rms_norm from dy bf16 [T][d] and its h (bf16 or
-    fp32); dh (h's dtype): the gradient along the residual stream.  Returns
-    (dx in h's dtype, the gradient of x and of the residual alike; d norm_w
-    fp32 [d]).  stream=...: the stream to run on."""
-    if h.dim() != 2:
-        raise ValueError("h must be [T][d]")
-    shape = h.shape
-    T, d = shape
-    ldh = _rows("h", h, (_BF16, _F32), shape)
-    lddy = _rows("dy", dy, (_BF16,), shape)
-    lddh = d if dh is None else _rows("dh", dh, (h.dtype,), shape)
-    dev = _device_of(h)
-    _norm_weight(norm_w, d)
-    _on_device(dev, dy=dy, norm_w=norm_w, dh=dh)
-    lib = B.load_library()
-    n = ctypes.c_size_t()
-    B._check("lmoe_add_rms_norm_backward_workspace",
-             lib.lmoe_add_rms_norm_backward_workspace(T, d, ctypes.byref(n)))
-    dx = torch.empty(shape, dtype=h.dtype, device=h.device)
-    dw = torch.empty(d, dtype=_F32, device=h.device)
-    ws = torch.empty(n.value, dtype=_U8, device=h.device)
-    status = lib.lmoe_add_rms_norm_backward(
-        dy.data_ptr(), lddy, h.data_ptr(), ldh, None if dh is None else dh.data_ptr(), lddh, _STREAM_TYPES[h.dtype],
-        T, d, norm_w.data_ptr(), eps, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), n.value, _raw_stream(dev))
-    if status:
-        raise B.LmoeError("lmoe_add_rms_norm_backward", status)
-    return dx, dw
 
 
 class GatedFFN:
@@ -182,7 +201,7 @@ class GatedFFN:
         for n, shape in shapes.items():
             t = weights[n]
             _packed(n, t, gate.dtype, shape)
-            _on_device(_device_of(gate), **{n: t})
+            _on_device(_device_of(gate), t)
             self._weights[n] = t
         self.d_model, self.d_ff, self.max_tokens, self.act = d, F, int(max_tokens), act
         self.training = bool(training)
@@ -206,7 +225,7 @@ class GatedFFN:
         if out is None:
             return torch.empty(T, self.d_model, dtype=_BF16, device=self._device)
         _packed("out", out, _BF16, (T, self.d_model))
-        _on_device(self._dev, out=out)
+        _on_device(self._dev, out)
         return out
 
     @_on_stream
@@ -236,7 +255,7 @@ class GatedFFN:
         lddy = self._tokens(dy, "dy", T)
         _packed("g", g, _BF16, (T, F))
         _packed("u", u, _BF16, (T, F))
-        _on_device(self._dev, g=g, u=u)
+        _on_device(self._dev, g, u)
         grads = [torch.empty(s, dtype=_BF16, device=self._device) if need else None
                  for s, need in (((T, d), need_dx), ((F, d), need_dw), ((F, d), need_dw), ((d, F), need_dw))]
         status = self._lib.lmoe_ffn_backward(
@@ -253,7 +272,7 @@ class GatedFFN:
         T = x_codes.shape[0]
         _packed("x_codes", x_codes, _U8, (T, self.d_model))
         _packed("x_scales", x_scales, _U8, (T, self.d_model // 32))
-        _on_device(self._dev, x_codes=x_codes, x_scales=x_scales)
+        _on_device(self._dev, x_codes, x_scales)
         out = self._out(T, out)
         status = self._lib.lmoe_ffn_forward_mx(self._h, x_codes.data_ptr(), x_scales.data_ptr(), T, out.data_ptr(),
                                                _raw_stream(self._dev))
