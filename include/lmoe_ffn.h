@@ -86,8 +86,8 @@ typedef struct {
 /* gate, up [d_ff][d_model], down [d_model][d_ff]: bf16, or MXFP8 codes with
  * *_s scales.  Borrowed: they stay valid while the handle lives.  bf16
  * weights are read anew by every call, so an optimizer may update them in
- * place between calls (in stream order); MXFP8 scales are laid out for the
- * tensor cores once, by lmoe_ffn_create, and must not change. */
+ * place between calls (in stream order); MXFP8 weights do not change after
+ * lmoe_ffn_create, which lays their scales out for the tensor cores. */
 typedef struct {
   const void* gate;
   const void* up;

@@ -395,8 +395,35 @@ lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8
   if (h->cfg.wfmt != LMOE_FFN_W_MXFP8) return LMOE_ERR_UNSUPPORTED;
   h->launches = 0;
   if (T == 0) return LMOE_OK;
-  if (!usable(x) || !x_scales || !usable(out)) return LMOE_ERR_INVALID_ARG;
+  if (!usable(x) || !usable(x_scales) || !usable(out)) return LMOE_ERR_INVALID_ARG;
   const int d = h->cfg.d_model, F = h->cfg.d_ff;
+  FfnMxSkinnyParams g = {}, n = {};
+  g.T = n.T = T;
+  g.M = F;
+  n.M = d;
+  g.nkb = ceil_div(d, 128);
+  n.nkb = ceil_div(F, 128);
+  if (ffn_mx_skinny_plan(g, true) && ffn_mx_skinny_plan(n, false)) {
+    g.b1 = h->cfg.situ_beta;
+    g.b2 = h->cfg.situ_linear_beta;
+    g.err = n.err = h->err;
+    g.kblks = d / 32;
+    g.b[0] = h->gate;
+    g.b[1] = h->up;
+    g.sfb = h->m_gu_sf;
+    g.row_sf = x_scales;
+    g.out = h->hid;
+    g.out_sf = h->hid_sf;
+    n.b[0] = h->down;
+    n.sfb = h->m_down_sf;
+    n.row_sf = h->hid_sf;
+    n.out = out;
+    if (!map_mx(&g.a, x, d, T, g.tb) || !map_mx(&n.a, h->hid, F, T, n.tb)) return LMOE_ERR_CUDA;
+    FFN_TRY(launch_ffn_mx_skinny(g, true, h->cfg.act == LMOE_ACT_SWIGLU, stream));
+    FFN_TRY(launch_ffn_mx_skinny(n, false, 0, stream));
+    h->launches = 2;
+    return LMOE_OK;
+  }
   FFN_TRY(launch_mx_row_atoms(x_scales, T, d, h->x_sf, stream));
   FfnMxParams p = {};
   p.b1 = h->cfg.situ_beta;

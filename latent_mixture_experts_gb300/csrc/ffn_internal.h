@@ -94,4 +94,20 @@ cudaError_t launch_mx_row_atoms(const uint8_t* s, int T, int K, uint8_t* out, cu
 cudaError_t launch_mx_weight_atoms(const uint8_t* a, const uint8_t* up, int rows, int K, int tiles, uint8_t* out,
                                    cudaStream_t stream);
 
+// Up to kSkinnyMaxTokens tokens: K split over clusters, as in the bf16 form.
+struct FfnMxSkinnyParams {
+  CUtensorMap a, b[2], sfb;     // codes: boxes of 128 K values x tb and 96 rows; the weights' atoms
+  const uint8_t* row_sf;        // gate/up: x's scales [T][kblks]; else hid's atoms
+  void* out;
+  uint8_t* out_sf;              // gate/up: hid's atoms
+  int T, M, nkb, kblks;         // tokens, output features, 128- and 32-wide K blocks
+  int tiles, splits, stages, tb;
+  int sfa_at, recv, reuse_ring; // where in shared memory the tokens' scales lie and the partial sums meet
+  float b1, b2;
+  int* err;
+};
+// Fills the tiling from T, M and nkb; false where the kernel does not take the shape.
+bool ffn_mx_skinny_plan(FfnMxSkinnyParams& p, bool gate_up);
+cudaError_t launch_ffn_mx_skinny(const FfnMxSkinnyParams& p, bool gate_up, int act, cudaStream_t s);
+
 }  // namespace lmoe

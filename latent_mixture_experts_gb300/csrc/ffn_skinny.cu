@@ -26,18 +26,6 @@ constexpr int kThreads = 128;
 constexpr int kCols = 128;       // MMA columns: weight rows of a tile
 constexpr int kMinCtas = 150;    // about one CTA per SM at least
 
-__device__ __forceinline__ void st_cluster4(uint32_t addr, const uint32_t* v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3])
-               : "memory");
-}
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // GU: gate and up rows of 64 features -> act(g, u); else 128 output features
 // of one matrix.
 template <bool GU, int ACT>

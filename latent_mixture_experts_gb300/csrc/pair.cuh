@@ -1,6 +1,5 @@
-// Inline-PTX wrappers for a cluster of two CTAs that work on one tensor-core
-// tile (cta_group::2): barriers of the even CTA reached from the odd one,
-// tensor-memory allocation and MMA of the pair, completion multicast to both.
+// Inline-PTX wrappers for clusters: barriers and shared memory of other CTAs,
+// and the tensor memory of two CTAs that work on one tile (cta_group::2).
 #pragma once
 #include "ptx.cuh"
 
@@ -12,15 +11,27 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 // Barrier of all threads of the cluster; orders their memory accesses.
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
 }
 // Address of CTA `rank`'s copy of a shared variable.
 __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
+}
+// 16 bytes to another CTA's shared memory.
+__device__ __forceinline__ void st_cluster4(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3])
+               : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
