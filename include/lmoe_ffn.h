@@ -55,8 +55,9 @@ LMOE_API lmoe_status lmoe_add_rms_norm(const void* x_bf16, int64_t ldx, const vo
  * dh_opt [T][d] (h's type): the gradient that reaches h along the residual
  * stream, or NULL.  dx may be dh (lddh = d).  workspace: 16-byte aligned,
  * lmoe_add_rms_norm_backward_workspace bytes, contents irrelevant.  The sums
- * over rows are added in an order that depends on T and d only.  T = 0
- * writes dw = 0.  Errors as above. */
+ * over rows are added in an order that depends on T, d and the types only.
+ * T = 0 writes dw = 0.  A bounded wait of the kernel that runs out (there is
+ * no handle to report it by) leaves NaN in dw.  Errors as above. */
 LMOE_API lmoe_status lmoe_add_rms_norm_backward_workspace(int T, int d, size_t* bytes);
 LMOE_API lmoe_status lmoe_add_rms_norm_backward(const void* dy_bf16, int64_t lddy, const void* h, int64_t ldh,
                                                 const void* dh_opt, int64_t lddh, lmoe_stream_type stream_type,

@@ -9,7 +9,9 @@
 // nothing is read twice.  Sums and the norm are fp32; the only roundings are
 // those of the stored outputs.
 #include "common.cuh"
+#include "ffn_internal.h"
 #include "lmoe_internal.h"
+#include "moe_common.cuh"
 
 namespace lmoe {
 namespace {
@@ -150,9 +152,15 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const __grid_constan
       // an infinity or NaN (exponent field 255) makes the block NaN: E8M0 byte 255
       const uint32_t s = m >= 0x7F800000u ? 255u : e4m3_block_scale(__uint_as_float(m));
       const float inv = s == 255u ? 1.0f : e8m0_to_f32(254u - s);
-      uint32_t q[2] = {0, 0};
+      uint32_t q[2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[j >> 2] |= static_cast<uint32_t>(f32_to_e4m3(f[j] * inv)) << (8 * (j & 3));
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * j] * inv, f[4 * j + 1] * inv), __NV_SATFINITE,
+                                                     __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * j + 2] * inv, f[4 * j + 3] * inv),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        q[j] = lo | (hi << 16);
+      }
       if (live && c < p.d) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + row * p.d + c) = make_uint2(q[0], q[1]);
         if ((threadIdx.x & 3) == 0) p.scale[row * (p.d >> 5) + (c >> 5)] = static_cast<uint8_t>(s);
@@ -171,22 +179,63 @@ struct NormBwdParams {
   const void* dh;       // gradient along the residual stream, or null
   const __nv_bfloat16* w;
   void* dx;
-  float* part;          // [gridDim.x * groups][d] partial sums of dw
+  float* part;          // [gridDim.x][d] partial sums of dw
   long long lddy, ldh, lddh;
-  int T, d, warps;
+  int T, d, warps, groups, stages;   // warps per row, rows at a time, rows in flight for each
   float eps;
 };
+// Compute warps of a CTA: two rows of up to 8192 values at once (4096 rows of
+// 7168: 38 us against 45 us with one), while the wider rows' registers allow
+// 16 warps and narrower rows gain nothing from more (4096 rows of 256: 10 us
+// with 16 rows at once, 15 us with 28).
+constexpr int bwd_max_warps(int vpt) { return vpt == 2 ? 28 : 16; }
+constexpr int kBwdMaxWarps = 28, kBwdMaxStages = 8;
+constexpr int kBwdSmem = 208 * 1024;
+static_assert(10 * kNormMaxWidth <= kBwdSmem, "a row fits");
 
-// One CTA takes rows blockIdx.x * groups + group, + gridDim.x * groups, ...:
-// the column sums of dw stay in its registers until the last row.
+// One CTA per SM.  Each group of warps takes every (gridDim.x * groups)-th row
+// and keeps its column sums of dw in registers until the last one.  Rows come
+// by bulk copies into a ring of shared memory, issued by a warp of their own
+// several rows ahead, so that HBM streams while a row is reduced, and
+// registers hold only the sums: the row is read from shared memory twice.
 template <class R, bool HAS_DH, int VPT>
-__global__ void __launch_bounds__(512) rms_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
-  __shared__ float slots[2][2][kMaxRowWarps];
-  const int group = (threadIdx.x >> 5) / p.warps;
-  const int groups = blockDim.x / (32 * p.warps);
+__global__ void __launch_bounds__(32 * bwd_max_warps(VPT) + 32) rms_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[kBwdMaxWarps * kBwdMaxStages], empty[kBwdMaxWarps * kBwdMaxStages];
+  __shared__ float slots[2][2][kBwdMaxWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / p.warps;                      // == groups: the copying warp
   const int t = threadIdx.x - group * 32 * p.warps, stride = 32 * p.warps;
+  const uint32_t dy_bytes = 2 * p.d, h_bytes = sizeof(R) * p.d;
+  const uint32_t row_bytes = dy_bytes + h_bytes * (HAS_DH ? 2 : 1);
+  const long long step = static_cast<long long>(gridDim.x) * p.groups;
+  if (threadIdx.x < p.groups * p.stages) {
+    mbar_init(&full[threadIdx.x], 1);
+    mbar_init(&empty[threadIdx.x], p.warps);
+    fence_mbar_init();
+  }
+  __syncthreads();
   griddep_launch();
   griddep_wait();
+  if (warp == p.groups * p.warps) {
+    // lane g feeds group g
+    if (lane < p.groups) {
+      int s = 0;
+      uint32_t phase = 1;       // the first round of the ring finds its slots empty
+      for (long long row = static_cast<long long>(blockIdx.x) * p.groups + lane; row < p.T; row += step) {
+        const int b = lane * p.stages + s;
+        if (!mbar_wait(&empty[b], phase)) break;
+        uint8_t* dst = ring + static_cast<size_t>(b) * row_bytes;
+        mbar_arrive_expect_tx(&full[b], row_bytes);
+        bulk_g2s(dst, p.dy + row * p.lddy, dy_bytes, &full[b]);
+        bulk_g2s(dst + dy_bytes, static_cast<const R*>(p.h) + row * p.ldh, h_bytes, &full[b]);
+        if constexpr (HAS_DH)
+          bulk_g2s(dst + dy_bytes + h_bytes, static_cast<const R*>(p.dh) + row * p.lddh, h_bytes, &full[b]);
+        if (++s == p.stages) s = 0, phase ^= 1;
+      }
+    }
+    return;
+  }
   Vec8<__nv_bfloat16> wv[VPT];
   float acc[VPT][8];
 #pragma unroll
@@ -197,82 +246,109 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_kernel(const __grid_constant
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
   }
-  int flip = 0;
-  for (long long row0 = static_cast<long long>(blockIdx.x) * groups; row0 < p.T;
-       row0 += static_cast<long long>(gridDim.x) * groups, flip ^= 1) {
-    const long long row = row0 + group;
-    const bool live = row < p.T;
-    Vec8<__nv_bfloat16> gv[VPT];
-    Vec8<R> hv[VPT], ev[VPT];
+  const float inv_d = 1.0f / static_cast<float>(p.d);
+  int s = 0, flip = 0;
+  uint32_t phase = 0;
+  for (long long row = static_cast<long long>(blockIdx.x) * p.groups + group; row < p.T; row += step, flip ^= 1) {
+    const int b = group * p.stages + s;
+    if (!mbar_wait(&full[b], phase)) {
+      // A bounded wait ran out, and no handle carries an error flag: dw becomes
+      // NaN.  Copies in flight get a millisecond to land.
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = __int_as_float(0x7FC00000);
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+      break;
+    }
+    const uint8_t* src = ring + static_cast<size_t>(b) * row_bytes;
+    const __nv_bfloat16* dy = reinterpret_cast<const __nv_bfloat16*>(src);
+    const R* h = reinterpret_cast<const R*>(src + dy_bytes);
+    const R* dh = reinterpret_cast<const R*>(src + dy_bytes + h_bytes);
     float ss = 0.0f, sc = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (t + i * stride) * 8;
-      gv[i].zero();
-      hv[i].zero();
-      if (live && c < p.d) {
-        gv[i].load(p.dy + row * p.lddy + c);
-        hv[i].load(static_cast<const R*>(p.h) + row * p.ldh + c);
-        if constexpr (HAS_DH) ev[i].load(static_cast<const R*>(p.dh) + row * p.lddh + c);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      float g[8], h[8], w[8];
-      gv[i].get(g);
-      hv[i].get(h);
+      if (c >= p.d) continue;
+      Vec8<__nv_bfloat16> gv;
+      Vec8<R> hv;
+      float g[8], x[8], w[8];
+      gv.load(dy + c);
+      hv.load(h + c);
+      gv.get(g);
+      hv.get(x);
       wv[i].get(w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        ss += h[j] * h[j];
-        sc += g[j] * w[j] * h[j];
+        ss += x[j] * x[j];
+        sc += g[j] * w[j] * x[j];
       }
     }
-    // two sums behind one barrier; the slots alternate between rows, so the
-    // next row's writes cannot meet this row's reads
+    // two sums behind one barrier of the group; the slots alternate between
+    // rows, so the next row's writes cannot meet this row's reads
     ss = warp_sum(ss);
     sc = warp_sum(sc);
     if (p.warps > 1) {
-      const int wi = (threadIdx.x >> 5) - group * p.warps, lane = threadIdx.x & 31;
       float* s0 = slots[flip][0] + group * p.warps;
       float* s1 = slots[flip][1] + group * p.warps;
-      if (lane == 0) s0[wi] = ss, s1[wi] = sc;
-      __syncthreads();
+      if (lane == 0) s0[warp - group * p.warps] = ss, s1[warp - group * p.warps] = sc;
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(32 * p.warps) : "memory");
       ss = warp_sum(lane < p.warps ? s0[lane] : 0.0f);
       sc = warp_sum(lane < p.warps ? s1[lane] : 0.0f);
     }
-    const float inv_d = 1.0f / static_cast<float>(p.d);
-    const float rho = rsqrtf(ss / static_cast<float>(p.d) + p.eps);
+    const float rho = rsqrtf(ss * inv_d + p.eps);
     const float k = rho * rho * (sc * inv_d);
-    if (live) {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = (t + i * stride) * 8;
-        if (c >= p.d) continue;
-        float g[8], h[8], w[8], e[8], o[8];
-        gv[i].get(g);
-        hv[i].get(h);
-        wv[i].get(w);
-        if constexpr (HAS_DH) ev[i].get(e);
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (t + i * stride) * 8;
+      if (c >= p.d) continue;
+      Vec8<__nv_bfloat16> gv;
+      Vec8<R> hv, ev, ov;
+      float g[8], x[8], w[8], e[8], o[8];
+      gv.load(dy + c);
+      hv.load(h + c);
+      if constexpr (HAS_DH) ev.load(dh + c);
+      gv.get(g);
+      hv.get(x);
+      wv[i].get(w);
+      if constexpr (HAS_DH) ev.get(e);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          o[j] = rho * (w[j] * g[j] - h[j] * k);
-          if constexpr (HAS_DH) o[j] += e[j];
-          acc[i][j] += g[j] * (h[j] * rho);
-        }
-        Vec8<R> ov;
-        ov.set(o);
-        ov.store(static_cast<R*>(p.dx) + row * p.d + c);
+      for (int j = 0; j < 8; ++j) {
+        o[j] = rho * (w[j] * g[j] - x[j] * k);
+        if constexpr (HAS_DH) o[j] += e[j];
+        acc[i][j] += g[j] * (x[j] * rho);
       }
+      ov.set(o);
+      ov.store(static_cast<R*>(p.dx) + row * p.d + c);
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[b]);
+    if (++s == p.stages) s = 0, phase ^= 1;
   }
-  float* part = p.part + (static_cast<size_t>(blockIdx.x) * groups + group) * p.d;
+  // One row of partial sums per CTA: its groups' sums meet in the ring, once
+  // all of them are done with it, and are added in order.
+  float* const out = p.part + static_cast<size_t>(blockIdx.x) * p.d;
+  float* part = out;
+  const int threads = 32 * p.warps * p.groups;
+  if (p.groups > 1) {
+    asm volatile("bar.sync 0, %0;" ::"r"(threads) : "memory");
+    part = reinterpret_cast<float*>(ring) + group * p.d;
+  }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = (t + i * stride) * 8;
     if (c < p.d) {
       reinterpret_cast<float4*>(part + c)[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
       reinterpret_cast<float4*>(part + c)[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
+  }
+  if (p.groups > 1) {
+    asm volatile("bar.sync 0, %0;" ::"r"(threads) : "memory");
+    for (int c = threadIdx.x; c < p.d; c += threads) {
+      float v = 0.0f;
+      for (int g = 0; g < p.groups; ++g) v += reinterpret_cast<const float*>(ring)[g * p.d + c];
+      out[c] = v;
     }
   }
 }
@@ -329,28 +405,49 @@ cudaError_t launch_fwd(const NormParams& p, const RowPlan& r, cudaStream_t s) {
   }
 }
 
-template <class R, bool HAS_DH>
-cudaError_t launch_bwd(const NormBwdParams& p, const RowPlan& r, int grid, cudaStream_t s) {
-  const dim3 block(32 * r.warps * r.groups);
-  switch (r.vpt) {
-    case 1: return launch_pdl(rms_norm_bwd_kernel<R, HAS_DH, 1>, dim3(grid), block, 0, s, p);
-    case 2: return launch_pdl(rms_norm_bwd_kernel<R, HAS_DH, 2>, dim3(grid), block, 0, s, p);
-    default: return launch_pdl(rms_norm_bwd_kernel<R, HAS_DH, 4>, dim3(grid), block, 0, s, p);
-  }
+// Backward: rows at a time, and how many CTAs.
+struct BwdPlan {
+  int vpt, warps, groups, grid;
+};
+constexpr int kBwdCtas = 152;        // one per SM
+constexpr int kBwdRows = 4;          // rows of a group at least: each group adds a row of partial sums
+BwdPlan bwd_plan(int T, int d) {
+  const RowPlan r = row_plan(d, 512);
+  BwdPlan b = {r.vpt, r.warps, bwd_max_warps(r.vpt) / r.warps, 1};
+  // one row of the widest types (bf16 and two fp32 values) fits the ring for each group
+  const int fit = kBwdSmem / (10 * d);
+  if (b.groups > fit) b.groups = fit;
+  const int need = (T + kBwdRows * b.groups - 1) / (kBwdRows * b.groups);
+  b.grid = need < kBwdCtas ? need : kBwdCtas;
+  return b;
 }
 
-constexpr int kBwdCtas = 304;    // two CTAs for each SM
-int bwd_grid(int T, const RowPlan& r) {
-  const int need = (T + r.groups - 1) / r.groups;
-  return need < kBwdCtas ? need : kBwdCtas;
+template <class R, bool HAS_DH, int VPT>
+cudaError_t launch_bwd_vpt(const NormBwdParams& p, int grid, cudaStream_t s) {
+  static const cudaError_t attr = cudaFuncSetAttribute(rms_norm_bwd_kernel<R, HAS_DH, VPT>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+  if (attr != cudaSuccess) return attr;
+  const size_t smem = static_cast<size_t>(p.groups) * p.stages * p.d * (2 + sizeof(R) * (HAS_DH ? 2 : 1));
+  return launch_pdl(rms_norm_bwd_kernel<R, HAS_DH, VPT>, dim3(grid), dim3(32 * (p.warps * p.groups + 1)), smem, s, p);
 }
-RowPlan bwd_plan(int d) { return row_plan(d, 512); }
+template <class R, bool HAS_DH>
+cudaError_t launch_bwd(NormBwdParams& p, const BwdPlan& b, cudaStream_t s) {
+  const int row = p.d * (2 + static_cast<int>(sizeof(R)) * (HAS_DH ? 2 : 1));
+  const int fit = kBwdSmem / (b.groups * row);
+  if (fit < 1) return cudaErrorInvalidValue;        // not for d <= kNormMaxWidth
+  p.stages = fit < kBwdMaxStages ? fit : kBwdMaxStages;
+  switch (b.vpt) {
+    case 1: return launch_bwd_vpt<R, HAS_DH, 1>(p, b.grid, s);
+    case 2: return launch_bwd_vpt<R, HAS_DH, 2>(p, b.grid, s);
+    default: return launch_bwd_vpt<R, HAS_DH, 4>(p, b.grid, s);
+  }
+}
 
 }  // namespace
 
 size_t rms_norm_bwd_partials(int T, int d) {
-  const RowPlan r = bwd_plan(d);
-  return static_cast<size_t>(bwd_grid(T, r)) * r.groups * d;
+  const BwdPlan b = bwd_plan(T, d);
+  return static_cast<size_t>(b.grid) * d;
 }
 
 cudaError_t launch_add_rms_norm(const void* x, long long ldx, const void* r, long long ldr, bool r_fp32, int T, int d,
@@ -367,7 +464,9 @@ cudaError_t launch_add_rms_norm(const void* x, long long ldx, const void* r, lon
   p.T = T;
   p.d = d;
   p.eps = eps;
-  const RowPlan pl = row_plan(d, 1024);
+  // One vector per thread up to 8192 values (8192 rows of 7168: 79 us against
+  // 90 us with two), four beyond (2048 rows of 16384: 51 us against 57 us).
+  const RowPlan pl = row_plan(d, d <= 8192 ? 1024 : 512);
   p.warps = pl.warps;
   if (!r) return scale ? launch_fwd<float, false, true>(p, pl, s) : launch_fwd<float, false, false>(p, pl, s);
   if (r_fp32) return scale ? launch_fwd<float, true, true>(p, pl, s) : launch_fwd<float, true, false>(p, pl, s);
@@ -390,18 +489,18 @@ cudaError_t launch_rms_norm_bwd(const void* dy, long long lddy, const void* h, l
   p.T = T;
   p.d = d;
   p.eps = eps;
-  const RowPlan pl = bwd_plan(d);
-  p.warps = pl.warps;
-  const int grid = bwd_grid(T, pl);
+  const BwdPlan b = bwd_plan(T, d);
+  p.warps = b.warps;
+  p.groups = b.groups;
   cudaError_t e;
   if (h_fp32)
-    e = dh ? launch_bwd<float, true>(p, pl, grid, s) : launch_bwd<float, false>(p, pl, grid, s);
+    e = dh ? launch_bwd<float, true>(p, b, s) : launch_bwd<float, false>(p, b, s);
   else
-    e = dh ? launch_bwd<__nv_bfloat16, true>(p, pl, grid, s) : launch_bwd<__nv_bfloat16, false>(p, pl, grid, s);
+    e = dh ? launch_bwd<__nv_bfloat16, true>(p, b, s) : launch_bwd<__nv_bfloat16, false>(p, b, s);
   if (e != cudaSuccess) return e;
   const int cols = 4 * kSumCols;
   return launch_pdl(sum_rows_kernel, dim3((d + cols - 1) / cols), dim3(kSumCols * kSumRows), 0, s,
-                    static_cast<const float*>(part), grid * pl.groups, d, dw);
+                    static_cast<const float*>(part), b.grid, d, dw);
 }
 
 }  // namespace lmoe
