@@ -21,7 +21,7 @@ struct lmoe_ffn_ctx {
   void* pool = nullptr;
   int* err = nullptr;
   void *hid = nullptr, *dg = nullptr, *du = nullptr;
-  CUtensorMap gate, up, down;         // K contiguous, boxes of 64 x 128 rows
+  CUtensorMap gate[2], up[2], down[2];   // K contiguous, boxes of 64 x 128 and 64 x 64 rows; MXFP8: [0] only
   CUtensorMap gate_n, up_n, down_n;   // the same memory as N contiguous operands, boxes of 64 x 64
   // MXFP8 blocks: hid holds codes; scale atoms of x, hid and the weights
   uint8_t *x_sf = nullptr, *hid_sf = nullptr, *gu_sf = nullptr, *down_sf = nullptr;
@@ -45,9 +45,9 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 bool usable(const void* p) { return p && aligned16(p); }
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// K-contiguous bf16 operand [rows][K]: boxes of 64 K values x 128 rows.
-bool map_k(CUtensorMap* m, const void* base, int K, int rows, long long ld) {
-  return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, K, rows, 2 * ld, 64, 128,
+// K-contiguous bf16 operand [rows][K]: boxes of 64 K values x `box` rows.
+bool map_k(CUtensorMap* m, const void* base, int K, int rows, long long ld, int box = 128) {
+  return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, K, rows, 2 * ld, 64, box,
                       CU_TENSOR_MAP_SWIZZLE_128B);
 }
 // The transposed use of [K][N]: boxes of 64 N values x 64 K rows.
@@ -217,15 +217,18 @@ lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* 
     e = launch_mx_weight_atoms(w->gate_s, w->up_s, F, d, static_cast<int>(gu_tiles), h->gu_sf, stream);
     if (e == cudaSuccess)
       e = launch_mx_weight_atoms(w->down_s, nullptr, d, F, static_cast<int>(down_tiles), h->down_sf, stream);
-    ok = map_mx(&h->gate, w->gate, d, F, kMxTileN / 2) && map_mx(&h->up, w->up, d, F, kMxTileN / 2) &&
-         map_mx(&h->down, w->down, F, d, kMxTileN / 2) && map_atoms(&h->m_x_sf, h->x_sf, x_sf, 1) &&
+    ok = map_mx(&h->gate[0], w->gate, d, F, kMxTileN / 2) && map_mx(&h->up[0], w->up, d, F, kMxTileN / 2) &&
+         map_mx(&h->down[0], w->down, F, d, kMxTileN / 2) && map_atoms(&h->m_x_sf, h->x_sf, x_sf, 1) &&
          map_atoms(&h->m_hid_sf, h->hid_sf, hid_sf, 1) && map_atoms(&h->m_gu_sf, h->gu_sf, gu_sf, 2) &&
          map_atoms(&h->m_down_sf, h->down_sf, down_sf, 2);
   } else {
     h->dg = base + 256 + act_bytes;
     h->du = base + 256 + 2 * act_bytes;
-    ok = map_k(&h->gate, w->gate, d, F, d) && map_k(&h->up, w->up, d, F, d) && map_k(&h->down, w->down, F, d, F) &&
-         map_n(&h->gate_n, w->gate, d, F, d) && map_n(&h->up_n, w->up, d, F, d) &&
+    ok = true;
+    for (int i = 0; i < 2; ++i)
+      ok = ok && map_k(&h->gate[i], w->gate, d, F, d, 128 >> i) && map_k(&h->up[i], w->up, d, F, d, 128 >> i) &&
+           map_k(&h->down[i], w->down, F, d, F, 128 >> i);
+    ok = ok && map_n(&h->gate_n, w->gate, d, F, d) && map_n(&h->up_n, w->up, d, F, d) &&
          map_n(&h->down_n, w->down, F, d, F);
   }
   // calls on other streams may follow: the workspace is ready when this returns
@@ -288,26 +291,25 @@ lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int 
   p.act = h->cfg.act == LMOE_ACT_SWIGLU;
   p.err = h->err;
   p.nprod = 1;
-  p.b[0] = h->gate;
-  p.b[1] = h->up;
   p.M[0] = T;
   p.N[0] = F;
-  p.tiles_n[0] = ceil_div(F, 128);
-  p.tile_end[0] = ceil_div(T, 256) * p.tiles_n[0];
   p.nkb = p.nkb0 = ceil_div(d, 64);
   p.out[0] = h->hid;
   p.out[1] = gate;
   p.out[2] = up;
+  int tn = ffn_pair_tiles(p, kFfnGateUp, h->ctas);
+  p.b[0] = h->gate[tn == 128];
+  p.b[1] = h->up[tn == 128];
   if (!map_k(&p.a[0], x, d, T, ldx)) return LMOE_ERR_CUDA;
-  FFN_TRY(launch_ffn_pair(kFfnGateUp, p, h->ctas, stream));
-  p.b[0] = h->down;
+  FFN_TRY(launch_ffn_pair(kFfnGateUp, p, tn, h->ctas, stream));
   p.N[0] = d;
-  p.tiles_n[0] = ceil_div(d, 256);
-  p.tile_end[0] = ceil_div(T, 256) * p.tiles_n[0];
   p.nkb = p.nkb0 = ceil_div(F, 64);
   p.out[0] = out;
+  p.out[1] = p.out[2] = nullptr;
+  tn = ffn_pair_tiles(p, kFfnPlain, h->ctas);
+  p.b[0] = h->down[tn == 128];
   if (!map_k(&p.a[0], h->hid, F, T, F)) return LMOE_ERR_CUDA;
-  FFN_TRY(launch_ffn_pair(kFfnPlain, p, h->ctas, stream));
+  FFN_TRY(launch_ffn_pair(kFfnPlain, p, tn, h->ctas, stream));
   h->launches = 2;
   return LMOE_OK;
 }
@@ -345,36 +347,29 @@ lmoe_status lmoe_ffn_backward(lmoe_ffn_handle h, const void* x, int64_t ldx, con
   p.out[2] = h->hid;
   p.M[0] = T;
   p.N[0] = F;
-  p.tiles_n[0] = ceil_div(F, 256);
-  p.tile_end[0] = ceil_div(T, 256) * p.tiles_n[0];
   p.nkb = p.nkb0 = ceil_div(d, 64);
   if (!map_k(&p.a[0], dy, d, T, lddy)) return LMOE_ERR_CUDA;
-  FFN_TRY(launch_ffn_pair(kFfnDHid, p, h->ctas, stream));
+  FFN_TRY(launch_ffn_pair(kFfnDHid, p, ffn_pair_tiles(p, kFfnDHid, h->ctas), h->ctas, stream));
   h->launches = 1;
   if (dx) {   // dx = [dg | du] [gate ; up]
     p.b[0] = h->gate_n;
     p.b[1] = h->up_n;
     p.out[0] = dx;
+    p.out[1] = p.out[2] = nullptr;
     p.N[0] = d;
-    p.tiles_n[0] = ceil_div(d, 256);
-    p.tile_end[0] = ceil_div(T, 256) * p.tiles_n[0];
     p.nkb0 = ceil_div(F, 64);
     p.nkb = 2 * p.nkb0;
     if (!map_k(&p.a[0], h->dg, F, T, F) || !map_k(&p.a[1], h->du, F, T, F)) return LMOE_ERR_CUDA;
-    FFN_TRY(launch_ffn_pair(kFfnDx, p, h->ctas, stream));
+    FFN_TRY(launch_ffn_pair(kFfnDx, p, ffn_pair_tiles(p, kFfnDx, h->ctas), h->ctas, stream));
     ++h->launches;
   }
   if (dwg || dwu || dwd) {
     p.nprod = 0;
-    int tiles = 0;
     auto add = [&](const void* a, long long lda, int M, const void* b, long long ldb, int N, void* out) {
       const int i = p.nprod++;
       p.out[i] = out;
       p.M[i] = M;
       p.N[i] = N;
-      p.tiles_n[i] = ceil_div(N, 256);
-      tiles += ceil_div(M, 256) * p.tiles_n[i];
-      p.tile_end[i] = tiles;
       return map_n(&p.a[i], a, M, T, lda) && map_n(&p.b[i], b, N, T, ldb);
     };
     bool ok = true;
@@ -383,7 +378,7 @@ lmoe_status lmoe_ffn_backward(lmoe_ffn_handle h, const void* x, int64_t ldx, con
     if (dwd) ok = ok && add(dy, lddy, d, h->hid, F, F, dwd);
     if (!ok) return LMOE_ERR_CUDA;
     p.nkb = p.nkb0 = ceil_div(T, 64);
-    FFN_TRY(launch_ffn_pair(kFfnDw, p, h->ctas, stream));
+    FFN_TRY(launch_ffn_pair(kFfnDw, p, ffn_pair_tiles(p, kFfnDw, h->ctas), h->ctas, stream));
     ++h->launches;
   }
   return LMOE_OK;
@@ -408,13 +403,13 @@ lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8
     g.b2 = h->cfg.situ_linear_beta;
     g.err = n.err = h->err;
     g.kblks = d / 32;
-    g.b[0] = h->gate;
-    g.b[1] = h->up;
+    g.b[0] = h->gate[0];
+    g.b[1] = h->up[0];
     g.sfb = h->m_gu_sf;
     g.row_sf = x_scales;
     g.out = h->hid;
     g.out_sf = h->hid_sf;
-    n.b[0] = h->down;
+    n.b[0] = h->down[0];
     n.sfb = h->m_down_sf;
     n.row_sf = h->hid_sf;
     n.out = out;
@@ -430,8 +425,8 @@ lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8
   p.b2 = h->cfg.situ_linear_beta;
   p.act = h->cfg.act == LMOE_ACT_SWIGLU;
   p.err = h->err;
-  p.b[0] = h->gate;
-  p.b[1] = h->up;
+  p.b[0] = h->gate[0];
+  p.b[1] = h->up[0];
   p.sfa = h->m_x_sf;
   p.sfb = h->m_gu_sf;
   p.out = h->hid;
@@ -444,7 +439,7 @@ lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8
   p.nkb = ceil_div(d, 128);
   if (!map_mx(&p.a, x, d, T, 128)) return LMOE_ERR_CUDA;
   FFN_TRY(launch_ffn_mx_pair(p, true, h->ctas, stream));
-  p.b[0] = h->down;
+  p.b[0] = h->down[0];
   p.sfa = h->m_hid_sf;
   p.sfb = h->m_down_sf;
   p.out = out;

@@ -1,5 +1,7 @@
 // The products of the dense feed-forward block on large batches: bf16, fp32
-// accumulation in tensor memory, one 256 x 256 output tile per pair of CTAs.
+// accumulation in tensor memory, one 256 x 256 output tile per pair of CTAs
+// (256 x 128 where those leave pairs idle: half the products and half the
+// epilogue of a tile, but half as much again to load for each product).
 //
 // A pair shares one tcgen05.mma (cta_group::2, M = 256, N = 256): each CTA
 // stages 128 rows of A and 128 of B, so a 64-wide K block costs 32 KB of
@@ -26,10 +28,15 @@
 namespace lmoe {
 namespace {
 
-constexpr int kStages = 6;
-constexpr int kOperand = 16384;              // 128 rows x 64 bf16
-constexpr int kStage = 2 * kOperand;
-constexpr int kPairSmem = kStages * kStage + 1024;
+// TN: columns of a tile.
+template <int TN>
+struct PairCfg {
+  static constexpr int kA = 16384;           // 128 rows x 64 bf16
+  static constexpr int kB = TN / 2 * 128;
+  static constexpr int kStage = kA + kB;
+  static constexpr int kStages = TN == 256 ? 6 : 8;
+  static constexpr int kSmem = kStages * kStage + 1024;
+};
 constexpr int kEpiPairWarps = 8;             // two for each TMEM lane quarter
 constexpr int kPairThreads = 64 + 32 * kEpiPairWarps;
 constexpr int kTileRows = 8;                 // tile rows of one raster group
@@ -51,112 +58,134 @@ __device__ __forceinline__ Tile tile_of(const FfnPairParams& p, int i) {
   return t;
 }
 
-__device__ __forceinline__ void store16(__nv_bfloat16* dst, const uint32_t (&w)[8], int left) {
-  if (left >= 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-  if (left >= 16) *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+// 32 bf16 columns of this thread's row, as far as `left` (a multiple of 8)
+// goes; `wide`: rows start on 32-byte boundaries, and whole sectors move per
+// instruction.
+__device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&w)[16], int left, bool wide) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 8) {
+    if (wide && left >= 2 * i + 16) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 2 * i), "r"(w[i]),
+                   "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
+                   "r"(w[i + 7])
+                   : "memory");
+    } else {
+      if (left >= 2 * i + 8) *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+      if (left >= 2 * i + 16)
+        *reinterpret_cast<uint4*>(dst + 2 * i + 8) = make_uint4(w[i + 4], w[i + 5], w[i + 6], w[i + 7]);
+    }
+  }
 }
-__device__ __forceinline__ void load16(const __nv_bfloat16* src, uint32_t (&w)[8], int left) {
-  uint4 a = make_uint4(0, 0, 0, 0), b = a;
-  if (left >= 8) a = *reinterpret_cast<const uint4*>(src);
-  if (left >= 16) b = *reinterpret_cast<const uint4*>(src + 8);
-  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+__device__ __forceinline__ void load32(const __nv_bfloat16* src, uint32_t (&w)[16], int left) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    uint4 a = make_uint4(0, 0, 0, 0);
+    if (left >= 2 * i + 8) a = *reinterpret_cast<const uint4*>(src + 2 * i);
+    w[i] = a.x, w[i + 1] = a.y, w[i + 2] = a.z, w[i + 3] = a.w;
+  }
+}
+__device__ __forceinline__ void pack32(const uint32_t (&v)[32], uint32_t (&w)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
 }
 
-// One row (this thread's) of half a tile's columns, from the CTA's
-// 256-column accumulator at `acc`.  N is a multiple of 8, so a row ends on a
-// 16-byte boundary.  `ready`: waits for the accumulator; what the epilogue
-// reads from memory is requested before, and then one step ahead.
-template <int MODE, int ACT, class Ready>
+// One row (this thread's) of half a tile's columns, from the CTA's TN-column
+// accumulator at `acc`.  N is a multiple of 8, so a row ends on a 16-byte
+// boundary.  `ready`: waits for the accumulator; what the epilogue reads from
+// memory is requested before, and then one step ahead.
+template <int MODE, int ACT, int TN, class Ready>
 __device__ __forceinline__ bool epilogue_row(const FfnPairParams& p, const Tile& t, uint32_t acc, int row,
                                              bool row_ok, int half, Ready ready) {
   const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
+  const bool wide = p.wide[t.prod];
   if constexpr (MODE == kFfnGateUp) {
-    const int n0 = t.n * 128, N = p.N[0];
+    constexpr int kF = TN / 2;      // features of a tile
+    const int n0 = t.n * kF, N = p.N[0];
     const size_t at = static_cast<size_t>(row) * N + n0;
     if (!ready()) return false;
 #pragma unroll 1
-    for (int c = 64 * half; c < 64 * half + 64; c += 16) {
-      if (n0 + c >= N) break;
-      uint32_t g[16], u[16], h[8];
-      tmem_ld16(acc + c, g);
-      tmem_ld16(acc + 128 + c, u);
+    for (int c = kF / 2 * half; c < kF / 2 * (half + 1); c += 32) {
+      const int left = N - n0 - c;
+      if (left <= 0) break;
+      uint32_t g[32], u[32], w[16];
+      tmem_ld32(acc + c, g);
+      tmem_ld32(acc + kF + c, u);
       tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        h[j] = pack_bf16(glu_hidden<ACT>(__uint_as_float(g[2 * j]), __uint_as_float(u[2 * j]), caps),
-                         glu_hidden<ACT>(__uint_as_float(g[2 * j + 1]), __uint_as_float(u[2 * j + 1]), caps));
-      if (row_ok) {
-        const int left = N - n0 - c;
-        store16(static_cast<__nv_bfloat16*>(p.out[0]) + at + c, h, left);
-        if (p.out[1]) {
-          uint32_t w[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] = pack_bf16(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
-          store16(static_cast<__nv_bfloat16*>(p.out[1]) + at + c, w, left);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] = pack_bf16(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
-          store16(static_cast<__nv_bfloat16*>(p.out[2]) + at + c, w, left);
-        }
+      if (p.out[1] && row_ok) {
+        pack32(g, w);
+        store32(static_cast<__nv_bfloat16*>(p.out[1]) + at + c, w, left, wide);
+        pack32(u, w);
+        store32(static_cast<__nv_bfloat16*>(p.out[2]) + at + c, w, left, wide);
       }
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        w[j] = pack_bf16(glu_hidden<ACT>(__uint_as_float(g[2 * j]), __uint_as_float(u[2 * j]), caps),
+                         glu_hidden<ACT>(__uint_as_float(g[2 * j + 1]), __uint_as_float(u[2 * j + 1]), caps));
+      if (row_ok) store32(static_cast<__nv_bfloat16*>(p.out[0]) + at + c, w, left, wide);
     }
   } else {
-    const int n0 = t.n * 256, N = p.N[t.prod], c0 = 128 * half;
+    const int n0 = t.n * TN, N = p.N[t.prod], c0 = TN / 2 * half;
     const size_t at = static_cast<size_t>(row) * N + n0;
     if constexpr (MODE == kFfnDHid) {
       const __nv_bfloat16* gp = static_cast<const __nv_bfloat16*>(p.in_g) + at;
       const __nv_bfloat16* up = static_cast<const __nv_bfloat16*>(p.in_u) + at;
-      uint32_t g[8], u[8], g1[8], u1[8], v[16];
-      load16(gp + c0, g, row_ok ? N - n0 - c0 : 0);
-      load16(up + c0, u, row_ok ? N - n0 - c0 : 0);
+      uint32_t g[16], u[16], v[32];
+      load32(gp + c0, g, row_ok ? N - n0 - c0 : 0);
+      load32(up + c0, u, row_ok ? N - n0 - c0 : 0);
       if (!ready()) return false;
 #pragma unroll 1
-      for (int c = c0; c < c0 + 128; c += 16) {
+      for (int c = c0; c < c0 + TN / 2; c += 32) {
         const int left = N - n0 - c;
         if (left <= 0) break;
-        const int next = row_ok && c + 16 < c0 + 128 ? left - 16 : 0;
-        load16(gp + c + 16, g1, next);
-        load16(up + c + 16, u1, next);
-        tmem_ld16(acc + c, v);
+        tmem_ld32(acc + c, v);
+        uint32_t g1[16], u1[16];
+        const int next = row_ok && c + 32 < c0 + TN / 2 ? left - 32 : 0;
+        load32(gp + c + 32, g1, next);
+        load32(up + c + 32, u1, next);
         tmem_ld_wait();
-        uint32_t dg[8], du[8], h[8];
+        uint32_t h[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 16; ++j) {
           const GluGrad x = glu_grad<ACT>(bf16_lo(g[j]), bf16_lo(u[j]), __uint_as_float(v[2 * j]), caps);
           const GluGrad y = glu_grad<ACT>(bf16_hi(g[j]), bf16_hi(u[j]), __uint_as_float(v[2 * j + 1]), caps);
-          dg[j] = pack_bf16(x.dg, y.dg);
-          du[j] = pack_bf16(x.du, y.du);
+          g[j] = pack_bf16(x.dg, y.dg);
+          u[j] = pack_bf16(x.du, y.du);
           h[j] = pack_bf16(x.hid, y.hid);
-          g[j] = g1[j];
-          u[j] = u1[j];
         }
         if (row_ok) {
-          store16(static_cast<__nv_bfloat16*>(p.out[0]) + at + c, dg, left);
-          store16(static_cast<__nv_bfloat16*>(p.out[1]) + at + c, du, left);
-          store16(static_cast<__nv_bfloat16*>(p.out[2]) + at + c, h, left);
+          store32(static_cast<__nv_bfloat16*>(p.out[0]) + at + c, g, left, wide);
+          store32(static_cast<__nv_bfloat16*>(p.out[1]) + at + c, u, left, wide);
+          store32(static_cast<__nv_bfloat16*>(p.out[2]) + at + c, h, left, wide);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          g[j] = g1[j];
+          u[j] = u1[j];
         }
       }
     } else {
       if (!ready()) return false;
 #pragma unroll 1
-      for (int c = c0; c < c0 + 128; c += 16) {
+      for (int c = c0; c < c0 + TN / 2; c += 32) {
         const int left = N - n0 - c;
         if (left <= 0) break;
-        uint32_t v[16], w[8];
-        tmem_ld16(acc + c, v);
+        uint32_t v[32], w[16];
+        tmem_ld32(acc + c, v);
         tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-        if (row_ok) store16(static_cast<__nv_bfloat16*>(p.out[t.prod]) + at + c, w, left);
+        pack32(v, w);
+        if (row_ok) store32(static_cast<__nv_bfloat16*>(p.out[t.prod]) + at + c, w, left, wide);
       }
     }
   }
   return true;
 }
 
-template <int MODE, int ACT>
+template <int MODE, int ACT, int TN>
 __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_constant__ FfnPairParams p) {
   constexpr bool kAMn = MODE == kFfnDw;
   constexpr bool kBMn = MODE == kFfnDHid || MODE == kFfnDx || MODE == kFfnDw;
+  using C = PairCfg<TN>;
+  constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
@@ -177,7 +206,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
   }
   cluster_sync();
   if (warp == 1) {
-    tmem_alloc_pair(&tmem_base, 512);
+    tmem_alloc_pair(&tmem_base, 2 * TN);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -201,10 +230,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
           ok = false;
           break;
         }
-        if (rank == 0) w_arrive_expect_tx(&full[s], 2 * kStage);
+        if (rank == 0) w_arrive_expect_tx(&full[s], 2 * C::kStage);
         const uint32_t bar = map_rank(&full[s], 0);
-        uint8_t* sa = sm + s * kStage;
-        uint8_t* sb = sa + kOperand;
+        uint8_t* sa = sm + s * C::kStage;
+        uint8_t* sb = sa + C::kA;
         int src = t.prod, k0 = kb * 64;
         if (MODE == kFfnDx && kb >= p.nkb0) {
           src = 1;
@@ -217,13 +246,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
           w_load_2d_pair(sa, &p.a[src], bar, k0, m0);
         }
         if constexpr (MODE == kFfnGateUp) {   // gate rows in the even CTA, up rows in the odd one
-          w_load_2d_pair(sb, &p.b[rank], bar, k0, t.n * 128);
+          w_load_2d_pair(sb, &p.b[rank], bar, k0, t.n * (TN / 2));
         } else if constexpr (kBMn) {
-          const int n0 = t.n * 256 + 128 * static_cast<int>(rank);
+          const int n0 = t.n * TN + TN / 2 * static_cast<int>(rank);
           w_load_2d_pair(sb, &p.b[src], bar, n0, k0);
-          w_load_2d_pair(sb + 8192, &p.b[src], bar, n0 + 64, k0);
+          if constexpr (TN == 256) w_load_2d_pair(sb + 8192, &p.b[src], bar, n0 + 64, k0);
         } else {
-          w_load_2d_pair(sb, &p.b[src], bar, k0, t.n * 256 + 128 * static_cast<int>(rank));
+          w_load_2d_pair(sb, &p.b[src], bar, k0, t.n * TN + TN / 2 * static_cast<int>(rank));
         }
       }
     }
@@ -238,17 +267,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
     }
   } else if (warp == 1) {
     if (rank == 0) {
-      constexpr uint32_t idesc = idesc_bf16(256, 256) | (kAMn ? kIdescAMajorMn : 0u) | (kBMn ? kIdescBMajorMn : 0u);
+      constexpr uint32_t idesc = idesc_bf16(256, TN) | (kAMn ? kIdescAMajorMn : 0u) | (kBMn ? kIdescBMajorMn : 0u);
       const uint32_t base = smem_u32(sm);
       const uint64_t a_desc = kAMn ? sdesc_sw128_mn(base, 8192) : sdesc_sw128(base);
-      const uint64_t b_desc = kBMn ? sdesc_sw128_mn(base + kOperand, 8192) : sdesc_sw128(base + kOperand);
+      const uint64_t b_desc = kBMn ? sdesc_sw128_mn(base + C::kA, 8192) : sdesc_sw128(base + C::kA);
       uint32_t it = 0, n = 0;
       bool ok = true;
       for (int i = first; i < total && ok; i += pairs, ++n) {
         const uint32_t b = n & 1, use = n >> 1;
         if (use > 0 && !warp_wait(&acc_empty[b], (use - 1) & 1, p.err)) break;
         tc_fence_after();
-        const uint32_t d = tbase + b * 256;
+        const uint32_t d = tbase + b * TN;
         for (int kb = 0; kb < p.nkb; ++kb, ++it) {
           const uint32_t s = it % kStages;
           if (!warp_wait(&full[s], (it / kStages) & 1, p.err)) {
@@ -258,7 +287,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
           tc_fence_after();
           // descriptors count 16-byte units: a step of 16 along K is 32 bytes of
           // a K-contiguous row, or 16 rows of 128 bytes
-          const uint64_t ad = a_desc + s * (kStage >> 4), bd = b_desc + s * (kStage >> 4);
+          const uint64_t ad = a_desc + s * (C::kStage >> 4), bd = b_desc + s * (C::kStage >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             w_mma_bf16_pair(d, ad + k * (kAMn ? 128 : 2), bd + k * (kBMn ? 128 : 2), idesc, (kb | k) != 0);
@@ -281,7 +310,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
       const Tile t = tile_of(p, i);
       const int row0 = t.m * 256 + 128 * static_cast<int>(rank) + 32 * q;
       const bool ok = row0 < p.M[t.prod]
-                          ? epilogue_row<MODE, ACT>(p, t, tbase + b * 256 + (static_cast<uint32_t>(32 * q) << 16),
+                          ? epilogue_row<MODE, ACT, TN>(p, t, tbase + b * TN + (static_cast<uint32_t>(32 * q) << 16),
                                                     row0 + lane, row0 + lane < p.M[t.prod], (warp - 2) >> 2, ready)
                           : ready();
       if (!ok) break;
@@ -293,42 +322,74 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
   __syncwarp();
   tc_fence_before();
   cluster_sync();
-  if (warp == 1) tmem_dealloc_pair(tbase, 512);
+  if (warp == 1) tmem_dealloc_pair(tbase, 2 * TN);
   cluster_sync();      // neither CTA leaves while the other still frees the pair's columns
 }
 
-template <int MODE, int ACT>
-cudaError_t launch(const FfnPairParams& p, int ctas, cudaStream_t s) {
+template <int MODE, int ACT, int TN>
+cudaError_t launch_tn(const FfnPairParams& p, int ctas, cudaStream_t s) {
+  using C = PairCfg<TN>;
   static const cudaError_t attr = cudaFuncSetAttribute(
-      ffn_pair_kernel<MODE, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+      ffn_pair_kernel<MODE, ACT, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (attr != cudaSuccess) return attr;
   const int tiles = p.tile_end[p.nprod - 1];
-  return launch_pdl_cluster(ffn_pair_kernel<MODE, ACT>, dim3(2 * tiles < ctas ? 2 * tiles : ctas), dim3(kPairThreads),
-                            kPairSmem, 2, s, p);
+  return launch_pdl_cluster(ffn_pair_kernel<MODE, ACT, TN>, dim3(2 * tiles < ctas ? 2 * tiles : ctas),
+                            dim3(kPairThreads), C::kSmem, 2, s, p);
+}
+template <int MODE, int ACT>
+cudaError_t launch(const FfnPairParams& p, int tn, int ctas, cudaStream_t s) {
+  return tn == 256 ? launch_tn<MODE, ACT, 256>(p, ctas, s) : launch_tn<MODE, ACT, 128>(p, ctas, s);
 }
 
 }  // namespace
 
-cudaError_t launch_ffn_pair(FfnMode mode, const FfnPairParams& p, int ctas, cudaStream_t s) {
+int ffn_pair_tiles(FfnPairParams& p, FfnMode mode, int ctas) {
+  const auto tiles = [&](int tn) {
+    int n = 0;
+    const int width = mode == kFfnGateUp ? tn / 2 : tn;
+    for (int i = 0; i < p.nprod; ++i) {
+      p.tiles_n[i] = (p.N[i] + width - 1) / width;
+      n += (p.M[i] + 255) / 256 * p.tiles_n[i];
+      p.tile_end[i] = n;
+    }
+    return n;
+  };
+  const int pairs = ctas / 2;
+  const auto waves = [&](int tn) { return (tiles(tn) + pairs - 1) / pairs; };
+  const int narrow = waves(128), wide = waves(256);      // leaves the wide tiling in p
+  // 1 where every output row starts on a 32-byte boundary
+  for (int i = 0; i < p.nprod; ++i) p.wide[i] = p.N[i] % 16 == 0 && reinterpret_cast<uintptr_t>(p.out[i]) % 32 == 0;
+  if (p.nprod == 1)
+    for (int i = 1; i < 3; ++i) p.wide[0] = p.wide[0] && reinterpret_cast<uintptr_t>(p.out[i]) % 32 == 0;
+  // With all SMs busy a narrow tile takes 0.55 to 0.58 of a wide one's time (4096 tokens at 7168 x 6144: forward
+  // 650 us against 593 us); 1003 tokens at 1152 x 864, which leave half of the wide grid idle: 15.9 us against 22.8 us.
+  if (0.57 * narrow < wide) {
+    tiles(128);
+    return 128;
+  }
+  return 256;
+}
+
+cudaError_t launch_ffn_pair(FfnMode mode, const FfnPairParams& p, int tn, int ctas, cudaStream_t s) {
   const bool sw = p.act == 1;
   switch (mode) {
-    case kFfnGateUp: return sw ? launch<kFfnGateUp, 1>(p, ctas, s) : launch<kFfnGateUp, 0>(p, ctas, s);
-    case kFfnPlain: return launch<kFfnPlain, 0>(p, ctas, s);
-    case kFfnDHid: return sw ? launch<kFfnDHid, 1>(p, ctas, s) : launch<kFfnDHid, 0>(p, ctas, s);
-    case kFfnDx: return launch<kFfnDx, 0>(p, ctas, s);
-    case kFfnDw: return launch<kFfnDw, 0>(p, ctas, s);
+    case kFfnGateUp: return sw ? launch<kFfnGateUp, 1>(p, tn, ctas, s) : launch<kFfnGateUp, 0>(p, tn, ctas, s);
+    case kFfnPlain: return launch<kFfnPlain, 0>(p, tn, ctas, s);
+    case kFfnDHid: return sw ? launch<kFfnDHid, 1>(p, tn, ctas, s) : launch<kFfnDHid, 0>(p, tn, ctas, s);
+    case kFfnDx: return launch<kFfnDx, 0>(p, tn, ctas, s);
+    case kFfnDw: return launch<kFfnDw, 0>(p, tn, ctas, s);
   }
   return cudaErrorInvalidValue;
 }
 
 cudaError_t ffn_pair_ctas(int* ctas) {
-  cudaError_t e = cudaFuncSetAttribute(ffn_pair_kernel<kFfnPlain, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kPairSmem);
+  cudaError_t e = cudaFuncSetAttribute(ffn_pair_kernel<kFfnPlain, 0, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       PairCfg<256>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.dynamicSmemBytes = PairCfg<256>::kSmem;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 2;
@@ -337,7 +398,7 @@ cudaError_t ffn_pair_ctas(int* ctas) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, ffn_pair_kernel<kFfnPlain, 0>, &cfg);
+  e = cudaOccupancyMaxActiveClusters(&n, ffn_pair_kernel<kFfnPlain, 0, 256>, &cfg);
   if (e != cudaSuccess) return e;
   *ctas = 2 * (n > 0 ? n : 1);
   return cudaSuccess;

@@ -20,9 +20,9 @@ cudaError_t launch_rms_norm_bwd(const void* dy, long long lddy, const void* h, l
                                 float* part, float* dw, cudaStream_t s);
 
 // ------------------------------------------------------ pair-tile bf16 GEMM
-// C[M][N] (bf16) = A B^T on 256 x 256 tiles of CTA pairs.
+// C[M][N] (bf16) = A B^T on tiles of CTA pairs, 256 rows x 256 or 128 columns.
 enum FfnMode {
-  kFfnGateUp = 0,   // A = x, B = gate | up rows of 128 features; out0 = act(g, u), out1/out2 = g, u when set
+  kFfnGateUp = 0,   // A = x, B = gate | up rows of half a tile's features; out0 = act(g, u), out1/out2 = g, u when set
   kFfnPlain = 1,    // A, B stored K contiguous; out0
   kFfnDHid = 2,     // B stored N contiguous; out0 = dg, out1 = du, out2 = hid from in_g, in_u
   kFfnDx = 3,       // B stored N contiguous, K concatenated over two (A, B); out0
@@ -34,12 +34,16 @@ struct FfnPairParams {
   const void *in_g, *in_u;
   int M[3], N[3];             // output rows and columns of each product
   int tiles_n[3], tile_end[3], nprod;
+  int wide[3];                // outputs whose rows start on 32-byte boundaries
   int nkb, nkb0;              // 64-wide K blocks in all; of the first (A, B) of a concatenation
   float b1, b2;
   int act;
   int* err;
 };
-cudaError_t launch_ffn_pair(FfnMode mode, const FfnPairParams& p, int ctas, cudaStream_t s);
+// Chooses the tile width (128 or 256) for M, N, nprod and out and fills
+// tiles_n, tile_end and wide; K-contiguous B maps have boxes of half of it.
+int ffn_pair_tiles(FfnPairParams& p, FfnMode mode, int ctas);
+cudaError_t launch_ffn_pair(FfnMode mode, const FfnPairParams& p, int tn, int ctas, cudaStream_t s);
 // Largest number of CTAs (an even number) of the pair kernels that run at once.
 cudaError_t ffn_pair_ctas(int* ctas);
 
