@@ -259,9 +259,10 @@ lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int 
   FFN_TRY_STATUS(row_args(x, ldx, d));
   if (!usable(out) || (gate == nullptr) != (up == nullptr) || !aligned16(gate) || !aligned16(up))
     return LMOE_ERR_INVALID_ARG;
-  // Up to 128 tokens stream the weights (ffn_skinny.cu), larger batches run on
-  // pair tiles: at widths 7168 and 6144, 73 us against 83 us for 128 tokens
-  // and, in two blocks of 128, 110 us against 84 us for 256.
+  // Up to 96 tokens stream the weights (ffn_skinny.cu), larger batches run on
+  // pair tiles.  Streaming against pair tiles, widths 7168 and 2048: 64 tokens
+  // 25 us and 33 us, 128 tokens 32 us and 34 us; 7168 and 6144: 64 tokens 56 us
+  // and 61 us, 128 tokens 68 us and 62 us.
   if (T <= kSkinnyMaxTokens) {
     FfnSkinnyParams g = {}, n = {};
     g.T = n.T = T;
@@ -443,6 +444,7 @@ lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8
   p.sfa = h->m_hid_sf;
   p.sfb = h->m_down_sf;
   p.out = out;
+  p.wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;   // d is a multiple of 32
   p.N = d;
   p.tiles_n = ceil_div(d, kMxTileN);
   p.tiles = ceil_div(T, 256) * p.tiles_n;

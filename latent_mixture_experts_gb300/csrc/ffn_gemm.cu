@@ -58,24 +58,7 @@ __device__ __forceinline__ Tile tile_of(const FfnPairParams& p, int i) {
   return t;
 }
 
-// 32 bf16 columns of this thread's row, as far as `left` (a multiple of 8)
-// goes; `wide`: rows start on 32-byte boundaries, and whole sectors move per
-// instruction.
-__device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&w)[16], int left, bool wide) {
-#pragma unroll
-  for (int i = 0; i < 16; i += 8) {
-    if (wide && left >= 2 * i + 16) {
-      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 2 * i), "r"(w[i]),
-                   "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
-                   "r"(w[i + 7])
-                   : "memory");
-    } else {
-      if (left >= 2 * i + 8) *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-      if (left >= 2 * i + 16)
-        *reinterpret_cast<uint4*>(dst + 2 * i + 8) = make_uint4(w[i + 4], w[i + 5], w[i + 6], w[i + 7]);
-    }
-  }
-}
+// 32 columns of this thread's row, zeros past `left`.
 __device__ __forceinline__ void load32(const __nv_bfloat16* src, uint32_t (&w)[16], int left) {
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
@@ -84,11 +67,6 @@ __device__ __forceinline__ void load32(const __nv_bfloat16* src, uint32_t (&w)[1
     w[i] = a.x, w[i + 1] = a.y, w[i + 2] = a.z, w[i + 3] = a.w;
   }
 }
-__device__ __forceinline__ void pack32(const uint32_t (&v)[32], uint32_t (&w)[16]) {
-#pragma unroll
-  for (int j = 0; j < 16; ++j) w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-}
-
 // One row (this thread's) of half a tile's columns, from the CTA's TN-column
 // accumulator at `acc`.  N is a multiple of 8, so a row ends on a 16-byte
 // boundary.  `ready`: waits for the accumulator; what the epilogue reads from

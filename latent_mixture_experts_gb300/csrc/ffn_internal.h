@@ -49,7 +49,7 @@ cudaError_t ffn_pair_ctas(int* ctas);
 
 // ------------------------------------------------------ small-batch passes
 // out[t][f] over all tokens of a batch of at most kSkinnyMaxTokens.
-constexpr int kSkinnyMaxTokens = 128;
+constexpr int kSkinnyMaxTokens = 96;
 constexpr int kSkinnyMaxStages = 16;
 constexpr int kSkinnyMaxSplits = 8;    // K splits: the portable cluster size
 constexpr int kSkinnySmem = 110 * 1024;
@@ -86,6 +86,7 @@ struct FfnMxParams {
   int out_nkb;
   int M, N;                     // tokens, output features
   int tiles_n, tiles, nkb;      // nkb: 128-wide K blocks
+  int wide;                     // bf16 output rows start on 32-byte boundaries
   float b1, b2;
   int act;
   int* err;
@@ -98,7 +99,7 @@ cudaError_t launch_mx_row_atoms(const uint8_t* s, int T, int K, uint8_t* out, cu
 cudaError_t launch_mx_weight_atoms(const uint8_t* a, const uint8_t* up, int rows, int K, int tiles, uint8_t* out,
                                    cudaStream_t stream);
 
-// Up to kSkinnyMaxTokens tokens: K split over clusters, as in the bf16 form.
+// Small batches: K split over clusters, as in the bf16 form.
 struct FfnMxSkinnyParams {
   CUtensorMap a, b[2], sfb;     // codes: boxes of 128 K values x tb and 96 rows; the weights' atoms
   const uint8_t* row_sf;        // gate/up: x's scales [T][kblks]; else hid's atoms

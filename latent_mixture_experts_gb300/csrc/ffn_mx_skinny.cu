@@ -1,4 +1,4 @@
-// The MXFP8 feed-forward passes on small batches (up to 128 tokens), bound by
+// The MXFP8 feed-forward passes on small batches (up to 48 tokens), bound by
 // streaming the weights' codes and scales once from HBM.
 //
 // As in the bf16 form, tokens are the MMA's M rows, weight rows its N columns
@@ -24,7 +24,11 @@ constexpr int kB = kN * 128;             // codes of a 128-wide K chunk
 constexpr int kMaxStages = 5;            // 12 columns of scales each, beside 192 of sums
 constexpr int kTmem = 256, kSfCols = 12;
 constexpr int kPitch = kN + 4;           // floats of a token's partial sums: 16-byte rows, four banks apart
-constexpr int kMinCtas = 150;
+constexpr int kMinCtas = 150;            // one for each SM (16 tokens at 7168 x 6144: 30 us; with 60, 47 us)
+// Up to here against the pair tiles: 48 tokens at widths 7168 and 6144 39.2 us
+// and 38.9 us, at 2048 and 2048 15.7 us and 17.7 us; 64 tokens 42.9 us and
+// 39.1 us, 18.1 us and 18.1 us.
+constexpr int kMxSkinnyMaxTokens = 48;
 static_assert(kN + kMaxStages * kSfCols <= kTmem, "tensor memory");
 
 template <bool GU, int ACT>
@@ -154,13 +158,13 @@ __global__ void __launch_bounds__(kThreads) ffn_mx_skinny_kernel(const __grid_co
     const int owner = t < p.T ? t / per : 0;
     const uint32_t dst = map_rank(recv, owner) + 4 * ((rank * per + t - owner * per) * kPitch);
 #pragma unroll 1
-    for (int c = 0; c < kN; c += 16) {
-      uint32_t v[16];
-      tmem_ld16(tmem_addr(tacc, 32 * q, c), v);
+    for (int c = 0; c < kN; c += 32) {
+      uint32_t v[32];
+      tmem_ld32(tmem_addr(tacc, 32 * q, c), v);
       tmem_ld_wait();
       if (t < p.T)
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) st_cluster4(dst + 4 * (c + j), v + j);
+        for (int j = 0; j < 32; j += 4) st_cluster4(dst + 4 * (c + j), v + j);
     }
   }
   tc_fence_before();
@@ -219,7 +223,7 @@ cudaError_t launch(const FfnMxSkinnyParams& p, cudaStream_t s) {
 }  // namespace
 
 bool ffn_mx_skinny_plan(FfnMxSkinnyParams& p, bool gate_up) {
-  if (p.T > kSkinnyMaxTokens) return false;
+  if (p.T > kMxSkinnyMaxTokens) return false;
   p.tiles = gate_up ? (p.M + kHalf - 1) / kHalf : (p.M + kN - 1) / kN;
   p.tb = (p.T + 7) / 8 * 8;
   p.splits = 1;
@@ -227,9 +231,11 @@ bool ffn_mx_skinny_plan(FfnMxSkinnyParams& p, bool gate_up) {
   const int budget = kSkinnySmem - 1024;
   const int sfa = (p.nkb + p.splits - 1) / p.splits * 512;
   const int recv = 4 * p.splits * ((p.T + p.splits - 1) / p.splits) * kPitch;
-  p.reuse_ring = recv > budget / 3;
+  // the partial sums meet behind the ring, or over it where room behind would cost a stage
+  const int stage = p.tb * 128 + kB + 1024;
+  p.reuse_ring = (budget - sfa - recv) / stage < (budget - sfa) / stage;
   const int ring = (budget - sfa - (p.reuse_ring ? 0 : recv)) / 1024 * 1024;
-  p.stages = ring / (p.tb * 128 + kB + 1024);
+  p.stages = ring / stage;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.sfa_at = ring;
   p.recv = p.reuse_ring ? 0 : ring + sfa;

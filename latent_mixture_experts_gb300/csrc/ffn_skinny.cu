@@ -1,19 +1,18 @@
 // The feed-forward block's two forward passes on small batches (bf16), where
 // streaming the weights once from HBM bounds the time.
 //
-// Tokens are the MMA's M rows (up to 128; rows past the batch are whatever
-// shared memory holds, and only reach output rows that nobody reads), weight
-// rows its N columns.  A cluster of up to 8 CTAs owns `rows` consecutive
-// output features and splits K; its partial sums are joined through
-// distributed shared memory, in rank order, by all of its CTAs.  An MMA costs
-// about the same for 32 columns as for 100 (it reads its 128 token rows either
-// way), so wide tiles with a split K keep up with HBM where one wave of narrow
-// tiles over the whole of K does not: one token at widths 7168 and 6144 takes
-// 48.4 us against 63.0 us, at 7168 and 2048 23.7 us against 32.1 us.  The gate and up rows of
-// the same features arrive side by side, through one tensor map whose third
-// dimension steps from one matrix to the other.  A ring of about 100 KB per
-// CTA puts two CTAs on an SM, and lets the down pass's CTAs load their first
-// weights while the gate/up pass's last ones finish.
+// Tokens are the MMA's M rows (rows past the batch are whatever shared memory
+// holds, and only reach output rows that nobody reads), weight rows its N
+// columns.  A cluster of up to 8 CTAs owns `rows` consecutive output features
+// and splits K; its partial sums are joined through distributed shared memory,
+// in rank order, by all of its CTAs: one token at widths 7168 and 2048 takes
+// 20 us, against 32 us with narrow tiles over the whole of K (an MMA reads its
+// 128 token rows whatever its width).  The gate and up rows of the same
+// features arrive side by side, through one tensor map whose third dimension
+// steps from one matrix to the other.  A ring of about 100 KB per CTA puts two
+// CTAs on an SM, and lets the down pass's CTAs load their first weights while
+// the gate/up pass's last ones finish.  One token at 7168 and 6144: 46 us,
+// 5.7 TB/s of weights.
 #include "ffn_act.cuh"
 #include "ffn_internal.h"
 #include "lmoe_internal.h"
@@ -23,8 +22,11 @@ namespace lmoe {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kCols = 128;       // MMA columns: weight rows of a tile
-constexpr int kMinCtas = 150;    // about one CTA per SM at least
+// MMA columns: weight rows of a tile.  Narrower tiles cost more MMAs (32: one
+// token at widths 7168 and 6144 61 us against 46 us), wider ones more bytes of
+// partial sums (128: 64 tokens at 7168 and 2048 29 us against 25 us; one token
+// 45 us and 19.5 us against 46 us and 20.1 us).
+constexpr int kCols = 64;
 
 // GU: gate and up rows of 64 features -> act(g, u); else 128 output features
 // of one matrix.
@@ -35,10 +37,9 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
   __shared__ uint64_t full[kSkinnyMaxStages], empty[kSkinnyMaxStages], done;
   __shared__ uint32_t tmem_base;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known uniform
-  constexpr int N = kCols;
-  constexpr int kRows = GU ? N / 2 : N;               // features of the cluster
+  constexpr int N = kCols, rows = GU ? N / 2 : N;     // features of the cluster
   const int rank = static_cast<int>(cluster_rank());  // K split of this CTA
-  const int f0 = static_cast<int>(blockIdx.x) / p.splits * kRows;   // first feature
+  const int f0 = static_cast<int>(blockIdx.x) / p.splits * rows;   // first feature
   const int a_chunk = p.tb * 128, b_chunk = N * 128;  // bytes of one 64-wide K chunk
   const int a_slot = a_chunk * p.kc, b_slot = b_chunk * p.kc;
   uint8_t* sb = sm + p.stages * a_slot;
@@ -158,28 +159,23 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
   __syncwarp();
   if (p.reuse_ring) cluster_arrive();
   cluster_wait();
-  const int fs = kRows / p.splits, pitch = N / p.splits + 4;   // 16-byte rows, four banks apart
+  const int lfs = 31 - __clz(rows / p.splits), fs = 1 << lfs, pitch = N / p.splits + 4;   // 16-byte rows, four banks apart
   float* recv = reinterpret_cast<float*>(sm + p.recv);
   const int row = 32 * warp;
   if (row < p.T) {                  // warp-uniform
     const uint32_t at = 4 * ((rank * p.T + row + lane) * pitch);
 #pragma unroll 1
-    for (int o = 0; o < p.splits; ++o) {
-      const uint32_t dst = map_rank(recv, o) + at;
-      for (int c = 0; c < fs; c += 8) {
-        uint32_t v[8], w[8];
-        tmem_ld8(tmem_addr(tacc, 32 * warp, o * fs + c), v);
-        if constexpr (GU) tmem_ld8(tmem_addr(tacc, 32 * warp, kRows + o * fs + c), w);
-        tmem_ld_wait();
-        if (row + lane < p.T) {
-          st_cluster4(dst + 4 * c, v);
-          st_cluster4(dst + 4 * c + 16, v + 4);
-          if constexpr (GU) {
-            st_cluster4(dst + 4 * (fs + c), w);
-            st_cluster4(dst + 4 * (fs + c) + 16, w + 4);
-          }
+    for (int c = 0; c < N; c += 32) {
+      uint32_t v[32];
+      tmem_ld32(tmem_addr(tacc, row, c), v);
+      tmem_ld_wait();
+      if (row + lane < p.T)
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          // four columns have one owner; its block holds fs gate columns, then fs up columns
+          const int up = GU && c + j >= rows, f = c + j - (up ? rows : 0), o = f >> lfs;
+          st_cluster4(map_rank(recv, o) + at + 4 * (f - o * fs + (up ? fs : 0)), v + j);
         }
-      }
     }
   }
   tc_fence_before();
@@ -188,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
   cluster_arrive();
   cluster_wait();
   const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
-  const int shift = 30 - __clz(fs);   // log2 of the pairs of features (fs is a power of two)
+  const int shift = lfs - 1;        // log2 of the pairs of features
   const int f1 = f0 + rank * fs, left = p.M - f1;
   for (int e = threadIdx.x; e < p.T << shift; e += kThreads) {
     const int t = e >> shift, f = 2 * (e - (t << shift));
@@ -240,12 +236,20 @@ bool ffn_skinny_plan(FfnSkinnyParams& p, bool gate_up) {
   // K chunks per stage: up to about 24 KB a stage
   p.kc = chunk <= 6 * 1024 ? 4 : chunk <= 12 * 1024 ? 2 : 1;
   const int all = (p.chunks + p.kc - 1) / p.kc;
+  // Split K until there is a CTA for most SMs, and on to two for each while
+  // that leaves a CTA 12 chunks of K or more (a CTA's fixed costs against what
+  // it streams: at 2048 x 2048 two splits of the gate/up pass 9.1 us, four
+  // 10.5 us; at 7168 x 2048 22.0 us and 20.1 us).
   p.splits = 1;
-  while (p.splits < kSkinnyMaxSplits && tiles * p.splits < kMinCtas && 2 * p.splits <= all)
-    p.splits *= 2;
+  for (int s = 2; s <= kSkinnyMaxSplits; s *= 2) {
+    const int ctas = tiles * p.splits, left = p.chunks / s;
+    if (s > all || !((ctas < 110 && left >= 4) || (ctas < 150 && left >= 12))) break;
+    p.splits = s;
+  }
   const int budget = kSkinnySmem - 1024;
   const int recv = 4 * p.T * (N + 4 * p.splits);
-  p.reuse_ring = recv > budget / 3;
+  // the partial sums meet behind the ring, or over it where room behind would leave fewer than four stages
+  p.reuse_ring = (budget - recv) / (chunk * p.kc) < 4;
   const int ring = p.reuse_ring ? budget : (budget - recv) / 1024 * 1024;
   p.recv = p.reuse_ring ? 0 : ring;
   p.stages = ring / (chunk * p.kc);
