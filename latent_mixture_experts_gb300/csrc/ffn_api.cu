@@ -301,6 +301,8 @@ lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int 
   int tn = ffn_pair_tiles(p, kFfnGateUp, h->ctas);
   p.b[0] = h->gate[tn == 128];
   p.b[1] = h->up[tn == 128];
+  p.b_half[0] = h->gate[1];
+  p.b_half[1] = h->up[1];
   if (!map_k(&p.a[0], x, d, T, ldx)) return LMOE_ERR_CUDA;
   FFN_TRY(launch_ffn_pair(kFfnGateUp, p, tn, h->ctas, stream));
   p.N[0] = d;
@@ -309,6 +311,7 @@ lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int 
   p.out[1] = p.out[2] = nullptr;
   tn = ffn_pair_tiles(p, kFfnPlain, h->ctas);
   p.b[0] = h->down[tn == 128];
+  p.b_half[0] = h->down[1];
   if (!map_k(&p.a[0], h->hid, F, T, F)) return LMOE_ERR_CUDA;
   FFN_TRY(launch_ffn_pair(kFfnPlain, p, tn, h->ctas, stream));
   h->launches = 2;

@@ -1,7 +1,8 @@
 // The products of the dense feed-forward block on large batches: bf16, fp32
 // accumulation in tensor memory, one 256 x 256 output tile per pair of CTAs
-// (256 x 128 where those leave pairs idle: half the products and half the
-// epilogue of a tile, but half as much again to load for each product).
+// (256 x 128 where those leave pairs idle, for the whole grid or its last wave:
+// half the products and half the epilogue of a tile, but half as much again to
+// load for each product).
 //
 // A pair shares one tcgen05.mma (cta_group::2, M = 256, N = 256): each CTA
 // stages 128 rows of A and 128 of B, so a 64-wide K block costs 32 KB of
@@ -41,11 +42,16 @@ constexpr int kEpiPairWarps = 8;             // two for each TMEM lane quarter
 constexpr int kPairThreads = 64 + 32 * kEpiPairWarps;
 constexpr int kTileRows = 8;                 // tile rows of one raster group
 
+// narrow: half a wide tile, at the end of the wide grid; n counts half tiles.
 struct Tile {
   int prod, m, n;
+  bool narrow;
 };
 __device__ __forceinline__ Tile tile_of(const FfnPairParams& p, int i) {
   Tile t;
+  t.narrow = i >= p.full;
+  const int sub = t.narrow ? (i - p.full) & 1 : 0;
+  if (t.narrow) i = p.full + ((i - p.full) >> 1);
   t.prod = 0;
   while (t.prod + 1 < p.nprod && i >= p.tile_end[t.prod]) ++t.prod;
   const int first = t.prod ? p.tile_end[t.prod - 1] : 0;
@@ -55,6 +61,7 @@ __device__ __forceinline__ Tile tile_of(const FfnPairParams& p, int i) {
   const int rows = min(kTileRows, tm - g * kTileRows);
   t.m = g * kTileRows + r % rows;
   t.n = r / rows;
+  if (t.narrow) t.n = 2 * t.n + sub;
   return t;
 }
 
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
   griddep_wait();
   const uint32_t tbase = tmem_base;
   const int pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
-  const int total = p.tile_end[p.nprod - 1];
+  const int total = 2 * p.tile_end[p.nprod - 1] - p.full;   // wide tiles, then halves
 
   if (warp == 0) {
     uint32_t it = 0;
@@ -208,7 +215,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
           ok = false;
           break;
         }
-        if (rank == 0) w_arrive_expect_tx(&full[s], 2 * C::kStage);
+        const bool half = TN == 256 && t.narrow;
+        if (rank == 0) w_arrive_expect_tx(&full[s], 2 * (half ? C::kA + C::kB / 2 : C::kStage));
         const uint32_t bar = map_rank(&full[s], 0);
         uint8_t* sa = sm + s * C::kStage;
         uint8_t* sb = sa + C::kA;
@@ -224,13 +232,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
           w_load_2d_pair(sa, &p.a[src], bar, k0, m0);
         }
         if constexpr (MODE == kFfnGateUp) {   // gate rows in the even CTA, up rows in the odd one
-          w_load_2d_pair(sb, &p.b[rank], bar, k0, t.n * (TN / 2));
+          if (half)
+            w_load_2d_pair(sb, &p.b_half[rank], bar, k0, t.n * (TN / 4));
+          else
+            w_load_2d_pair(sb, &p.b[rank], bar, k0, t.n * (TN / 2));
         } else if constexpr (kBMn) {
-          const int n0 = t.n * TN + TN / 2 * static_cast<int>(rank);
+          const int width = half ? TN / 2 : TN, n0 = t.n * width + width / 2 * static_cast<int>(rank);
           w_load_2d_pair(sb, &p.b[src], bar, n0, k0);
-          if constexpr (TN == 256) w_load_2d_pair(sb + 8192, &p.b[src], bar, n0 + 64, k0);
+          if (TN == 256 && !half) w_load_2d_pair(sb + 8192, &p.b[src], bar, n0 + 64, k0);
         } else {
-          w_load_2d_pair(sb, &p.b[src], bar, k0, t.n * TN + TN / 2 * static_cast<int>(rank));
+          if (half)
+            w_load_2d_pair(sb, &p.b_half[src], bar, k0, t.n * (TN / 2) + TN / 4 * static_cast<int>(rank));
+          else
+            w_load_2d_pair(sb, &p.b[src], bar, k0, t.n * TN + TN / 2 * static_cast<int>(rank));
         }
       }
     }
@@ -245,7 +259,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
     }
   } else if (warp == 1) {
     if (rank == 0) {
-      constexpr uint32_t idesc = idesc_bf16(256, TN) | (kAMn ? kIdescAMajorMn : 0u) | (kBMn ? kIdescBMajorMn : 0u);
+      constexpr uint32_t major = (kAMn ? kIdescAMajorMn : 0u) | (kBMn ? kIdescBMajorMn : 0u);
       const uint32_t base = smem_u32(sm);
       const uint64_t a_desc = kAMn ? sdesc_sw128_mn(base, 8192) : sdesc_sw128(base);
       const uint64_t b_desc = kBMn ? sdesc_sw128_mn(base + C::kA, 8192) : sdesc_sw128(base + C::kA);
@@ -256,6 +270,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
         if (use > 0 && !warp_wait(&acc_empty[b], (use - 1) & 1, p.err)) break;
         tc_fence_after();
         const uint32_t d = tbase + b * TN;
+        const uint32_t idesc = TN == 256 && i >= p.full ? idesc_bf16(256, TN / 2) | major : idesc_bf16(256, TN) | major;
         for (int kb = 0; kb < p.nkb; ++kb, ++it) {
           const uint32_t s = it % kStages;
           if (!warp_wait(&full[s], (it / kStages) & 1, p.err)) {
@@ -287,10 +302,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
       };
       const Tile t = tile_of(p, i);
       const int row0 = t.m * 256 + 128 * static_cast<int>(rank) + 32 * q;
-      const bool ok = row0 < p.M[t.prod]
-                          ? epilogue_row<MODE, ACT, TN>(p, t, tbase + b * TN + (static_cast<uint32_t>(32 * q) << 16),
-                                                    row0 + lane, row0 + lane < p.M[t.prod], (warp - 2) >> 2, ready)
-                          : ready();
+      const uint32_t acc = tbase + b * TN + (static_cast<uint32_t>(32 * q) << 16);
+      const int row = row0 + lane, half = (warp - 2) >> 2;
+      const bool row_ok = row < p.M[t.prod];
+      bool ok;
+      if (row0 >= p.M[t.prod])
+        ok = ready();
+      else if (TN == 256 && t.narrow)
+        ok = epilogue_row<MODE, ACT, 128>(p, t, acc, row, row_ok, half, ready);
+      else
+        ok = epilogue_row<MODE, ACT, TN>(p, t, acc, row, row_ok, half, ready);
       if (!ok) break;
       tc_fence_before();
       __syncwarp();
@@ -310,7 +331,7 @@ cudaError_t launch_tn(const FfnPairParams& p, int ctas, cudaStream_t s) {
   static const cudaError_t attr = cudaFuncSetAttribute(
       ffn_pair_kernel<MODE, ACT, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (attr != cudaSuccess) return attr;
-  const int tiles = p.tile_end[p.nprod - 1];
+  const int tiles = 2 * p.tile_end[p.nprod - 1] - p.full;
   return launch_pdl_cluster(ffn_pair_kernel<MODE, ACT, TN>, dim3(2 * tiles < ctas ? 2 * tiles : ctas),
                             dim3(kPairThreads), C::kSmem, 2, s, p);
 }
@@ -332,19 +353,25 @@ int ffn_pair_tiles(FfnPairParams& p, FfnMode mode, int ctas) {
     }
     return n;
   };
-  const int pairs = ctas / 2;
-  const auto waves = [&](int tn) { return (tiles(tn) + pairs - 1) / pairs; };
-  const int narrow = waves(128), wide = waves(256);      // leaves the wide tiling in p
   // 1 where every output row starts on a 32-byte boundary
   for (int i = 0; i < p.nprod; ++i) p.wide[i] = p.N[i] % 16 == 0 && reinterpret_cast<uintptr_t>(p.out[i]) % 32 == 0;
   if (p.nprod == 1)
     for (int i = 1; i < 3; ++i) p.wide[0] = p.wide[0] && reinterpret_cast<uintptr_t>(p.out[i]) % 32 == 0;
-  // With all SMs busy a narrow tile takes 0.55 to 0.58 of a wide one's time (4096 tokens at 7168 x 6144: forward
-  // 650 us against 593 us); 1003 tokens at 1152 x 864, which leave half of the wide grid idle: 15.9 us against 22.8 us.
-  if (0.57 * narrow < wide) {
-    tiles(128);
+  // With all SMs busy a narrow tile takes 0.55 to 0.58 of a wide one's time
+  // (4096 tokens at 7168 x 6144: forward 650 us against 593 us); 1003 tokens at
+  // 1152 x 864, which leave half of the wide grid idle: 15.9 us against
+  // 22.8 us.  A last wave of wide tiles that fills at most half of the pairs is
+  // cut into halves.
+  constexpr float kNarrow = 0.57f;
+  const int pairs = ctas / 2, narrow = (tiles(128) + pairs - 1) / pairs;
+  const int all = tiles(256), rest = all % pairs;       // leaves the wide tiling in p
+  const bool cut = all > pairs && rest > 0 && 2 * rest <= pairs;
+  const float wide = all / pairs + (rest == 0 ? 0.0f : cut ? kNarrow : 1.0f);
+  if (kNarrow * narrow < wide) {
+    p.full = tiles(128);
     return 128;
   }
+  p.full = cut ? all - rest : all;
   return 256;
 }
 

@@ -30,10 +30,12 @@ enum FfnMode {
 };
 struct FfnPairParams {
   CUtensorMap a[3], b[3];
+  CUtensorMap b_half[2];      // K-contiguous b with boxes of half as many rows
   void* out[3];
   const void *in_g, *in_u;
   int M[3], N[3];             // output rows and columns of each product
   int tiles_n[3], tile_end[3], nprod;
+  int full;                   // tiles from here on are worked in halves of their columns
   int wide[3];                // outputs whose rows start on 32-byte boundaries
   int nkb, nkb0;              // 64-wide K blocks in all; of the first (A, B) of a concatenation
   float b1, b2;
@@ -41,7 +43,8 @@ struct FfnPairParams {
   int* err;
 };
 // Chooses the tile width (128 or 256) for M, N, nprod and out and fills
-// tiles_n, tile_end and wide; K-contiguous B maps have boxes of half of it.
+// tiles_n, tile_end, full and wide; K-contiguous b maps have boxes of half of
+// it, b_half (width 256) of a quarter.
 int ffn_pair_tiles(FfnPairParams& p, FfnMode mode, int ctas);
 cudaError_t launch_ffn_pair(FfnMode mode, const FfnPairParams& p, int tn, int ctas, cudaStream_t s);
 // Largest number of CTAs (an even number) of the pair kernels that run at once.

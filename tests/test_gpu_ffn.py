@@ -80,7 +80,9 @@ def test_forward_and_backward(ops, T, d, F, act):
     layer.close()
 
 
-@pytest.mark.parametrize("T,d,F", [(1, 7168, 2048), (64, 7168, 2048), (300, 2048, 6144), (2100, 1152, 864)])
+# the last: more 256-column tiles than the GPU has CTA pairs, with a few left over in every product
+@pytest.mark.parametrize("T,d,F", [(1, 7168, 2048), (64, 7168, 2048), (96, 2048, 1040), (97, 2048, 1040),
+                                   (300, 2048, 6144), (2100, 1152, 864), (2600, 1752, 2000)])
 def test_model_widths(ops, T, d, F):
     x, W, dy = _make(T, d, F, 3)
     layer = ops.GatedFFN(W, max_tokens=T, training=True)
