@@ -69,13 +69,23 @@ def test_forward(ops, T, d, rt):
         _check_mx(q, s, ref)
 
 
-@pytest.mark.parametrize("T,d", [(4000, 7168), (8192, 256), (1, 512)])
-def test_forward_many_rows(ops, T, d):
-    x, r, w = _make(T, d, 5, torch.bfloat16)
+@pytest.mark.parametrize("rt", [None, torch.bfloat16, torch.float32], ids=["none", "bf16", "fp32"])
+@pytest.mark.parametrize("T,d", [(4000, 7168), (8200, 256), (3001, 1152), (1000, 2600), (300, 8192), (301, 8184)])
+def test_forward_many_rows(ops, T, d, rt):
+    x, r, w = _make(T, d, 5, rt)
     y, _, h = ops.lmoe_add_rms_norm(x, w, EPS, residual=r)
     ref, href = R.norm(x, r, w, EPS)
-    assert torch.equal(h, href)
+    assert r is None or torch.equal(h, href)
     _check_y(y, ref)
+    if d % 32 == 0:
+        q, s, h = ops.lmoe_add_rms_norm(x, w, EPS, residual=r, out_format="mxfp8")
+        assert r is None or torch.equal(h, href)
+        _check_mx(q, s, ref)
+    if r is not None:                # strided rows, the sum in place
+        wide = torch.empty(T, d + 64, device="cuda", dtype=torch.bfloat16)
+        wide[:, 32:32 + d] = x
+        y2, _, h2 = ops.lmoe_add_rms_norm(wide[:, 32:32 + d], w, EPS, residual=r, h_out=r)
+        assert torch.equal(h2, href) and torch.equal(y2, y)
 
 
 def test_strided_rows_in_place_and_none(ops):
