@@ -6,3 +6,4 @@ from .binding import (LatentMoE, LmoeError, load_library, status_string, make_co
                       LMOE_OK, LMOE_ERR_INVALID_ARG, LMOE_ERR_UNSUPPORTED, LMOE_ERR_CUDA, LMOE_ERR_OOM,
                       LMOE_ERR_TIMEOUT)
 from .feed_forward import GatedFFN, lmoe_add_rms_norm, lmoe_add_rms_norm_backward  # noqa: F401
+from .sublayer import FeedForwardSublayer  # noqa: F401
