@@ -18,6 +18,7 @@ from . import binding as B
 _OUT_FORMATS = {"bf16": 0, "mxfp8": 1}
 _STREAM_TYPES = {torch.bfloat16: 0, torch.float32: 1}
 _BF16, _U8, _F32 = torch.bfloat16, torch.uint8, torch.float32
+_PACKED = torch.contiguous_format
 
 
 def _rows(name: str, t: torch.Tensor, dtypes, shape) -> int:
@@ -93,7 +94,7 @@ def lmoe_add_rms_norm(x: torch.Tensor, norm_w: torch.Tensor, eps: float, residua
         _on_device(dev, norm_w, residual)
         st = _STREAM_TYPES[residual.dtype]
         if h_out is None:
-            h = torch.empty(shape, dtype=residual.dtype, device=x.device)
+            h = torch.empty_like(residual, memory_format=_PACKED)
         else:
             h = h_out
             _packed("h_out", h, residual.dtype, shape)
@@ -104,11 +105,11 @@ def lmoe_add_rms_norm(x: torch.Tensor, norm_w: torch.Tensor, eps: float, residua
         if h_out is not None:
             raise ValueError("h_out needs a residual")
     if fmt:
-        y = torch.empty(shape, dtype=_U8, device=x.device)
+        y = torch.empty_like(x, dtype=_U8, memory_format=_PACKED)
         s = torch.empty(T, d // 32, dtype=_U8, device=x.device)
         sp = s.data_ptr()
     else:
-        y = torch.empty(shape, dtype=_BF16, device=x.device)
+        y = torch.empty_like(x, memory_format=_PACKED)
     status = B.load_library().lmoe_add_rms_norm(x.data_ptr(), ldx, rp, ldr, st, T, d, norm_w.data_ptr(), eps, hp,
                                                 y.data_ptr(), fmt, sp, _raw_stream(dev))
     if status:
@@ -148,7 +149,7 @@ def lmoe_add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, norm_w: torch.
         _on_device(dev, dh)
         ep = dh.data_ptr()
     n = _norm_backward_workspace(T, d)
-    dx = torch.empty(shape, dtype=h.dtype, device=h.device)
+    dx = torch.empty_like(h, memory_format=_PACKED)
     dw = torch.empty(d, dtype=_F32, device=h.device)
     ws = torch.empty(n, dtype=_U8, device=h.device)
     status = B.load_library().lmoe_add_rms_norm_backward(
@@ -157,17 +158,6 @@ def lmoe_add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, norm_w: torch.
     if status:
         raise B.LmoeError("lmoe_add_rms_norm_backward", status)
     return dx, dw
-
-
-def _on_stream(f):
-    """With stream=..., run the call and its allocations on that stream; otherwise on the current one."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
-    return call
 
 
 class GatedFFN:
@@ -228,57 +218,72 @@ class GatedFFN:
         _on_device(self._dev, out)
         return out
 
-    @_on_stream
-    def lmoe_ffn_forward(self, x: torch.Tensor, save: bool = False, out: torch.Tensor | None = None):
+    def lmoe_ffn_forward(self, x: torch.Tensor, save: bool = False, out: torch.Tensor | None = None, stream=None):
         """x bf16 [T][d_model] -> y bf16; with save=True (y, g, u): the
         pre-activations bf16 [T][d_ff] that lmoe_ffn_backward takes."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.lmoe_ffn_forward(x, save, out)
         T = x.shape[0]
         ldx = self._tokens(x, "x", T)
-        out = self._out(T, out)
-        g = u = gp = up = None
-        if save:
-            g = torch.empty(T, self.d_ff, dtype=_BF16, device=self._device)
-            u = torch.empty(T, self.d_ff, dtype=_BF16, device=self._device)
-            gp, up = g.data_ptr(), u.data_ptr()
-        status = self._lib.lmoe_ffn_forward(self._h, x.data_ptr(), ldx, T, out.data_ptr(), gp, up,
+        y = torch.empty_like(x, memory_format=_PACKED) if out is None else self._out(T, out)
+        if not save:
+            status = self._lib.lmoe_ffn_forward(self._h, x.data_ptr(), ldx, T, y.data_ptr(), None, None,
+                                                _raw_stream(self._dev))
+            if status:
+                raise B.LmoeError("lmoe_ffn_forward", status)
+            return y
+        g = torch.empty(T, self.d_ff, dtype=_BF16, device=self._device)
+        u = torch.empty_like(g)
+        status = self._lib.lmoe_ffn_forward(self._h, x.data_ptr(), ldx, T, y.data_ptr(), g.data_ptr(), u.data_ptr(),
                                             _raw_stream(self._dev))
         if status:
             raise B.LmoeError("lmoe_ffn_forward", status)
-        return (out, g, u) if save else out
+        return y, g, u
 
-    @_on_stream
     def lmoe_ffn_backward(self, x: torch.Tensor, g: torch.Tensor, u: torch.Tensor, dy: torch.Tensor,
-                          need_dx: bool = True, need_dw: bool = True):
+                          need_dx: bool = True, need_dw: bool = True, stream=None):
         """-> (dx, dw_gate, dw_up, dw_down), bf16; None for those not asked for."""
-        T, d, F = x.shape[0], self.d_model, self.d_ff
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.lmoe_ffn_backward(x, g, u, dy, need_dx, need_dw)
+        T, shape = x.shape[0], (x.shape[0], self.d_ff)
         ldx = self._tokens(x, "x", T)
         lddy = self._tokens(dy, "dy", T)
-        _packed("g", g, _BF16, (T, F))
-        _packed("u", u, _BF16, (T, F))
+        _packed("g", g, _BF16, shape)
+        _packed("u", u, _BF16, shape)
         _on_device(self._dev, g, u)
-        grads = [torch.empty(s, dtype=_BF16, device=self._device) if need else None
-                 for s, need in (((T, d), need_dx), ((F, d), need_dw), ((F, d), need_dw), ((d, F), need_dw))]
-        status = self._lib.lmoe_ffn_backward(
-            self._h, x.data_ptr(), ldx, g.data_ptr(), u.data_ptr(), dy.data_ptr(), lddy, T,
-            *(None if t is None else t.data_ptr() for t in grads), _raw_stream(self._dev))
+        dx = dwg = dwu = dwd = xp = gp = up = dp = None
+        if need_dx:
+            dx = torch.empty_like(x, memory_format=_PACKED)
+            xp = dx.data_ptr()
+        if need_dw:
+            w = self._weights
+            dwg, dwu, dwd = torch.empty_like(w["gate"]), torch.empty_like(w["up"]), torch.empty_like(w["down"])
+            gp, up, dp = dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr()
+        status = self._lib.lmoe_ffn_backward(self._h, x.data_ptr(), ldx, g.data_ptr(), u.data_ptr(), dy.data_ptr(),
+                                             lddy, T, xp, gp, up, dp, _raw_stream(self._dev))
         if status:
             raise B.LmoeError("lmoe_ffn_backward", status)
-        return tuple(grads)
+        return dx, dwg, dwu, dwd
 
-    @_on_stream
-    def lmoe_ffn_forward_mx(self, x_codes: torch.Tensor, x_scales: torch.Tensor, out: torch.Tensor | None = None):
+    def lmoe_ffn_forward_mx(self, x_codes: torch.Tensor, x_scales: torch.Tensor, out: torch.Tensor | None = None,
+                            stream=None):
         """MXFP8 x (codes uint8 [T][d_model], scales uint8 [T][d_model/32],
         as lmoe_add_rms_norm(out_format="mxfp8") returns them) -> y bf16."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.lmoe_ffn_forward_mx(x_codes, x_scales, out)
         T = x_codes.shape[0]
         _packed("x_codes", x_codes, _U8, (T, self.d_model))
         _packed("x_scales", x_scales, _U8, (T, self.d_model // 32))
         _on_device(self._dev, x_codes, x_scales)
-        out = self._out(T, out)
-        status = self._lib.lmoe_ffn_forward_mx(self._h, x_codes.data_ptr(), x_scales.data_ptr(), T, out.data_ptr(),
+        y = self._out(T, out)
+        status = self._lib.lmoe_ffn_forward_mx(self._h, x_codes.data_ptr(), x_scales.data_ptr(), T, y.data_ptr(),
                                                _raw_stream(self._dev))
         if status:
             raise B.LmoeError("lmoe_ffn_forward_mx", status)
-        return out
+        return y
 
     def lmoe_ffn_sync_status(self, stream=None):
         B._check("lmoe_ffn_sync_status", self._lib.lmoe_ffn_sync_status(self._h, B._stream(stream)))
