@@ -21,11 +21,13 @@ struct lmoe_ffn_ctx {
   void* pool = nullptr;
   int* err = nullptr;
   void *hid = nullptr, *dg = nullptr, *du = nullptr;
-  CUtensorMap gate[2], up[2], down[2];   // K contiguous, boxes of 64 x 128 and 64 x 64 rows; MXFP8: [0] only
+  // K contiguous, boxes of 64 K values x 128 and 64 rows; MXFP8: 128 K values x 96 and 64 rows
+  CUtensorMap gate[2], up[2], down[2];
   CUtensorMap gate_n, up_n, down_n;   // the same memory as N contiguous operands, boxes of 64 x 64
   // MXFP8 blocks: hid holds codes; scale atoms of x, hid and the weights
-  uint8_t *x_sf = nullptr, *hid_sf = nullptr, *gu_sf = nullptr, *down_sf = nullptr;
-  CUtensorMap m_x_sf, m_hid_sf, m_gu_sf, m_down_sf;
+  // (of the pair tiles, and [1] of the small-batch tiles)
+  uint8_t *x_sf = nullptr, *hid_sf = nullptr, *gu_sf[2] = {}, *down_sf[2] = {};
+  CUtensorMap m_x_sf, m_hid_sf, m_gu_sf[2], m_down_sf[2];
   int launches = 0;
 };
 
@@ -192,9 +194,18 @@ lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* 
   // scale atoms: 512 bytes for 128 rows x 128 values
   const size_t kd = ceil_div(d, 128), kf = ceil_div(F, 128);
   const size_t x_sf = T256 / 128 * kd * 512, hid_sf = T256 / 128 * kf * 512;
-  const size_t gu_tiles = ceil_div(F, kMxTileN / 2), down_tiles = ceil_div(d, kMxTileN);
-  const size_t gu_sf = gu_tiles * kd * 1024, down_sf = down_tiles * kf * 1024;
-  const size_t bytes = 256 + act_bytes * (cfg->training ? 3 : 1) + (mx ? x_sf + hid_sf + gu_sf + down_sf : 0);
+  // tiles of the weights' atoms: pair tiles (two atoms for 192 rows), small-batch tiles (one for 128)
+  const int width[2] = {kMxTileN, kMxSkinnyN}, per[2] = {1024, 512};
+  size_t gu_sf[2], down_sf[2], w_sf = 0;
+  int gu_tiles[2], down_tiles[2];
+  for (int i = 0; i < 2; ++i) {
+    gu_tiles[i] = ceil_div(F, width[i] / 2);
+    down_tiles[i] = ceil_div(d, width[i]);
+    gu_sf[i] = gu_tiles[i] * kd * per[i];
+    down_sf[i] = down_tiles[i] * kf * per[i];
+    w_sf += gu_sf[i] + down_sf[i];
+  }
+  const size_t bytes = 256 + act_bytes * (cfg->training ? 3 : 1) + (mx ? x_sf + hid_sf + w_sf : 0);
   cudaError_t e = ffn_pair_ctas(&h->ctas);
   if (e == cudaSuccess) e = cudaMalloc(&h->pool, bytes);
   // the error flag, and the bytes of the scale atoms that nothing writes
@@ -212,15 +223,20 @@ lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* 
   if (mx) {
     h->x_sf = base + 256 + act_bytes;
     h->hid_sf = h->x_sf + x_sf;
-    h->gu_sf = h->hid_sf + hid_sf;
-    h->down_sf = h->gu_sf + gu_sf;
-    e = launch_mx_weight_atoms(w->gate_s, w->up_s, F, d, static_cast<int>(gu_tiles), h->gu_sf, stream);
-    if (e == cudaSuccess)
-      e = launch_mx_weight_atoms(w->down_s, nullptr, d, F, static_cast<int>(down_tiles), h->down_sf, stream);
-    ok = map_mx(&h->gate[0], w->gate, d, F, kMxTileN / 2) && map_mx(&h->up[0], w->up, d, F, kMxTileN / 2) &&
-         map_mx(&h->down[0], w->down, F, d, kMxTileN / 2) && map_atoms(&h->m_x_sf, h->x_sf, x_sf, 1) &&
-         map_atoms(&h->m_hid_sf, h->hid_sf, hid_sf, 1) && map_atoms(&h->m_gu_sf, h->gu_sf, gu_sf, 2) &&
-         map_atoms(&h->m_down_sf, h->down_sf, down_sf, 2);
+    ok = map_atoms(&h->m_x_sf, h->x_sf, x_sf, 1) && map_atoms(&h->m_hid_sf, h->hid_sf, hid_sf, 1);
+    uint8_t* at = h->hid_sf + hid_sf;
+    for (int i = 0; i < 2 && ok && e == cudaSuccess; ++i) {
+      const int box = i == 0 ? kMxTileN / 2 : kMxSkinnyN / 2;
+      h->gu_sf[i] = at;
+      h->down_sf[i] = at + gu_sf[i];
+      at += gu_sf[i] + down_sf[i];
+      e = launch_mx_weight_atoms(w->gate_s, w->up_s, F, d, width[i], gu_tiles[i], h->gu_sf[i], stream);
+      if (e == cudaSuccess)
+        e = launch_mx_weight_atoms(w->down_s, nullptr, d, F, width[i], down_tiles[i], h->down_sf[i], stream);
+      ok = map_mx(&h->gate[i], w->gate, d, F, box) && map_mx(&h->up[i], w->up, d, F, box) &&
+           map_mx(&h->down[i], w->down, F, d, box) && map_atoms(&h->m_gu_sf[i], h->gu_sf[i], gu_sf[i], per[i] / 512) &&
+           map_atoms(&h->m_down_sf[i], h->down_sf[i], down_sf[i], per[i] / 512);
+    }
   } else {
     h->dg = base + 256 + act_bytes;
     h->du = base + 256 + 2 * act_bytes;
@@ -407,14 +423,14 @@ lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8
     g.b2 = h->cfg.situ_linear_beta;
     g.err = n.err = h->err;
     g.kblks = d / 32;
-    g.b[0] = h->gate[0];
-    g.b[1] = h->up[0];
-    g.sfb = h->m_gu_sf;
+    g.b[0] = h->gate[1];
+    g.b[1] = h->up[1];
+    g.sfb = h->m_gu_sf[1];
     g.row_sf = x_scales;
     g.out = h->hid;
     g.out_sf = h->hid_sf;
-    n.b[0] = h->down[0];
-    n.sfb = h->m_down_sf;
+    n.b[0] = h->down[1];
+    n.sfb = h->m_down_sf[1];
     n.row_sf = h->hid_sf;
     n.out = out;
     if (!map_mx(&g.a, x, d, T, g.tb) || !map_mx(&n.a, h->hid, F, T, n.tb)) return LMOE_ERR_CUDA;
@@ -432,7 +448,7 @@ lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8
   p.b[0] = h->gate[0];
   p.b[1] = h->up[0];
   p.sfa = h->m_x_sf;
-  p.sfb = h->m_gu_sf;
+  p.sfb = h->m_gu_sf[0];
   p.out = h->hid;
   p.out_sf = h->hid_sf;
   p.out_nkb = ceil_div(F, 128);
@@ -445,7 +461,7 @@ lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8
   FFN_TRY(launch_ffn_mx_pair(p, true, h->ctas, stream));
   p.b[0] = h->down[0];
   p.sfa = h->m_hid_sf;
-  p.sfb = h->m_down_sf;
+  p.sfb = h->m_down_sf[0];
   p.out = out;
   p.wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;   // d is a multiple of 32
   p.N = d;

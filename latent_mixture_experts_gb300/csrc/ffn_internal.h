@@ -98,13 +98,15 @@ cudaError_t launch_ffn_mx_pair(const FfnMxParams& p, bool gate_up, int ctas, cud
 // Scales [T][K/32] -> atoms; bytes of blocks past K/32 keep the zeros that the
 // buffer is created with where a group of four is not begun.
 cudaError_t launch_mx_row_atoms(const uint8_t* s, int T, int K, uint8_t* out, cudaStream_t stream);
-// Weight scales [rows][K/32] (with `up`: gate and up) -> atoms of `tiles` tiles.
-cudaError_t launch_mx_weight_atoms(const uint8_t* a, const uint8_t* up, int rows, int K, int tiles, uint8_t* out,
-                                   cudaStream_t stream);
+// Weight scales [rows][K/32] (with `up`: gate and up) -> atoms of tiles of
+// `width` (192 or 128) rows.
+cudaError_t launch_mx_weight_atoms(const uint8_t* a, const uint8_t* up, int rows, int K, int width, int tiles,
+                                   uint8_t* out, cudaStream_t stream);
 
 // Small batches: K split over clusters, as in the bf16 form.
+constexpr int kMxSkinnyN = 128;   // weight rows of a tile: 64 gate and 64 up rows, or 128 output features
 struct FfnMxSkinnyParams {
-  CUtensorMap a, b[2], sfb;     // codes: boxes of 128 K values x tb and 96 rows; the weights' atoms
+  CUtensorMap a, b[2], sfb;     // codes: boxes of 128 K values x tb and 64 rows; the weights' atoms [tile][nkb]
   const uint8_t* row_sf;        // gate/up: x's scales [T][kblks]; else hid's atoms
   void* out;
   uint8_t* out_sf;              // gate/up: hid's atoms

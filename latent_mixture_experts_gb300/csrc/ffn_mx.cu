@@ -245,28 +245,30 @@ __global__ void mx_row_atoms_kernel(const uint8_t* __restrict__ s, int T, int kb
   }
 }
 
-// Weight scales -> atoms [tile][nkb][2][512].  Tile row n of 192: with `up`,
-// gate row 96 tile + n, then up row 96 tile + n - 96; else row 192 tile + n of
-// the one matrix.  Rows past the end and blocks past kblks get zeros.
+// Weight scales -> atoms [tile][nkb][width / 128 rounded up][512].  Tile row
+// r < width: with `up`, gate row width/2 * tile + r, then the up rows of the
+// same features; else row width * tile + r of the one matrix.  Rows past the
+// end and blocks past kblks get zeros.
 __global__ void mx_weight_atoms_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ up, int rows,
-                                       int kblks, int nkb, int tiles, uint8_t* __restrict__ out) {
-  const long long n = static_cast<long long>(tiles) * nkb * 256;
+                                       int kblks, int nkb, int width, int tiles, uint8_t* __restrict__ out) {
+  const int atoms = (width + 127) / 128, half = width / 2;
+  const long long n = static_cast<long long>(tiles) * nkb * atoms * 128;
   for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < n;
        i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const int r = static_cast<int>(i & 255);
-    const long long tk = i >> 8;
+    const int r = static_cast<int>(i % (atoms * 128));
+    const long long tk = i / (atoms * 128);
     const int g = static_cast<int>(tk % nkb), t = static_cast<int>(tk / nkb);
     const uint8_t* src = a;
-    int row = t * kMxTileN + r;
+    int row = t * width + r;
     if (up) {
-      row = t * kHalfN + (r < kHalfN ? r : r - kHalfN);
-      if (r >= kHalfN) src = up;
+      row = t * half + (r < half ? r : r - half);
+      if (r >= half) src = up;
     }
     uint32_t w = 0;
-    if (r < kMxTileN && row < rows)
+    if (r < width && row < rows)
       for (int k = 0; k < 4; ++k)
         if (4 * g + k < kblks) w |= static_cast<uint32_t>(src[static_cast<size_t>(row) * kblks + 4 * g + k]) << (8 * k);
-    *reinterpret_cast<uint32_t*>(out + tk * 1024 + (r >> 7) * 512 + sf_atom_offset(r & 127, 0)) = w;
+    *reinterpret_cast<uint32_t*>(out + (tk * atoms + (r >> 7)) * 512 + sf_atom_offset(r & 127, 0)) = w;
   }
 }
 
@@ -292,10 +294,11 @@ cudaError_t launch_mx_row_atoms(const uint8_t* s, int T, int K, uint8_t* out, cu
                     K / 32, nkb, out);
 }
 
-cudaError_t launch_mx_weight_atoms(const uint8_t* a, const uint8_t* up, int rows, int K, int tiles, uint8_t* out,
-                                   cudaStream_t stream) {
+cudaError_t launch_mx_weight_atoms(const uint8_t* a, const uint8_t* up, int rows, int K, int width, int tiles,
+                                   uint8_t* out, cudaStream_t stream) {
   const int nkb = (K + 127) / 128;
-  mx_weight_atoms_kernel<<<ew_blocks(256ll * tiles * nkb), 256, 0, stream>>>(a, up, rows, K / 32, nkb, tiles, out);
+  mx_weight_atoms_kernel<<<ew_blocks(256ll * tiles * nkb), 256, 0, stream>>>(a, up, rows, K / 32, nkb, width, tiles,
+                                                                             out);
   return cudaGetLastError();
 }
 

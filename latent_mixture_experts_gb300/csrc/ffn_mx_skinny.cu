@@ -1,9 +1,9 @@
-// The MXFP8 feed-forward passes on small batches (up to 48 tokens), bound by
+// The MXFP8 feed-forward passes on small batches (up to 64 tokens), bound by
 // streaming the weights' codes and scales once from HBM.
 //
 // As in the bf16 form, tokens are the MMA's M rows, weight rows its N columns
-// (tiles of the large-batch form, so both read the same scale atoms), and a
-// cluster splits K.  Each CTA finishes a share of the tokens with all of the
+// (128: one whole scale atom for each 128-wide K block, so the weights' atoms
+// are laid out a second time for these tiles), and a cluster splits K.  Each CTA finishes a share of the tokens with all of the
 // tile's features, so that a warp holds a whole 32-value block of the hidden
 // activation when it encodes it.  The scales of the tokens are put into
 // shared memory once, for all of the CTA's K range: x's by the epilogue's
@@ -19,16 +19,16 @@ namespace lmoe {
 namespace {
 
 constexpr int kThreads = 192;            // TMA, MMA, 4 epilogue warps
-constexpr int kN = kMxTileN, kHalf = kMxTileN / 2;
-constexpr int kB = kN * 128;             // codes of a 128-wide K chunk
-constexpr int kMaxStages = 5;            // 12 columns of scales each, beside 192 of sums
-constexpr int kTmem = 256, kSfCols = 12;
+constexpr int kN = kMxSkinnyN, kHalf = kN / 2;
+constexpr int kB = kN * 128;             // codes of a 128-wide K block
+constexpr int kMaxStages = 8;            // 8 columns of scales each, beside 128 of sums
+constexpr int kTmem = 256, kSfCols = 8;
+constexpr int kSfb = 512;
 constexpr int kPitch = kN + 4;           // floats of a token's partial sums: 16-byte rows, four banks apart
-constexpr int kMinCtas = 150;            // one for each SM (16 tokens at 7168 x 6144: 30 us; with 60, 47 us)
-// Up to here against the pair tiles: 48 tokens at widths 7168 and 6144 39.2 us
-// and 38.9 us, at 2048 and 2048 15.7 us and 17.7 us; 64 tokens 42.9 us and
-// 39.1 us, 18.1 us and 18.1 us.
-constexpr int kMxSkinnyMaxTokens = 48;
+// Up to here rather than the pair tiles: 64 tokens at widths 7168 and 6144 take
+// 42 us here and 39 us there, at 7168 and 2048 21 us and 27 us, at 2048 and 2048
+// 16.5 us and 18.2 us.  16 tokens at 7168 and 6144: 29 us, 4.7 TB/s of weights.
+constexpr int kMxSkinnyMaxTokens = 64;
 static_assert(kN + kMaxStages * kSfCols <= kTmem, "tensor memory");
 
 template <bool GU, int ACT>
@@ -80,11 +80,11 @@ __global__ void __launch_bounds__(kThreads) ffn_mx_skinny_kernel(const __grid_co
         w_load_2d(dst, &p.b[0], &full[s], kb * 128, tile * kN);
         w_load_2d(dst + kHalf * 128, &p.b[0], &full[s], kb * 128, tile * kN + kHalf);
       }
-      w_load_2d(sfb + s * 1024, &p.sfb, &full[s], 0, 2 * (tile * p.nkb + kb));
+      w_load_2d(sfb + s * kSfb, &p.sfb, &full[s], 0, tile * p.nkb + kb);
     };
     const int pre = steps < p.stages ? steps : p.stages;
     for (int i = 0; i < pre; ++i) {
-      w_arrive_expect_tx(&full[i], a_bytes + kB + 1024);
+      w_arrive_expect_tx(&full[i], a_bytes + kB + kSfb);
       load_b(i, i);
     }
     griddep_wait();
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) ffn_mx_skinny_kernel(const __grid_co
     uint32_t phase = 0;
     for (int i = pre; i < steps; ++i) {
       if (!warp_wait(&empty[s], phase, p.err)) break;
-      w_arrive_expect_tx(&full[s], a_bytes + kB + 1024);
+      w_arrive_expect_tx(&full[s], a_bytes + kB + kSfb);
       load_b(i, s);
       w_load_2d(sm + s * a_bytes, &p.a, &full[s], (first + i) * 128, 0);
       if (++s == p.stages) s = 0, phase ^= 1;
@@ -114,8 +114,7 @@ __global__ void __launch_bounds__(kThreads) ffn_mx_skinny_kernel(const __grid_co
       const uint64_t ad = a_desc + static_cast<uint32_t>(s * a_bytes >> 4), bd = b_desc + s * (kB >> 4);
       const uint32_t sf = tacc + kN + s * kSfCols;
       w_copy_atom(sf, sa_desc + 32 * i);
-      w_copy_atom(sf + 4, sb_desc + 64 * s);
-      w_copy_atom(sf + 8, sb_desc + 64 * s + 32);
+      w_copy_atom(sf + 4, sb_desc + 32 * s);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         w_mma_mx(tacc, ad + 2 * k, bd + 2 * k, idesc_mxf8f6f4(128, kN, 0, 0, k, k), sf, sf + 4, (i | k) != 0);
@@ -175,9 +174,10 @@ __global__ void __launch_bounds__(kThreads) ffn_mx_skinny_kernel(const __grid_co
   const int tok0 = rank * per, ntok = min(per, p.T - tok0);
   if constexpr (GU) {
     // one warp for each token and block of 32 features, lane = feature
+    constexpr int kBlocks = kHalf / 32;
     const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
-    for (int e = warp; e < 3 * ntok; e += kThreads / 32) {
-      const int i = e / 3, c = 32 * (e - 3 * i), f = tile * kHalf + c;
+    for (int e = warp; e < kBlocks * ntok; e += kThreads / 32) {
+      const int i = e / kBlocks, c = 32 * (e - kBlocks * i), f = tile * kHalf + c;
       if (f >= p.M) continue;
       float g = 0.f, u = 0.f;
       for (int r = 0; r < p.splits; ++r) {
@@ -226,13 +226,18 @@ bool ffn_mx_skinny_plan(FfnMxSkinnyParams& p, bool gate_up) {
   if (p.T > kMxSkinnyMaxTokens) return false;
   p.tiles = gate_up ? (p.M + kHalf - 1) / kHalf : (p.M + kN - 1) / kN;
   p.tb = (p.T + 7) / 8 * 8;
+  // as in the bf16 form, in 128-wide K blocks
   p.splits = 1;
-  while (p.splits < kSkinnyMaxSplits && p.tiles * p.splits < kMinCtas && 2 * p.splits <= p.nkb) p.splits *= 2;
+  for (int n = 2; n <= kSkinnyMaxSplits; n *= 2) {
+    const int ctas = p.tiles * p.splits, left = p.nkb / n;
+    if (n > p.nkb || !((ctas < 110 && left >= 2) || (ctas < 150 && left >= 6))) break;
+    p.splits = n;
+  }
   const int budget = kSkinnySmem - 1024;
   const int sfa = (p.nkb + p.splits - 1) / p.splits * 512;
   const int recv = 4 * p.splits * ((p.T + p.splits - 1) / p.splits) * kPitch;
   // the partial sums meet behind the ring, or over it where room behind would cost a stage
-  const int stage = p.tb * 128 + kB + 1024;
+  const int stage = p.tb * 128 + kB + kSfb;
   p.reuse_ring = (budget - sfa - recv) / stage < (budget - sfa) / stage;
   const int ring = (budget - sfa - (p.reuse_ring ? 0 : recv)) / 1024 * 1024;
   p.stages = ring / stage;

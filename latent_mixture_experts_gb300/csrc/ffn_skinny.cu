@@ -22,14 +22,14 @@ namespace lmoe {
 namespace {
 
 constexpr int kThreads = 128;
-// MMA columns: weight rows of a tile.  Narrower tiles cost more MMAs (32: one
-// token at widths 7168 and 6144 61 us against 46 us), wider ones more bytes of
-// partial sums (128: 64 tokens at 7168 and 2048 29 us against 25 us; one token
-// 45 us and 19.5 us against 46 us and 20.1 us).
+// MMA columns, the weight rows of a tile.  Wider tiles cost fewer MMAs, narrower
+// ones fewer bytes of partial sums: one token at widths 7168 and 6144 takes
+// 45.5 us with 128 columns, 46.4 us with 64 and 61 us with 32; at 7168 and 2048
+// 20.6 us, 20.0 us and 23.6 us; 64 tokens there 29 us, 25 us and 26 us.
 constexpr int kCols = 64;
 
-// GU: gate and up rows of 64 features -> act(g, u); else 128 output features
-// of one matrix.
+// GU: gate and up rows of 32 features -> act(g, u); else 64 output features of
+// one matrix.
 template <bool GU, int ACT>
 __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_constant__ FfnSkinnyParams p) {
   extern __shared__ uint8_t smem_raw[];
