@@ -3,7 +3,7 @@
 //
 //   forward:  gate/up products + activation -> hid;  hid x down
 //   backward: dy x down + activation gradient -> dg, du, hid;
-//             dg x gate + du x up -> dx;  dg^T x, du^T x, dy^T hid in one launch
+//             dg x gate + du x up -> dx, dg^T x, du^T x, dy^T hid in one launch
 #include <cmath>
 #include <new>
 
@@ -310,7 +310,7 @@ lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int 
   p.nprod = 1;
   p.M[0] = T;
   p.N[0] = F;
-  p.nkb = p.nkb0 = ceil_div(d, 64);
+  p.nkb = ceil_div(d, 64);
   p.out[0] = h->hid;
   p.out[1] = gate;
   p.out[2] = up;
@@ -322,9 +322,8 @@ lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int 
   if (!map_k(&p.a[0], x, d, T, ldx)) return LMOE_ERR_CUDA;
   FFN_TRY(launch_ffn_pair(kFfnGateUp, p, tn, h->ctas, stream));
   p.N[0] = d;
-  p.nkb = p.nkb0 = ceil_div(F, 64);
+  p.nkb = ceil_div(F, 64);
   p.out[0] = out;
-  p.out[1] = p.out[2] = nullptr;
   tn = ffn_pair_tiles(p, kFfnPlain, h->ctas);
   p.b[0] = h->down[tn == 128];
   p.b_half[0] = h->down[1];
@@ -367,40 +366,38 @@ lmoe_status lmoe_ffn_backward(lmoe_ffn_handle h, const void* x, int64_t ldx, con
   p.out[2] = h->hid;
   p.M[0] = T;
   p.N[0] = F;
-  p.nkb = p.nkb0 = ceil_div(d, 64);
+  p.nkb = ceil_div(d, 64);
   if (!map_k(&p.a[0], dy, d, T, lddy)) return LMOE_ERR_CUDA;
   FFN_TRY(launch_ffn_pair(kFfnDHid, p, ffn_pair_tiles(p, kFfnDHid, h->ctas), h->ctas, stream));
   h->launches = 1;
-  if (dx) {   // dx = [dg | du] [gate ; up]
+  // the gradients, in one launch: dx = [dg | du] [gate ; up], dw = dg^T x, du^T x, dy^T hid
+  p.nprod = 0;
+  const auto add = [&](int M, int N, void* out) {
+    p.M[p.nprod] = M;
+    p.N[p.nprod] = N;
+    p.out[p.nprod] = out;
+    return p.nprod++;
+  };
+  bool ok = true;
+  if (dx) {
+    add(T, d, dx);
+    p.cat = 1;
+    p.nkb_cat = ceil_div(F, 64);
     p.b[0] = h->gate_n;
-    p.b[1] = h->up_n;
-    p.out[0] = dx;
-    p.out[1] = p.out[2] = nullptr;
-    p.N[0] = d;
-    p.nkb0 = ceil_div(F, 64);
-    p.nkb = 2 * p.nkb0;
-    if (!map_k(&p.a[0], h->dg, F, T, F) || !map_k(&p.a[1], h->du, F, T, F)) return LMOE_ERR_CUDA;
-    FFN_TRY(launch_ffn_pair(kFfnDx, p, ffn_pair_tiles(p, kFfnDx, h->ctas), h->ctas, stream));
-    ++h->launches;
+    p.b_cat = h->up_n;
+    ok = map_k(&p.a[0], h->dg, F, T, F) && map_k(&p.a_cat, h->du, F, T, F);
   }
-  if (dwg || dwu || dwd) {
-    p.nprod = 0;
-    auto add = [&](const void* a, long long lda, int M, const void* b, long long ldb, int N, void* out) {
-      const int i = p.nprod++;
-      p.out[i] = out;
-      p.M[i] = M;
-      p.N[i] = N;
-      return map_n(&p.a[i], a, M, T, lda) && map_n(&p.b[i], b, N, T, ldb);
-    };
-    bool ok = true;
-    if (dwg) ok = ok && add(h->dg, F, F, x, ldx, d, dwg);
-    if (dwu) ok = ok && add(h->du, F, F, x, ldx, d, dwu);
-    if (dwd) ok = ok && add(dy, lddy, d, h->hid, F, F, dwd);
-    if (!ok) return LMOE_ERR_CUDA;
-    p.nkb = p.nkb0 = ceil_div(T, 64);
-    FFN_TRY(launch_ffn_pair(kFfnDw, p, ffn_pair_tiles(p, kFfnDw, h->ctas), h->ctas, stream));
-    ++h->launches;
-  }
+  const auto add_dw = [&](const void* a, long long lda, int M, const void* b, long long ldb, int N, void* out) {
+    const int i = add(M, N, out);
+    return map_n(&p.a[i], a, M, T, lda) && map_n(&p.b[i], b, N, T, ldb);
+  };
+  if (dwg) ok = ok && add_dw(h->dg, F, F, x, ldx, d, dwg);
+  if (dwu) ok = ok && add_dw(h->du, F, F, x, ldx, d, dwu);
+  if (dwd) ok = ok && add_dw(dy, lddy, d, h->hid, F, F, dwd);
+  if (!ok) return LMOE_ERR_CUDA;
+  p.nkb = ceil_div(T, 64);
+  FFN_TRY(launch_ffn_pair(kFfnGrads, p, ffn_pair_tiles(p, kFfnGrads, h->ctas), h->ctas, stream));
+  h->launches = 2;
   return LMOE_OK;
 }
 

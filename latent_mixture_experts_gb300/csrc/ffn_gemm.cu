@@ -47,6 +47,27 @@ struct Tile {
   int prod, m, n;
   bool narrow;
 };
+// The tiles of a pair, round by round: item `round` of pair `pair` of `pairs`, -1
+// for none in this round, -2 at the end.  Tiles are dealt out in turn, except
+// that a dx tile counts for `delta` of the weight gradients' (their K ranges
+// differ): the pairs that get one more dx tile sit out delta - 1 rounds.
+__device__ __forceinline__ int item_of(const FfnPairParams& p, int total, int round, int pair, int pairs) {
+  const int k1 = p.n1 / pairs, r = p.n1 - k1 * pairs;
+  if (round < k1) return round * pairs + pair;
+  round -= k1;
+  int i;
+  if (r == 0) {
+    i = round * pairs + pair;
+  } else if (round < p.delta) {
+    if (pair < r) return round == 0 ? k1 * pairs + pair : -1;
+    i = round * (pairs - r) + pair - r;
+  } else {
+    i = p.delta * (pairs - r) + (round - p.delta) * pairs + pair;
+  }
+  i += p.n1;
+  return i < total ? i : -2;
+}
+
 __device__ __forceinline__ Tile tile_of(const FfnPairParams& p, int i) {
   Tile t;
   t.narrow = i >= p.full;
@@ -167,8 +188,7 @@ __device__ __forceinline__ bool epilogue_row(const FfnPairParams& p, const Tile&
 
 template <int MODE, int ACT, int TN>
 __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_constant__ FfnPairParams p) {
-  constexpr bool kAMn = MODE == kFfnDw;
-  constexpr bool kBMn = MODE == kFfnDHid || MODE == kFfnDx || MODE == kFfnDw;
+  constexpr bool kBMn = MODE == kFfnDHid || MODE == kFfnGrads;
   using C = PairCfg<TN>;
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -206,10 +226,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
   if (warp == 0) {
     uint32_t it = 0;
     bool ok = true;
-    for (int i = first; i < total && ok; i += pairs) {
+    for (int round = 0; ok; ++round) {
+      const int i = item_of(p, total, round, first, pairs);
+      if (i == -1) continue;
+      if (i < 0) break;
       const Tile t = tile_of(p, i);
       const int m0 = t.m * 256 + 128 * static_cast<int>(rank);
-      for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+      const bool dx = MODE == kFfnGrads && p.cat && t.prod == 0, a_mn = MODE == kFfnGrads && !dx;
+      const int nkb = dx ? 2 * p.nkb_cat : p.nkb;
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
         const uint32_t s = it % kStages;
         if (it >= kStages && !warp_wait(&empty[s], ((it / kStages) - 1) & 1, p.err)) {
           ok = false;
@@ -220,16 +245,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
         const uint32_t bar = map_rank(&full[s], 0);
         uint8_t* sa = sm + s * C::kStage;
         uint8_t* sb = sa + C::kA;
-        int src = t.prod, k0 = kb * 64;
-        if (MODE == kFfnDx && kb >= p.nkb0) {
-          src = 1;
-          k0 = (kb - p.nkb0) * 64;
-        }
-        if constexpr (kAMn) {
-          w_load_2d_pair(sa, &p.a[src], bar, m0, k0);
-          w_load_2d_pair(sa + 8192, &p.a[src], bar, m0 + 64, k0);
+        const bool second = dx && kb >= p.nkb_cat;      // the concatenation's second half
+        const int k0 = (second ? kb - p.nkb_cat : kb) * 64;
+        const CUtensorMap* A = second ? &p.a_cat : &p.a[t.prod];
+        const CUtensorMap* Bm = second ? &p.b_cat : &p.b[t.prod];
+        if (a_mn) {
+          w_load_2d_pair(sa, A, bar, m0, k0);
+          w_load_2d_pair(sa + 8192, A, bar, m0 + 64, k0);
         } else {
-          w_load_2d_pair(sa, &p.a[src], bar, k0, m0);
+          w_load_2d_pair(sa, A, bar, k0, m0);
         }
         if constexpr (MODE == kFfnGateUp) {   // gate rows in the even CTA, up rows in the odd one
           if (half)
@@ -238,13 +262,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
             w_load_2d_pair(sb, &p.b[rank], bar, k0, t.n * (TN / 2));
         } else if constexpr (kBMn) {
           const int width = half ? TN / 2 : TN, n0 = t.n * width + width / 2 * static_cast<int>(rank);
-          w_load_2d_pair(sb, &p.b[src], bar, n0, k0);
-          if (TN == 256 && !half) w_load_2d_pair(sb + 8192, &p.b[src], bar, n0 + 64, k0);
+          w_load_2d_pair(sb, Bm, bar, n0, k0);
+          if (TN == 256 && !half) w_load_2d_pair(sb + 8192, Bm, bar, n0 + 64, k0);
         } else {
           if (half)
-            w_load_2d_pair(sb, &p.b_half[src], bar, k0, t.n * (TN / 2) + TN / 4 * static_cast<int>(rank));
+            w_load_2d_pair(sb, &p.b_half[0], bar, k0, t.n * (TN / 2) + TN / 4 * static_cast<int>(rank));
           else
-            w_load_2d_pair(sb, &p.b[src], bar, k0, t.n * TN + TN / 2 * static_cast<int>(rank));
+            w_load_2d_pair(sb, Bm, bar, k0, t.n * TN + TN / 2 * static_cast<int>(rank));
         }
       }
     }
@@ -259,31 +283,38 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
     }
   } else if (warp == 1) {
     if (rank == 0) {
-      constexpr uint32_t major = (kAMn ? kIdescAMajorMn : 0u) | (kBMn ? kIdescBMajorMn : 0u);
       const uint32_t base = smem_u32(sm);
-      const uint64_t a_desc = kAMn ? sdesc_sw128_mn(base, 8192) : sdesc_sw128(base);
       const uint64_t b_desc = kBMn ? sdesc_sw128_mn(base + C::kA, 8192) : sdesc_sw128(base + C::kA);
       uint32_t it = 0, n = 0;
       bool ok = true;
-      for (int i = first; i < total && ok; i += pairs, ++n) {
+      for (int round = 0; ok; ++round) {
+        const int i = item_of(p, total, round, first, pairs);
+        if (i == -1) continue;
+        if (i < 0) break;
         const uint32_t b = n & 1, use = n >> 1;
+        ++n;
         if (use > 0 && !warp_wait(&acc_empty[b], (use - 1) & 1, p.err)) break;
         tc_fence_after();
         const uint32_t d = tbase + b * TN;
-        const uint32_t idesc = TN == 256 && i >= p.full ? idesc_bf16(256, TN / 2) | major : idesc_bf16(256, TN) | major;
-        for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+        const bool dx = MODE == kFfnGrads && p.cat && tile_of(p, i).prod == 0, a_mn = MODE == kFfnGrads && !dx;
+        const int nkb = dx ? 2 * p.nkb_cat : p.nkb;
+        const uint32_t idesc = idesc_bf16(256, TN == 256 && i >= p.full ? TN / 2 : TN) | (a_mn ? kIdescAMajorMn : 0u) |
+                               (kBMn ? kIdescBMajorMn : 0u);
+        // descriptors count 16-byte units: a step of 16 along K is 32 bytes of a
+        // K-contiguous row, or 16 rows of 128 bytes
+        const uint64_t a_desc = a_mn ? sdesc_sw128_mn(base, 8192) : sdesc_sw128(base);
+        const uint32_t a_step = a_mn ? 128 : 2;
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
           const uint32_t s = it % kStages;
           if (!warp_wait(&full[s], (it / kStages) & 1, p.err)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          // descriptors count 16-byte units: a step of 16 along K is 32 bytes of
-          // a K-contiguous row, or 16 rows of 128 bytes
           const uint64_t ad = a_desc + s * (C::kStage >> 4), bd = b_desc + s * (C::kStage >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            w_mma_bf16_pair(d, ad + k * (kAMn ? 128 : 2), bd + k * (kBMn ? 128 : 2), idesc, (kb | k) != 0);
+            w_mma_bf16_pair(d, ad + k * a_step, bd + k * (kBMn ? 128 : 2), idesc, (kb | k) != 0);
           w_commit_pair(&empty[s]);
         }
         if (ok) w_commit_pair(&acc_full[b]);
@@ -293,10 +324,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
     const int q = warp & 3;
     const uint32_t remote_empty[2] = {map_rank(&acc_empty[0], 0), map_rank(&acc_empty[1], 0)};
     uint32_t n = 0;
-    for (int i = first; i < total; i += pairs, ++n) {
-      const uint32_t b = n & 1;
+    for (int round = 0;; ++round) {
+      const int i = item_of(p, total, round, first, pairs);
+      if (i == -1) continue;
+      if (i < 0) break;
+      const uint32_t b = n & 1, use = n >> 1;
+      ++n;
       const auto ready = [&] {
-        const bool ok = mbar_wait_cluster(&acc_full[b], (n >> 1) & 1, p.err, kErrTimeout);
+        const bool ok = mbar_wait_cluster(&acc_full[b], use & 1, p.err, kErrTimeout);
         tc_fence_after();
         return __all_sync(0xFFFFFFFFu, ok) != 0;
       };
@@ -355,23 +390,35 @@ int ffn_pair_tiles(FfnPairParams& p, FfnMode mode, int ctas) {
   };
   // 1 where every output row starts on a 32-byte boundary
   for (int i = 0; i < p.nprod; ++i) p.wide[i] = p.N[i] % 16 == 0 && reinterpret_cast<uintptr_t>(p.out[i]) % 32 == 0;
-  if (p.nprod == 1)
+  if (mode == kFfnGateUp || mode == kFfnDHid)           // three outputs of one product
     for (int i = 1; i < 3; ++i) p.wide[0] = p.wide[0] && reinterpret_cast<uintptr_t>(p.out[i]) % 32 == 0;
   // With all SMs busy a narrow tile takes 0.55 to 0.58 of a wide one's time
   // (4096 tokens at 7168 x 6144: forward 650 us against 593 us); 1003 tokens at
   // 1152 x 864, which leave half of the wide grid idle: 15.9 us against
-  // 22.8 us.  A last wave of wide tiles that fills at most half of the pairs is
-  // cut into halves.
+  // 22.8 us.  A last round of wide tiles that fills at most half of the pairs
+  // is cut into halves.  Tiles cost their K blocks, the epilogue's time at least.
   constexpr float kNarrow = 0.57f;
-  const int pairs = ctas / 2, narrow = (tiles(128) + pairs - 1) / pairs;
-  const int all = tiles(256), rest = all % pairs;       // leaves the wide tiling in p
-  const bool cut = all > pairs && rest > 0 && 2 * rest <= pairs;
-  const float wide = all / pairs + (rest == 0 ? 0.0f : cut ? kNarrow : 1.0f);
-  if (kNarrow * narrow < wide) {
-    p.full = tiles(128);
+  const auto cost = [](int nkb) { return static_cast<float>(nkb < 12 ? 14 : nkb + 2); };
+  const int pairs = ctas / 2;
+  const float c2 = cost(p.nkb), c1 = p.cat ? cost(2 * p.nkb_cat) : c2;
+  p.delta = c1 > c2 ? static_cast<int>(c1 / c2 + 0.5f) : 1;
+  int rest = 0, cut = 0;
+  const auto rounds = [&](int tn) {          // of a pair, in c2; rest: the tiles of the last one
+    const int all = tiles(tn);
+    p.n1 = p.cat ? p.tile_end[0] : 0;
+    const int k1 = p.n1 / pairs, r = p.n1 % pairs, slots = all - p.n1 + r * p.delta, n = slots / pairs;
+    rest = slots % pairs;
+    cut = tn == 256 && rest > 0 && 2 * rest <= pairs && rest <= all - p.n1 && n >= (r > 0 ? p.delta : k1 > 0 ? 0 : 1);
+    const float others = n + (rest == 0 ? 0.0f : cut ? kNarrow : 1.0f), dx = r > 0 ? c1 / c2 : 0.0f;
+    return k1 * c1 / c2 + (others > dx ? others : dx);
+  };
+  const float narrow = kNarrow * rounds(128), wide = rounds(256);   // leaves the wide tiling in p
+  if (narrow < wide) {
+    rounds(128);
+    p.full = p.tile_end[p.nprod - 1];
     return 128;
   }
-  p.full = cut ? all - rest : all;
+  p.full = p.tile_end[p.nprod - 1] - (cut ? rest : 0);
   return 256;
 }
 
@@ -381,8 +428,7 @@ cudaError_t launch_ffn_pair(FfnMode mode, const FfnPairParams& p, int tn, int ct
     case kFfnGateUp: return sw ? launch<kFfnGateUp, 1>(p, tn, ctas, s) : launch<kFfnGateUp, 0>(p, tn, ctas, s);
     case kFfnPlain: return launch<kFfnPlain, 0>(p, tn, ctas, s);
     case kFfnDHid: return sw ? launch<kFfnDHid, 1>(p, tn, ctas, s) : launch<kFfnDHid, 0>(p, tn, ctas, s);
-    case kFfnDx: return launch<kFfnDx, 0>(p, tn, ctas, s);
-    case kFfnDw: return launch<kFfnDw, 0>(p, tn, ctas, s);
+    case kFfnGrads: return launch<kFfnGrads, 0>(p, tn, ctas, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -25,25 +25,28 @@ enum FfnMode {
   kFfnGateUp = 0,   // A = x, B = gate | up rows of half a tile's features; out0 = act(g, u), out1/out2 = g, u when set
   kFfnPlain = 1,    // A, B stored K contiguous; out0
   kFfnDHid = 2,     // B stored N contiguous; out0 = dg, out1 = du, out2 = hid from in_g, in_u
-  kFfnDx = 3,       // B stored N contiguous, K concatenated over two (A, B); out0
-  kFfnDw = 4        // A and B stored M / N contiguous; up to three products out[i] = A[i]^T B[i]
+  kFfnGrads = 3     // up to four products, all with B stored N contiguous: with `cat` first dx, A stored K contiguous and
+                    // K concatenated over (a[0], b[0]) and (a_cat, b_cat); then out[i] = A[i]^T B[i], A stored M contiguous
 };
+constexpr int kPairProducts = 4;
 struct FfnPairParams {
-  CUtensorMap a[3], b[3];
+  CUtensorMap a[kPairProducts], b[kPairProducts], a_cat, b_cat;
   CUtensorMap b_half[2];      // K-contiguous b with boxes of half as many rows
-  void* out[3];
+  void* out[kPairProducts];
   const void *in_g, *in_u;
-  int M[3], N[3];             // output rows and columns of each product
-  int tiles_n[3], tile_end[3], nprod;
+  int M[kPairProducts], N[kPairProducts];   // output rows and columns of each product
+  int tiles_n[kPairProducts], tile_end[kPairProducts], nprod;
   int full;                   // tiles from here on are worked in halves of their columns
-  int wide[3];                // outputs whose rows start on 32-byte boundaries
-  int nkb, nkb0;              // 64-wide K blocks in all; of the first (A, B) of a concatenation
+  int wide[kPairProducts];    // outputs whose rows start on 32-byte boundaries
+  int nkb;                    // 64-wide K blocks
+  int cat, nkb_cat;           // kFfnGrads: the first product is dx, of 2 * nkb_cat K blocks
+  int n1, delta;              // its tiles, and how many of the others one of them counts for
   float b1, b2;
   int act;
   int* err;
 };
 // Chooses the tile width (128 or 256) for M, N, nprod and out and fills
-// tiles_n, tile_end, full and wide; K-contiguous b maps have boxes of half of
+// tiles_n, tile_end, full, n1, delta and wide; K-contiguous b maps have boxes of half of
 // it, b_half (width 256) of a quarter.
 int ffn_pair_tiles(FfnPairParams& p, FfnMode mode, int ctas);
 cudaError_t launch_ffn_pair(FfnMode mode, const FfnPairParams& p, int tn, int ctas, cudaStream_t s);
@@ -55,7 +58,7 @@ cudaError_t ffn_pair_ctas(int* ctas);
 constexpr int kSkinnyMaxTokens = 96;
 constexpr int kSkinnyMaxStages = 16;
 constexpr int kSkinnyMaxSplits = 8;    // K splits: the portable cluster size
-constexpr int kSkinnySmem = 110 * 1024;
+constexpr int kSkinnySmem = 110 * 1024;   // two CTAs on an SM; with 74 KB and three, one token at 7168 x 6144 48.6 us against 46.5 us
 struct FfnSkinnyParams {
   // whole (K a multiple of 64): a (64, T, K/64), b (64, features, K/64) or, gate/up, (64, features, 2, K/64),
   // boxes of tb / rows and kc chunks; else a (K, T), b (K, features[, 2]), one box per 64-wide chunk

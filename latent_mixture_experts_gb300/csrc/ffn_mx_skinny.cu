@@ -24,6 +24,7 @@ constexpr int kB = kN * 128;             // codes of a 128-wide K block
 constexpr int kMaxStages = 8;            // 8 columns of scales each, beside 128 of sums
 constexpr int kTmem = 256, kSfCols = 8;
 constexpr int kSfb = 512;
+constexpr int kMxSkinnySmem = 110 * 1024;   // two CTAs on an SM
 constexpr int kPitch = kN + 4;           // floats of a token's partial sums: 16-byte rows, four banks apart
 // Up to here rather than the pair tiles: 64 tokens at widths 7168 and 6144 take
 // 42 us here and 39 us there, at 7168 and 2048 21 us and 27 us, at 2048 and 2048
@@ -214,9 +215,9 @@ __global__ void __launch_bounds__(kThreads) ffn_mx_skinny_kernel(const __grid_co
 template <bool GU, int ACT>
 cudaError_t launch(const FfnMxSkinnyParams& p, cudaStream_t s) {
   static const cudaError_t attr =
-      cudaFuncSetAttribute(ffn_mx_skinny_kernel<GU, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSkinnySmem);
+      cudaFuncSetAttribute(ffn_mx_skinny_kernel<GU, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSkinnySmem);
   if (attr != cudaSuccess) return attr;
-  return launch_pdl_cluster(ffn_mx_skinny_kernel<GU, ACT>, dim3(p.tiles * p.splits), dim3(kThreads), kSkinnySmem,
+  return launch_pdl_cluster(ffn_mx_skinny_kernel<GU, ACT>, dim3(p.tiles * p.splits), dim3(kThreads), kMxSkinnySmem,
                             p.splits, s, p);
 }
 
@@ -233,7 +234,7 @@ bool ffn_mx_skinny_plan(FfnMxSkinnyParams& p, bool gate_up) {
     if (n > p.nkb || !((ctas < 110 && left >= 2) || (ctas < 150 && left >= 6))) break;
     p.splits = n;
   }
-  const int budget = kSkinnySmem - 1024;
+  const int budget = kMxSkinnySmem - 1024;
   const int sfa = (p.nkb + p.splits - 1) / p.splits * 512;
   const int recv = 4 * p.splits * ((p.T + p.splits - 1) / p.splits) * kPitch;
   // the partial sums meet behind the ring, or over it where room behind would cost a stage
