@@ -25,7 +25,7 @@ struct lmoe_ffn_ctx {
   CUtensorMap gate[2], up[2], down[2];
   CUtensorMap gate_n, up_n, down_n;   // the same memory as N contiguous operands, boxes of 64 x 64
   // MXFP8 blocks: hid holds codes; scale atoms of x, hid and the weights
-  // (of the pair tiles, and [1] of the small-batch tiles)
+  // (for tiles of 192 and of 128 rows)
   uint8_t *x_sf = nullptr, *hid_sf = nullptr, *gu_sf[2] = {}, *down_sf[2] = {};
   CUtensorMap m_x_sf, m_hid_sf, m_gu_sf[2], m_down_sf[2];
   int launches = 0;
@@ -194,13 +194,13 @@ lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* 
   // scale atoms: 512 bytes for 128 rows x 128 values
   const size_t kd = ceil_div(d, 128), kf = ceil_div(F, 128);
   const size_t x_sf = T256 / 128 * kd * 512, hid_sf = T256 / 128 * kf * 512;
-  // tiles of the weights' atoms: pair tiles (two atoms for 192 rows), small-batch tiles (one for 128)
-  const int width[2] = {kMxTileN, kMxSkinnyN}, per[2] = {1024, 512};
+  // the weights' atoms for both tile widths: two atoms for 192 rows, one for 128
+  const int per[2] = {1024, 512};
   size_t gu_sf[2], down_sf[2], w_sf = 0;
   int gu_tiles[2], down_tiles[2];
   for (int i = 0; i < 2; ++i) {
-    gu_tiles[i] = ceil_div(F, width[i] / 2);
-    down_tiles[i] = ceil_div(d, width[i]);
+    gu_tiles[i] = ceil_div(F, kMxTileN[i] / 2);
+    down_tiles[i] = ceil_div(d, kMxTileN[i]);
     gu_sf[i] = gu_tiles[i] * kd * per[i];
     down_sf[i] = down_tiles[i] * kf * per[i];
     w_sf += gu_sf[i] + down_sf[i];
@@ -226,13 +226,13 @@ lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* 
     ok = map_atoms(&h->m_x_sf, h->x_sf, x_sf, 1) && map_atoms(&h->m_hid_sf, h->hid_sf, hid_sf, 1);
     uint8_t* at = h->hid_sf + hid_sf;
     for (int i = 0; i < 2 && ok && e == cudaSuccess; ++i) {
-      const int box = i == 0 ? kMxTileN / 2 : kMxSkinnyN / 2;
+      const int box = kMxTileN[i] / 2;
       h->gu_sf[i] = at;
       h->down_sf[i] = at + gu_sf[i];
       at += gu_sf[i] + down_sf[i];
-      e = launch_mx_weight_atoms(w->gate_s, w->up_s, F, d, width[i], gu_tiles[i], h->gu_sf[i], stream);
+      e = launch_mx_weight_atoms(w->gate_s, w->up_s, F, d, kMxTileN[i], gu_tiles[i], h->gu_sf[i], stream);
       if (e == cudaSuccess)
-        e = launch_mx_weight_atoms(w->down_s, nullptr, d, F, width[i], down_tiles[i], h->down_sf[i], stream);
+        e = launch_mx_weight_atoms(w->down_s, nullptr, d, F, kMxTileN[i], down_tiles[i], h->down_sf[i], stream);
       ok = map_mx(&h->gate[i], w->gate, d, F, box) && map_mx(&h->up[i], w->up, d, F, box) &&
            map_mx(&h->down[i], w->down, F, d, box) && map_atoms(&h->m_gu_sf[i], h->gu_sf[i], gu_sf[i], per[i] / 512) &&
            map_atoms(&h->m_down_sf[i], h->down_sf[i], down_sf[i], per[i] / 512);
@@ -442,31 +442,30 @@ lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8
   p.b2 = h->cfg.situ_linear_beta;
   p.act = h->cfg.act == LMOE_ACT_SWIGLU;
   p.err = h->err;
-  p.b[0] = h->gate[0];
-  p.b[1] = h->up[0];
   p.sfa = h->m_x_sf;
-  p.sfb = h->m_gu_sf[0];
   p.out = h->hid;
   p.out_sf = h->hid_sf;
   p.out_nkb = ceil_div(F, 128);
   p.M = T;
   p.N = F;
-  p.tiles_n = ceil_div(F, kMxTileN / 2);
-  p.tiles = ceil_div(T, 256) * p.tiles_n;
   p.nkb = ceil_div(d, 128);
+  int tn = ffn_mx_tiles(p, true, h->ctas), i = tn == kMxTileN[1];
+  p.b[0] = h->gate[i];
+  p.b[1] = h->up[i];
+  p.sfb = h->m_gu_sf[i];
   if (!map_mx(&p.a, x, d, T, 128)) return LMOE_ERR_CUDA;
-  FFN_TRY(launch_ffn_mx_pair(p, true, h->ctas, stream));
-  p.b[0] = h->down[0];
+  FFN_TRY(launch_ffn_mx_pair(p, true, tn, h->ctas, stream));
   p.sfa = h->m_hid_sf;
-  p.sfb = h->m_down_sf[0];
   p.out = out;
   p.wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;   // d is a multiple of 32
   p.N = d;
-  p.tiles_n = ceil_div(d, kMxTileN);
-  p.tiles = ceil_div(T, 256) * p.tiles_n;
   p.nkb = ceil_div(F, 128);
+  tn = ffn_mx_tiles(p, false, h->ctas);
+  i = tn == kMxTileN[1];
+  p.b[0] = h->down[i];
+  p.sfb = h->m_down_sf[i];
   if (!map_mx(&p.a, h->hid, F, T, 128)) return LMOE_ERR_CUDA;
-  FFN_TRY(launch_ffn_mx_pair(p, false, h->ctas, stream));
+  FFN_TRY(launch_ffn_mx_pair(p, false, tn, h->ctas, stream));
   h->launches = 3;
   return LMOE_OK;
 }

@@ -83,10 +83,11 @@ bool ffn_skinny_plan(FfnSkinnyParams& p, bool gate_up);
 cudaError_t launch_ffn_skinny(const FfnSkinnyParams& p, bool gate_up, int act, cudaStream_t s);
 
 // ------------------------------------------------------------ MXFP8 passes
-constexpr int kMxTileN = 192;   // weight rows of a tile: 96 gate and 96 up rows, or 192 output features
+// Weight rows of a tile: half gate and half up rows, or output features.
+constexpr int kMxTileN[2] = {192, 128};
 struct FfnMxParams {
-  CUtensorMap a, b[2];          // codes, boxes of 128 K values x 128 (a) or 96 (b) rows
-  CUtensorMap sfa, sfb;         // scale atoms [row / 128][nkb], [tile][nkb][2] of 128 32-bit words; boxes of 1 and 2
+  CUtensorMap a, b[2];          // codes, boxes of 128 K values x 128 rows (a) or half a tile's (b)
+  CUtensorMap sfa, sfb;         // scale atoms [row / 128][nkb], [tile][nkb][2 or 1] of 128 32-bit words, boxes of 1 and 2 or 1
   void* out;                    // gate/up: hidden codes [M][N]; else bf16 [M][N]
   uint8_t* out_sf;              // gate/up: the hidden activation's atoms
   int out_nkb;
@@ -97,7 +98,9 @@ struct FfnMxParams {
   int act;
   int* err;
 };
-cudaError_t launch_ffn_mx_pair(const FfnMxParams& p, bool gate_up, int ctas, cudaStream_t s);
+// Chooses the tile width for M and N and fills tiles_n and tiles.
+int ffn_mx_tiles(FfnMxParams& p, bool gate_up, int ctas);
+cudaError_t launch_ffn_mx_pair(const FfnMxParams& p, bool gate_up, int tn, int ctas, cudaStream_t s);
 // Scales [T][K/32] -> atoms; bytes of blocks past K/32 keep the zeros that the
 // buffer is created with where a group of four is not begun.
 cudaError_t launch_mx_row_atoms(const uint8_t* s, int T, int K, uint8_t* out, cudaStream_t stream);
@@ -107,7 +110,7 @@ cudaError_t launch_mx_weight_atoms(const uint8_t* a, const uint8_t* up, int rows
                                    uint8_t* out, cudaStream_t stream);
 
 // Small batches: K split over clusters, as in the bf16 form.
-constexpr int kMxSkinnyN = 128;   // weight rows of a tile: 64 gate and 64 up rows, or 128 output features
+constexpr int kMxSkinnyN = kMxTileN[1];
 struct FfnMxSkinnyParams {
   CUtensorMap a, b[2], sfb;     // codes: boxes of 128 K values x tb and 64 rows; the weights' atoms [tile][nkb]
   const uint8_t* row_sf;        // gate/up: x's scales [T][kblks]; else hid's atoms

@@ -1,6 +1,7 @@
 // The feed-forward block on MXFP8 operands (E4M3 codes, one E8M0 scale per 32
 // values along K): kind::mxf8f6f4 block-scaled tcgen05, scales applied by the
-// tensor cores, fp32 accumulation, on 256 x 192 tiles of CTA pairs.
+// tensor cores, fp32 accumulation, on 256 x 192 tiles of CTA pairs (256 x 128
+// where those leave pairs idle).
 //
 // The structure is that of the bf16 pair tiles.  N = 192 rather than 256: two
 // accumulators and seven stages' scales (12 columns each) fit tensor memory,
@@ -18,22 +19,27 @@
 // front.
 #include "ffn_act.cuh"
 #include "ffn_internal.h"
-#include "lmoe_internal.h"
 #include "issue.cuh"
+#include "lmoe_internal.h"
 
 namespace lmoe {
 namespace {
 
-constexpr int kHalfN = kMxTileN / 2;                 // B rows of each CTA
-constexpr int kOperandA = 128 * 128, kOperandB = kHalfN * 128;
-constexpr int kStage = kOperandA + kOperandB;
-constexpr int kSf = 512 + 1024;                      // A atom, two B atoms
-constexpr int kStages = 7;
-constexpr int kSmem = kStages * (kStage + kSf) + 1024;
+// TN: weight rows of a tile, 192 or 128.
+template <int TN>
+struct MxCfg {
+  static constexpr int kHalf = TN / 2;                     // B rows of each CTA
+  static constexpr int kA = 128 * 128, kB = kHalf * 128;
+  static constexpr int kStage = kA + kB;
+  static constexpr int kAtoms = (TN + 127) / 128;          // scale atoms of B
+  static constexpr int kSf = 512 * (1 + kAtoms);
+  static constexpr int kStages = TN == 192 ? 7 : 8;
+  static constexpr int kSmem = kStages * (kStage + kSf) + 1024;
+  static constexpr int kSfCols = 4 * (1 + kAtoms), kSfBase = 2 * TN;
+  static_assert(kStage % 1024 == 0 && kSmem <= 227 * 1024 && kSfBase + kStages * kSfCols <= 512, "budgets");
+};
 constexpr int kThreads = 320;                        // TMA, MMA, 8 epilogue warps: two for each lane quarter
-constexpr int kSfCols = 12, kSfBase = 2 * kMxTileN;
 constexpr int kTileRows = 8;
-static_assert(kStage % 1024 == 0 && kSmem <= 227 * 1024 && kSfBase + kStages * kSfCols <= 512, "budgets");
 
 __device__ __forceinline__ void tile_of(const FfnMxParams& p, int i, int& m, int& n) {
   const int tm = p.tiles / p.tiles_n;
@@ -70,8 +76,10 @@ __device__ __forceinline__ size_t atom_byte(int row, int kblk, int nkb) {
   return (static_cast<size_t>(row >> 7) * nkb + (kblk >> 2)) * 512 + sf_atom_offset(row & 127, kblk & 3);
 }
 
-template <bool GU, int ACT>
+template <bool GU, int ACT, int TN>
 __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_constant__ FfnMxParams p) {
+  using C = MxCfg<TN>;
+  constexpr int kStages = C::kStages, kStage = C::kStage, kSf = C::kSf, kHalfN = C::kHalf;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   uint8_t* sf = sm + kStages * kStage;
@@ -112,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
       int m, n;
       tile_of(p, i, m, n);
       const int m0 = m * 256 + 128 * rank;
-      const int atom_a = (2 * m + rank) * p.nkb, atom_b = 2 * n * p.nkb;
+      const int atom_a = (2 * m + rank) * p.nkb, atom_b = C::kAtoms * n * p.nkb;
       for (int kb = 0; kb < p.nkb; ++kb, ++it) {
         const uint32_t s = it % kStages;
         if (it >= kStages && !warp_wait(&empty[s], ((it / kStages) - 1) & 1, p.err)) {
@@ -124,11 +132,11 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
         uint8_t* sa = sm + s * kStage;
         w_load_2d_pair(sa, &p.a, bar, kb * 128, m0);
         if constexpr (GU)      // gate rows in the even CTA, up rows in the odd one
-          w_load_2d_pair(sa + kOperandA, &p.b[rank], bar, kb * 128, n * kHalfN);
+          w_load_2d_pair(sa + C::kA, &p.b[rank], bar, kb * 128, n * kHalfN);
         else
-          w_load_2d_pair(sa + kOperandA, &p.b[0], bar, kb * 128, n * kMxTileN + rank * kHalfN);
+          w_load_2d_pair(sa + C::kA, &p.b[0], bar, kb * 128, n * TN + rank * kHalfN);
         w_load_2d_pair(sf + s * kSf, &p.sfa, bar, 0, atom_a + kb);
-        w_load_2d_pair(sf + s * kSf + 512, &p.sfb, bar, 0, atom_b + 2 * kb);   // both CTAs need all N scales
+        w_load_2d_pair(sf + s * kSf + 512, &p.sfb, bar, 0, atom_b + C::kAtoms * kb);   // both CTAs need all N scales
       }
     }
     // every stage has been read before the pair may leave; after a wait that
@@ -141,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
     }
   } else if (warp == 1) {
     if (rank == 0) {
-      const uint64_t a_desc = sdesc_sw128(smem_u32(sm)), b_desc = sdesc_sw128(smem_u32(sm) + kOperandA);
+      const uint64_t a_desc = sdesc_sw128(smem_u32(sm)), b_desc = sdesc_sw128(smem_u32(sm) + C::kA);
       const uint64_t sf_desc = sdesc_noswz(smem_u32(sf), 16, 128);
       uint32_t it = 0, n = 0;
       bool ok = true;
@@ -149,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
         const uint32_t b = n & 1, use = n >> 1;
         if (use > 0 && !warp_wait(&acc_empty[b], (use - 1) & 1, p.err)) break;
         tc_fence_after();
-        const uint32_t d = tbase + b * kMxTileN;
+        const uint32_t d = tbase + b * TN;
         for (int kb = 0; kb < p.nkb; ++kb, ++it) {
           const uint32_t s = it % kStages;
           if (!warp_wait(&full[s], (it / kStages) & 1, p.err)) {
@@ -159,12 +167,12 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
           tc_fence_after();
           const uint64_t ad = a_desc + s * (kStage >> 4), bd = b_desc + s * (kStage >> 4);
           const uint64_t sd = sf_desc + s * (kSf >> 4);
-          const uint32_t sfa = tbase + kSfBase + s * kSfCols;
+          const uint32_t sfa = tbase + C::kSfBase + s * C::kSfCols;
 #pragma unroll
-          for (int k = 0; k < 3; ++k) w_copy_atom_pair(sfa + 4 * k, sd + 32 * k);
+          for (int k = 0; k < 1 + C::kAtoms; ++k) w_copy_atom_pair(sfa + 4 * k, sd + 32 * k);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            w_mma_mx_pair(d, ad + 2 * k, bd + 2 * k, idesc_mxf8f6f4(256, kMxTileN, 0, 0, k, k), sfa, sfa + 4,
+            w_mma_mx_pair(d, ad + 2 * k, bd + 2 * k, idesc_mxf8f6f4(256, TN, 0, 0, k, k), sfa, sfa + 4,
                           (kb | k) != 0);
           w_commit_pair(&empty[s]);
         }
@@ -184,11 +192,12 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
       int m, n;
       tile_of(p, i, m, n);
       const int row0 = m * 256 + 128 * rank + 32 * q, row = row0 + lane;
-      const uint32_t acc = tbase + b * kMxTileN + (static_cast<uint32_t>(32 * q) << 16);
+      const uint32_t acc = tbase + b * TN + (static_cast<uint32_t>(32 * q) << 16);
       if (row0 < p.M) {
         if constexpr (GU) {
+          constexpr int kFirst = (kHalfN / 32 + 1) / 2 * 32;   // two of three 32-value blocks, or one of two
 #pragma unroll 1
-          for (int c = 64 * half; c < (half ? kHalfN : 64); c += 32) {   // two of the three blocks, or the third
+          for (int c = kFirst * half; c < (half ? kHalfN : kFirst); c += 32) {
             const int f = n * kHalfN + c;
             if (f >= p.N) break;
             uint32_t g[32], u[32];
@@ -203,10 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
                                  p.out_sf + atom_byte(row, f >> 5, p.out_nkb));
           }
         } else {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(row) * p.N + n * kMxTileN;
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(row) * p.N + n * TN;
 #pragma unroll 1
           for (int c = kHalfN * half; c < kHalfN * (half + 1); c += 32) {
-            const int left = p.N - n * kMxTileN - c;
+            const int left = p.N - n * TN - c;
             if (left <= 0) break;
             uint32_t v[32], w[16];
             tmem_ld32(acc + c, v);
@@ -272,13 +281,17 @@ __global__ void mx_weight_atoms_kernel(const uint8_t* __restrict__ a, const uint
   }
 }
 
-template <bool GU, int ACT>
-cudaError_t launch(const FfnMxParams& p, int ctas, cudaStream_t s) {
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(ffn_mx_pair_kernel<GU, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+template <bool GU, int ACT, int TN>
+cudaError_t launch_tn(const FfnMxParams& p, int ctas, cudaStream_t s) {
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      ffn_mx_pair_kernel<GU, ACT, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, MxCfg<TN>::kSmem);
   if (attr != cudaSuccess) return attr;
-  return launch_pdl_cluster(ffn_mx_pair_kernel<GU, ACT>, dim3(2 * p.tiles < ctas ? 2 * p.tiles : ctas), dim3(kThreads),
-                            kSmem, 2, s, p);
+  return launch_pdl_cluster(ffn_mx_pair_kernel<GU, ACT, TN>, dim3(2 * p.tiles < ctas ? 2 * p.tiles : ctas),
+                            dim3(kThreads), MxCfg<TN>::kSmem, 2, s, p);
+}
+template <bool GU, int ACT>
+cudaError_t launch(const FfnMxParams& p, int tn, int ctas, cudaStream_t s) {
+  return tn == 192 ? launch_tn<GU, ACT, 192>(p, ctas, s) : launch_tn<GU, ACT, 128>(p, ctas, s);
 }
 
 int ew_blocks(long long n) {
@@ -302,9 +315,25 @@ cudaError_t launch_mx_weight_atoms(const uint8_t* a, const uint8_t* up, int rows
   return cudaGetLastError();
 }
 
-cudaError_t launch_ffn_mx_pair(const FfnMxParams& p, bool gate_up, int ctas, cudaStream_t s) {
-  if (!gate_up) return launch<false, 0>(p, ctas, s);
-  return p.act == 1 ? launch<true, 1>(p, ctas, s) : launch<true, 0>(p, ctas, s);
+int ffn_mx_tiles(FfnMxParams& p, bool gate_up, int ctas) {
+  const auto rounds = [&](int tn) {
+    const int width = gate_up ? tn / 2 : tn;
+    p.tiles_n = (p.N + width - 1) / width;
+    p.tiles = (p.M + 255) / 256 * p.tiles_n;
+    return (p.tiles + ctas / 2 - 1) / (ctas / 2);
+  };
+  // With all SMs busy a 128-row tile takes 0.76 of a 192-row one's time (4096
+  // tokens at 7168 x 6144: 362 us against 319 us); where both leave pairs idle
+  // the narrow ones win (300 tokens at 1152 x 864: 13.4 us against 15.8 us).
+  const int narrow = rounds(128), wide = rounds(192);      // leaves the wide tiling in p
+  if (wide <= 0.76f * narrow) return 192;
+  rounds(128);
+  return 128;
+}
+
+cudaError_t launch_ffn_mx_pair(const FfnMxParams& p, bool gate_up, int tn, int ctas, cudaStream_t s) {
+  if (!gate_up) return launch<false, 0>(p, tn, ctas, s);
+  return p.act == 1 ? launch<true, 1>(p, tn, ctas, s) : launch<true, 0>(p, tn, ctas, s);
 }
 
 }  // namespace lmoe

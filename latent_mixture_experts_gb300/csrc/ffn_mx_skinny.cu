@@ -1,4 +1,4 @@
-// The MXFP8 feed-forward passes on small batches (up to 64 tokens), bound by
+// The MXFP8 feed-forward passes on small batches (up to 48 tokens), bound by
 // streaming the weights' codes and scales once from HBM.
 //
 // As in the bf16 form, tokens are the MMA's M rows, weight rows its N columns
@@ -26,10 +26,11 @@ constexpr int kTmem = 256, kSfCols = 8;
 constexpr int kSfb = 512;
 constexpr int kMxSkinnySmem = 110 * 1024;   // two CTAs on an SM
 constexpr int kPitch = kN + 4;           // floats of a token's partial sums: 16-byte rows, four banks apart
-// Up to here rather than the pair tiles: 64 tokens at widths 7168 and 6144 take
-// 42 us here and 39 us there, at 7168 and 2048 21 us and 27 us, at 2048 and 2048
-// 16.5 us and 18.2 us.  16 tokens at 7168 and 6144: 29 us, 4.7 TB/s of weights.
-constexpr int kMxSkinnyMaxTokens = 64;
+// Up to here rather than the pair tiles: 48 tokens at widths 7168 and 6144 take
+// 37.6 us here and 37.0 us there, at 7168 and 2048 18.5 us and 23.7 us; 64 tokens
+// 41.9 us and 37.2 us, 21.2 us and 22.4 us.  16 tokens at 7168 and 6144: 29.3 us,
+// 4.7 TB/s of weights.
+constexpr int kMxSkinnyMaxTokens = 48;
 static_assert(kN + kMaxStages * kSfCols <= kTmem, "tensor memory");
 
 template <bool GU, int ACT>
