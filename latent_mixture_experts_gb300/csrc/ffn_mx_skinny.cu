@@ -2,10 +2,10 @@
 // streaming the weights' codes and scales once from HBM.
 //
 // As in the bf16 form, tokens are the MMA's M rows, weight rows its N columns
-// (128: one whole scale atom for each 128-wide K block, so the weights' atoms
-// are laid out a second time for these tiles), and a cluster splits K.  Each CTA finishes a share of the tokens with all of the
-// tile's features, so that a warp holds a whole 32-value block of the hidden
-// activation when it encodes it.  The scales of the tokens are put into
+// (128: one whole scale atom for each 128-wide K block), and a cluster splits
+// K.  Each CTA finishes a share of the tokens with all of the tile's features,
+// so that a warp holds a whole 32-value block of the hidden activation when it
+// encodes it.  The scales of the tokens are put into
 // shared memory once, for all of the CTA's K range: x's by the epilogue's
 // warps, which are idle then, from rows as the caller has them; hid's by one
 // bulk copy.  MXFP8 weights do not change while the handle lives, so both
