@@ -455,26 +455,34 @@ __global__ void __launch_bounds__(32 * bwd_max_warps(VPT) + 32) rms_norm_bwd_ker
 }
 
 // dw[c] = sum of part[0..n)[c], in a fixed order: thread (x, y) adds rows y,
-// y + 32, ... of its four columns, and the 32 sums are added in order.
+// y + 32, ... of its four columns; then the four y of a warp, then the warps.
 constexpr int kSumCols = 8, kSumRows = 32;
 __global__ void __launch_bounds__(kSumCols * kSumRows) sum_rows_kernel(const float* part, int n, int d, float* out) {
-  __shared__ float4 s[kSumRows][kSumCols];
+  __shared__ float4 s[kSumRows / 4][kSumCols];
   griddep_launch();
   griddep_wait();
   const int x = threadIdx.x % kSumCols, y = threadIdx.x / kSumCols;
   const int c = (blockIdx.x * kSumCols + x) * 4;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c < d) {
-#pragma unroll 4
+#pragma unroll 5
     for (int r = y; r < n; r += kSumRows) {
       const float4 v = *reinterpret_cast<const float4*>(part + static_cast<size_t>(r) * d + c);
       a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
     }
   }
-  s[y][x] = a;
+#pragma unroll
+  for (int o = kSumCols; o < 32; o *= 2) {
+    a.x += __shfl_xor_sync(0xFFFFFFFFu, a.x, o);
+    a.y += __shfl_xor_sync(0xFFFFFFFFu, a.y, o);
+    a.z += __shfl_xor_sync(0xFFFFFFFFu, a.z, o);
+    a.w += __shfl_xor_sync(0xFFFFFFFFu, a.w, o);
+  }
+  if (y % 4 == 0) s[y / 4][x] = a;
   __syncthreads();
   if (y == 0 && c < d) {
-    for (int r = 1; r < kSumRows; ++r) {
+#pragma unroll
+    for (int r = 1; r < kSumRows / 4; ++r) {
       const float4 v = s[r][x];
       a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
     }
