@@ -545,14 +545,13 @@ cudaError_t launch_fwd(NormParams& p, cudaStream_t s) {
 struct BwdPlan {
   int vpt, warps, groups, grid;
 };
-constexpr int kBwdRows = 4;          // rows of a group at least: each group adds a row of partial sums
 BwdPlan bwd_plan(int T, int d) {
   const RowPlan r = row_plan(d, 512);
   BwdPlan b = {r.vpt, r.warps, bwd_max_warps(r.vpt) / r.warps, 1};
   // one row of the widest types (bf16 and two fp32 values) fits the ring for each group
   const int fit = kRingSmem / (10 * d);
   if (b.groups > fit) b.groups = fit;
-  const int need = (T + kBwdRows * b.groups - 1) / (kBwdRows * b.groups);
+  const int need = (T + b.groups - 1) / b.groups;
   b.grid = need < kRingCtas ? need : kRingCtas;
   return b;
 }
