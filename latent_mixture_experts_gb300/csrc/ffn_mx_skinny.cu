@@ -18,7 +18,9 @@
 namespace lmoe {
 namespace {
 
-constexpr int kThreads = 192;            // TMA, MMA, 4 epilogue warps
+// Warps: 0 = TMA, 1 = MMA, 2-5 read the sums out of tensor memory; all finish
+// them, ten of them for more than 16 tokens.
+constexpr int kThreads = 192, kManyThreads = 320, kManyTokens = 16;
 constexpr int kN = kMxSkinnyN, kHalf = kN / 2;
 constexpr int kB = kN * 128;             // codes of a 128-wide K block
 constexpr int kMaxStages = 8;            // 8 columns of scales each, beside 128 of sums
@@ -34,7 +36,7 @@ constexpr int kMxSkinnyMaxTokens = 48;
 static_assert(kN + kMaxStages * kSfCols <= kTmem, "tensor memory");
 
 template <bool GU, int ACT>
-__global__ void __launch_bounds__(kThreads) ffn_mx_skinny_kernel(const __grid_constant__ FfnMxSkinnyParams p) {
+__global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __grid_constant__ FfnMxSkinnyParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done, rows_ready;
@@ -56,7 +58,7 @@ __global__ void __launch_bounds__(kThreads) ffn_mx_skinny_kernel(const __grid_co
       mbar_init(&empty[i], 1);
     }
     mbar_init(&done, 1);
-    mbar_init(&rows_ready, GU ? 4 : 1);
+    mbar_init(&rows_ready, GU ? blockDim.x / 32 - 2 : 1);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) ffn_mx_skinny_kernel(const __grid_co
   } else if constexpr (GU) {
     // x's scales of this K range, from rows [T][K/32] to the MMA's image
     const int t0 = threadIdx.x - 64;
-    for (int e = t0; e < p.T * steps; e += 128) {
+    for (int e = t0; e < p.T * steps; e += static_cast<int>(blockDim.x) - 64) {
       const int row = e / steps, i = e - row * steps, blk = 4 * (first + i);
       const uint8_t* src = p.row_sf + static_cast<size_t>(row) * p.kblks + blk;
       uint32_t w = 0;
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) ffn_mx_skinny_kernel(const __grid_co
   // CTA's shared memory, one block [per][kPitch] for each source rank.
   const int per = (p.T + p.splits - 1) / p.splits;
   const int q = warp & 3, t = 32 * q + lane;
-  if (warp >= 2 && 32 * q < p.T) {
+  if (warp >= 2 && warp < 6 && 32 * q < p.T) {
     const int owner = t < p.T ? t / per : 0;
     const uint32_t dst = map_rank(recv, owner) + 4 * ((rank * per + t - owner * per) * kPitch);
 #pragma unroll 1
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) ffn_mx_skinny_kernel(const __grid_co
     // one warp for each token and block of 32 features, lane = feature
     constexpr int kBlocks = kHalf / 32;
     const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
-    for (int e = warp; e < kBlocks * ntok; e += kThreads / 32) {
+    for (int e = warp; e < kBlocks * ntok; e += blockDim.x / 32) {
       const int i = e / kBlocks, c = 32 * (e - kBlocks * i), f = tile * kHalf + c;
       if (f >= p.M) continue;
       float g = 0.f, u = 0.f;
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) ffn_mx_skinny_kernel(const __grid_co
         p.out_sf[static_cast<size_t>(f >> 7) * 512 + sf_atom_offset(row, (f >> 5) & 3)] = static_cast<uint8_t>(s);
     }
   } else {
-    for (int e = threadIdx.x; e < ntok * kHalf; e += kThreads) {
+    for (int e = threadIdx.x; e < ntok * kHalf; e += blockDim.x) {
       const int i = e / kHalf, c = 2 * (e - i * kHalf), f = tile * kN + c;
       if (f >= p.M) continue;
       float2 v = make_float2(0.f, 0.f);
@@ -218,7 +220,8 @@ cudaError_t launch(const FfnMxSkinnyParams& p, cudaStream_t s) {
   static const cudaError_t attr =
       cudaFuncSetAttribute(ffn_mx_skinny_kernel<GU, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSkinnySmem);
   if (attr != cudaSuccess) return attr;
-  return launch_pdl_cluster(ffn_mx_skinny_kernel<GU, ACT>, dim3(p.tiles * p.splits), dim3(kThreads), kMxSkinnySmem,
+  return launch_pdl_cluster(ffn_mx_skinny_kernel<GU, ACT>, dim3(p.tiles * p.splits),
+                            dim3(p.T > kManyTokens ? kManyThreads : kThreads), kMxSkinnySmem,
                             p.splits, s, p);
 }
 
