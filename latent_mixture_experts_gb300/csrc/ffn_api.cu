@@ -33,8 +33,11 @@ struct lmoe_ffn_ctx {
 
 namespace {
 
+// A failed call is reported here; the runtime's copy of the error is cleared,
+// so that the caller's next check of its own launches does not find it.
 lmoe_status cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return LMOE_OK;
+  cudaGetLastError();
   return e == cudaErrorMemoryAllocation ? LMOE_ERR_OOM : LMOE_ERR_CUDA;
 }
 #define FFN_TRY(expr)                              \
@@ -83,7 +86,8 @@ bool skinny_maps(FfnSkinnyParams& p, const void* a, long long lda, const void* w
     p.apart = u == v || (u < v ? v - u : u - v) >= (1ull << 40);
   }
   if (p.apart) {
-    if (!make_tmap_2d(&p.b, dt, w0, k, M, row, 64, rows, sw) || !make_tmap_2d(&p.b_up, dt, w1, k, M, row, 64, rows, sw))
+    if (!make_tmap_2d(&p.b, dt, w0, k, M, row, 64, rows, sw) ||
+        !make_tmap_2d(&p.b_up, dt, w1, k, M, row, 64, rows, sw))
       return false;
   } else if (w1) {
     const uint8_t* other = static_cast<const uint8_t*>(w1);
@@ -92,13 +96,14 @@ bool skinny_maps(FfnSkinnyParams& p, const void* a, long long lda, const void* w
     if (p.swapped) base = other;
   }
   if (p.whole) {
-    const bool b = p.apart ? true : w1 ? make_tmap_4d(&p.b, dt, base, 64, M, 2, k / 64, row, step, 128, 64, rows, 2, p.kc, sw)
-                      : make_tmap_3d(&p.b, dt, base, 64, M, k / 64, row, 128, 64, rows, p.kc, sw);
+    const bool b = p.apart ? true
+                   : w1    ? make_tmap_4d(&p.b, dt, base, 64, M, 2, k / 64, row, step, 128, 64, rows, 2, p.kc, sw)
+                           : make_tmap_3d(&p.b, dt, base, 64, M, k / 64, row, 128, 64, rows, p.kc, sw);
     return b && make_tmap_3d(&p.a, dt, a, 64, T, k / 64, 2 * lda, 128, 64, p.tb, p.kc, sw);
   }
   const bool b = p.apart ? true
                  : w1    ? make_tmap_3d(&p.b, dt, base, k, M, 2, row, step, 64, rows, 2, sw)
-                    : make_tmap_2d(&p.b, dt, base, k, M, row, 64, rows, sw);
+                         : make_tmap_2d(&p.b, dt, base, k, M, row, 64, rows, sw);
   return b && make_tmap_2d(&p.a, dt, a, k, T, 2 * lda, 64, p.tb, sw);
 }
 

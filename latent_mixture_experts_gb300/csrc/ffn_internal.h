@@ -25,8 +25,8 @@ enum FfnMode {
   kFfnGateUp = 0,   // A = x, B = gate | up rows of half a tile's features; out0 = act(g, u), out1/out2 = g, u when set
   kFfnPlain = 1,    // A, B stored K contiguous; out0
   kFfnDHid = 2,     // B stored N contiguous; out0 = dg, out1 = du, out2 = hid from in_g, in_u
-  kFfnGrads = 3     // up to four products, all with B stored N contiguous: with `cat` first dx, A stored K contiguous and
-                    // K concatenated over (a[0], b[0]) and (a_cat, b_cat); then out[i] = A[i]^T B[i], A stored M contiguous
+  kFfnGrads = 3     // up to four products, B stored N contiguous: with `cat` first dx, A stored K contiguous, K
+                    // concatenated over (a[0], b[0]) and (a_cat, b_cat); then A[i]^T B[i], A stored M contiguous
 };
 constexpr int kPairProducts = 4;
 struct FfnPairParams {
@@ -46,8 +46,8 @@ struct FfnPairParams {
   int* err;
 };
 // Chooses the tile width (128 or 256) for M, N, nprod and out and fills
-// tiles_n, tile_end, full, n1, delta and wide; K-contiguous b maps have boxes of half of
-// it, b_half (width 256) of a quarter.
+// tiles_n, tile_end, full, n1, delta and wide; K-contiguous b maps have boxes
+// of half of it, b_half (width 256) of a quarter.
 int ffn_pair_tiles(FfnPairParams& p, FfnMode mode, int ctas);
 cudaError_t launch_ffn_pair(FfnMode mode, const FfnPairParams& p, int tn, int ctas, cudaStream_t s);
 // Largest number of CTAs (an even number) of the pair kernels that run at once.
@@ -58,7 +58,8 @@ cudaError_t ffn_pair_ctas(int* ctas);
 constexpr int kSkinnyMaxTokens = 96;
 constexpr int kSkinnyMaxStages = 16;
 constexpr int kSkinnyMaxSplits = 8;    // K splits: the portable cluster size
-constexpr int kSkinnySmem = 110 * 1024;   // two CTAs on an SM; with 74 KB and three, one token at 7168 x 6144 48.6 us against 46.5 us
+// Two CTAs on an SM (one token at 7168 x 6144: 46.5 us; with 74 KB and three CTAs 48.6 us).
+constexpr int kSkinnySmem = 110 * 1024;
 struct FfnSkinnyParams {
   // whole (K a multiple of 64): a (64, T, K/64), b (64, features, K/64) or, gate/up, (64, features, 2, K/64),
   // boxes of tb / rows and kc chunks; else a (K, T), b (K, features[, 2]), one box per 64-wide chunk
@@ -87,7 +88,7 @@ cudaError_t launch_ffn_skinny(const FfnSkinnyParams& p, bool gate_up, int act, c
 constexpr int kMxTileN[2] = {192, 128};
 struct FfnMxParams {
   CUtensorMap a, b[2];          // codes, boxes of 128 K values x 128 rows (a) or half a tile's (b)
-  CUtensorMap sfa, sfb;         // scale atoms [row / 128][nkb], [tile][nkb][2 or 1] of 128 32-bit words, boxes of 1 and 2 or 1
+  CUtensorMap sfa, sfb;         // scale atoms [row / 128][nkb], [tile][nkb][2 or 1] of 128 words; boxes of 1, 2 or 1
   void* out;                    // gate/up: hidden codes [M][N]; else bf16 [M][N]
   uint8_t* out_sf;              // gate/up: the hidden activation's atoms
   int out_nkb;

@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
       if (!(ok = warp_wait(&full[s], phase, p.err))) break;
       tc_fence_after();
       // descriptors count 16-byte units
-      uint64_t ad = a_desc + static_cast<uint32_t>(s * a_slot >> 4), bd = b_desc + static_cast<uint32_t>(s * b_slot >> 4);
+      uint64_t ad = a_desc + static_cast<uint32_t>(s * a_slot >> 4);
+      uint64_t bd = b_desc + static_cast<uint32_t>(s * b_slot >> 4);
       for (int c = 0; c < p.kc; ++c) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -162,7 +163,8 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
   __syncwarp();
   if (p.reuse_ring) cluster_arrive();
   cluster_wait();
-  const int lfs = 31 - __clz(rows / p.splits), fs = 1 << lfs, pitch = N / p.splits + 4;   // 16-byte rows, four banks apart
+  const int lfs = 31 - __clz(rows / p.splits), fs = 1 << lfs;
+  const int pitch = N / p.splits + 4;   // 16-byte rows, four banks apart
   float* recv = reinterpret_cast<float*>(sm + p.recv);
   const int row = 32 * warp;
   if (warp < 4 && row < p.T) {      // warp-uniform
@@ -223,8 +225,8 @@ cudaError_t launch(const FfnSkinnyParams& p, cudaStream_t s) {
   static const cudaError_t attr =
       cudaFuncSetAttribute(ffn_skinny_kernel<GU, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSkinnySmem);
   if (attr != cudaSuccess) return attr;
-  return launch_pdl_cluster(ffn_skinny_kernel<GU, ACT>, dim3((p.M + p.rows - 1) / p.rows * p.splits), dim3(p.T > kManyTokens ? kManyThreads : kThreads),
-                            kSkinnySmem, p.splits, s, p);
+  return launch_pdl_cluster(ffn_skinny_kernel<GU, ACT>, dim3((p.M + p.rows - 1) / p.rows * p.splits),
+                            dim3(p.T > kManyTokens ? kManyThreads : kThreads), kSkinnySmem, p.splits, s, p);
 }
 
 }  // namespace

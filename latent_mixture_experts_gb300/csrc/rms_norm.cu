@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const __grid_constan
 // of its own fills by bulk copies, several rows ahead; a slot is free again as
 // soon as its row is in registers.
 template <class R, bool HAS_R, bool MX, int VPT>
-__global__ void __launch_bounds__(32 * kRingMaxWarps + 32) add_rms_norm_ring_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(32 * kRingMaxWarps + 32)
+    add_rms_norm_ring_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kRingMaxWarps * kRingMaxStages], empty[kRingMaxWarps * kRingMaxStages];
   __shared__ float slots[2][kRingMaxWarps];
@@ -300,7 +301,8 @@ constexpr int bwd_max_warps(int vpt) { return vpt == 2 ? 28 : 16; }
 // several rows ahead, so that HBM streams while a row is reduced, and
 // registers hold only the sums: the row is read from shared memory twice.
 template <class R, bool HAS_DH, int VPT>
-__global__ void __launch_bounds__(32 * bwd_max_warps(VPT) + 32) rms_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+__global__ void __launch_bounds__(32 * bwd_max_warps(VPT) + 32)
+    rms_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kRingMaxWarps * kRingMaxStages], empty[kRingMaxWarps * kRingMaxStages];
   __shared__ float slots[2][2][kRingMaxWarps];

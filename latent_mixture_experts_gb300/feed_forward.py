@@ -167,8 +167,9 @@ class GatedFFN:
     weights: dict of contiguous CUDA tensors gate, up [d_ff][d_model] and down
     [d_model][d_ff]: bf16, or uint8 E4M3 codes with gate_s, up_s, down_s
     uint8 E8M0 scales (one per 32 input values).  Borrowed: in-place updates
-    of bf16 weights between calls are seen; MXFP8 weights must not change.  training=True allocates what the backward pass
-    needs (bf16 weights).  One stream at a time."""
+    of bf16 weights between calls are seen; MXFP8 weights must not change.
+    training=True allocates what the backward pass needs (bf16 weights).  One
+    stream at a time."""
 
     def __init__(self, weights: dict, max_tokens: int, act: str = "situ", situ_beta: float = 4.0,
                  situ_linear_beta: float = 25.0, training: bool = False, stream=None):

@@ -214,6 +214,17 @@ def test_streams_and_graph(ops, T):
     layer.lmoe_ffn_sync_status()
 
 
+def test_workspace_that_does_not_fit(ops):
+    """An allocation that fails is refused, and leaves no error behind for the caller's next launch."""
+    x, W, _ = _make(8, 64, 512, 90)
+    with pytest.raises(ops.LmoeError) as e:
+        ops.GatedFFN(W, max_tokens=2 ** 31 - 1, training=True)      # 6.6 TB
+    assert e.value.status == ops.LMOE_ERR_OOM
+    assert bool((x + 0 == x).all())
+    layer = ops.GatedFFN(W, max_tokens=8)
+    _check_forward(layer.lmoe_ffn_forward(x), x, W, "situ")
+
+
 def test_binding_refusals(ops):
     x, W, dy = _make(8, 64, 64, 91)
     with pytest.raises(ValueError):

@@ -47,7 +47,7 @@ def _check(y, q, s, W, act, b1=4.0, b2=25.0):
     dg, du = R.ACC * (x.abs() @ wg.abs().T), R.ACC * (x.abs() @ wu.abs().T)
     eh = v.abs() * (da.abs() * dg + dg * dg) + a.abs() * (dv.abs() * du + du * du) + 2 * dg * du + R.FAST * h.abs()
     f = torch.exp2(hs.to(R.D) - 127).repeat_interleave(32, -1)
-    # from the exact h to the stored one: half a step of the GPU's own encoding (a scale one up doubles the subnormal one)
+    # from the exact h to the stored one: half a step of the GPU's own encoding (a scale one up doubles the least)
     eq = eh + torch.maximum(2.0 ** -4 * (h.abs() + eh), 2.0 ** -9 * f)
     bound = eq @ wd.abs().T + R.ACC * ((h.abs() + eq) @ wd.abs().T)
     exact = h @ wd.T

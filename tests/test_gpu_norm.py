@@ -193,7 +193,8 @@ def test_binding_refusals(ops):
     bad = [lambda: ops.lmoe_add_rms_norm(x.float(), w, EPS), lambda: ops.lmoe_add_rms_norm(x, w.float(), EPS),
            lambda: ops.lmoe_add_rms_norm(x, w[:32], EPS), lambda: ops.lmoe_add_rms_norm(x, w, EPS, residual=r[:3]),
            lambda: ops.lmoe_add_rms_norm(x.t().contiguous().t(), w, EPS),
-           lambda: ops.lmoe_add_rms_norm(x, w, EPS, h_out=r), lambda: ops.lmoe_add_rms_norm(x, w, EPS, residual=r.half()),
+           lambda: ops.lmoe_add_rms_norm(x, w, EPS, h_out=r),
+           lambda: ops.lmoe_add_rms_norm(x, w, EPS, residual=r.half()),
            lambda: ops.lmoe_add_rms_norm_backward(x, r, w, EPS, dh=r.float()),
            lambda: ops.lmoe_add_rms_norm_backward(x[:2], r, w, EPS)]
     for f in bad:
