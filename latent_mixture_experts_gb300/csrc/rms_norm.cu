@@ -289,17 +289,11 @@ struct NormBwdParams {
   int T, d, warps, groups, stages;   // warps per row, rows at a time, rows in flight for each
   float eps;
 };
-// Compute warps of a CTA: two rows of up to 8192 values at once (4096 rows of
-// 7168: 38 us against 45 us with one), while the wider rows' registers allow
-// 16 warps and narrower rows gain nothing from more (4096 rows of 256: 10 us
-// with 16 rows at once, 15 us with 28).
-constexpr int bwd_max_warps(int vpt) { return vpt == 2 ? 28 : 16; }
+// Compute warps of a CTA: with 28 it works two rows of 7168 or 3584 values at
+// once (4096 rows: 42.6 us and 23.7 us, with 16 warps and one row 48 us and 28.1
+// us); wider rows take more registers than that leaves a thread.
+constexpr int bwd_max_warps(int vpt) { return vpt <= 2 ? kRingMaxWarps : 16; }
 
-// One CTA per SM.  Each group of warps takes every (gridDim.x * groups)-th row
-// and keeps its column sums of dw in registers until the last one.  Rows come
-// by bulk copies into a ring of shared memory, issued by a warp of their own
-// several rows ahead, so that HBM streams while a row is reduced, and
-// registers hold only the sums: the row is read from shared memory twice.
 template <class R, bool HAS_DH, int VPT>
 __global__ void __launch_bounds__(32 * bwd_max_warps(VPT) + 32)
     rms_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
