@@ -290,8 +290,9 @@ struct NormBwdParams {
   float eps;
 };
 // Compute warps of a CTA: with 28 it works two rows of 7168 or 3584 values at
-// once (4096 rows: 42.6 us and 23.7 us, with 16 warps and one row 48 us and 28.1
-// us); wider rows take more registers than that leaves a thread.
+// once (4096 rows of 7168: 38 us against 45 us with 16 warps and one row; of
+// 3584: 23.7 us against 28.1 us); wider rows take more registers than that
+// leaves a thread.
 constexpr int bwd_max_warps(int vpt) { return vpt <= 2 ? kRingMaxWarps : 16; }
 
 template <class R, bool HAS_DH, int VPT>
