@@ -134,3 +134,51 @@ def test_training_a_stack(ops):
                 w[n].sub_((20.0 * getattr(grad, n).float()).bfloat16())
             sub.norm_w.sub_((20.0 * grad.norm_w).bfloat16())
     assert losses[-1] < 0.95 * losses[0], losses
+
+
+def test_blocks_on_streams_of_their_own(ops):
+    """Dense, MXFP8 and MoE blocks and the norms, each on a stream of its own at the same time: the bits of the calls
+    one after the other."""
+    wl = C.workload("k3_tiny_t16")
+    d, F = wl.cfg.d_model, 512
+    g = torch.Generator(device="cuda").manual_seed(2)
+    W = _dense(d, F, g)
+    M = {}
+    for n, o, i in (("gate", F, d), ("up", F, d), ("down", d, F)):
+        M[n], M[n + "_s"] = R.mx_random((o, i), i ** -0.5, g, "cuda")
+    E, _ = gpu_inputs(wl, T=1)
+    w = (1 + 0.1 * torch.randn(d, device="cuda", generator=g)).bfloat16()
+    xs = {T: torch.randn(T, d, device="cuda", generator=g).bfloat16() for T in (1, 16, 40, 300, 1100)}
+    rs = {T: torch.randn(T, d, device="cuda", generator=g).bfloat16() for T in xs}
+
+    def dense(T):
+        block = ops.GatedFFN(W, max_tokens=T, training=True)
+
+        def call():
+            y, gg, u = block.lmoe_ffn_forward(xs[T], save=True)
+            return (y, *block.lmoe_ffn_backward(xs[T], gg, u, y))
+        return call
+
+    def mx(T):
+        block = ops.GatedFFN(M, max_tokens=T)
+        q, s, _ = ops.lmoe_add_rms_norm(xs[T], w, EPS, out_format="mxfp8")
+        return lambda: (block.lmoe_ffn_forward_mx(q, s),)
+
+    def moe(T):
+        layer = make_layer(wl, E, max_tokens=T, keep_f32=False)
+        return lambda: (layer.lmoe_forward(xs[T]),)
+
+    def norm(T):
+        return lambda: ops.lmoe_add_rms_norm_backward(xs[T], rs[T], w, EPS, dh=xs[T])
+    calls = [dense(300), dense(16), mx(16), mx(1100), moe(40), norm(1100), dense(1100), mx(1)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(20):
+        got = []
+        for c, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                got.append(c())
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
