@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(32 * kRingMaxWarps + 32)
       for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[b]);
+    if (lane == 0 && ok) mbar_arrive(&empty[b]);
     if (++s == p.stages) s = 0, phase ^= 1;
     ss = warp_sum(ss);
     if (p.warps > 1) {       // the slots alternate between rows
@@ -271,7 +271,8 @@ __global__ void __launch_bounds__(32 * kRingMaxWarps + 32)
       asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(32 * p.warps) : "memory");
       ss = warp_sum(lane < p.warps ? at[lane] : 0.0f);
     }
-    // a bounded wait that ran out (no handle carries an error flag) makes this row and the group's next ones NaN
+    // a bounded wait that ran out (no handle carries an error flag) makes this row and the group's next ones NaN;
+    // their slots are not given back, so no copy is issued any more that the CTA could leave in flight
     const float rho = ok ? rsqrtf(ss * inv_d + p.eps) : __int_as_float(0x7FC00000);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) write_vec<MX>(p, row, (t + i * stride) * 8, true, v[i], wv[i], rho);
@@ -289,11 +290,9 @@ struct NormBwdParams {
   int T, d, warps, groups, stages;   // warps per row, rows at a time, rows in flight for each
   float eps;
 };
-// Compute warps of a CTA: with 28 it works two rows of 7168 or 3584 values at
-// once (4096 rows of 7168: 38 us against 45 us with 16 warps and one row; of
-// 3584: 23.7 us against 28.1 us); wider rows take more registers than that
-// leaves a thread.
-constexpr int bwd_max_warps(int vpt) { return vpt <= 2 ? kRingMaxWarps : 16; }
+// Compute warps of a CTA: what leaves a thread the registers of its vectors
+// (64 of them with 28 warps and the copying one, 128 with 15).
+constexpr int bwd_max_warps(int vpt) { return vpt == 1 ? kRingMaxWarps : 15; }
 
 template <class R, bool HAS_DH, int VPT>
 __global__ void __launch_bounds__(32 * bwd_max_warps(VPT) + 32)
@@ -351,13 +350,17 @@ __global__ void __launch_bounds__(32 * bwd_max_warps(VPT) + 32)
     const int b = group * p.stages + s;
     if (!mbar_wait(&full[b], phase)) {
       // A bounded wait ran out, and no handle carries an error flag: dw becomes
-      // NaN.  Copies in flight get a millisecond to land.
+      // NaN.  This warp still meets the group's others, which may not have given
+      // up, at each row's barrier; no slot is given back, so the copies end.
+      const float k = __int_as_float(0x7FC00000);
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = __int_as_float(0x7FC00000);
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+        for (int j = 0; j < 8; ++j) acc[i][j] = k;
+      if (lane < 4) slots[lane & 1][lane >> 1][warp] = k;
+      __syncwarp();
+      if (p.warps > 1)
+        for (; row < p.T; row += step) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(32 * p.warps) : "memory");
       break;
     }
     const uint8_t* src = ring + static_cast<size_t>(b) * row_bytes;
@@ -538,16 +541,25 @@ cudaError_t launch_fwd(NormParams& p, cudaStream_t s) {
                     : launch_pdl(add_rms_norm_kernel<R, HAS_R, MX, 4>, grid, block, 0, s, p);
 }
 
-// Backward: rows at a time, and how many CTAs.
+// Backward: warps of a row, rows at a time and in flight, and how many CTAs.
 struct BwdPlan {
-  int vpt, warps, groups, grid;
+  int vpt, warps, groups, stages, grid;
 };
-BwdPlan bwd_plan(int T, int d) {
-  const RowPlan r = row_plan(d, 512);
-  BwdPlan b = {r.vpt, r.warps, bwd_max_warps(r.vpt) / r.warps, 1};
-  // one row of the widest types (bf16 and two fp32 values) fits the ring for each group
-  const int fit = kRingSmem / (10 * d);
-  if (b.groups > fit) b.groups = fit;
+BwdPlan bwd_plan(int T, int d, int row) {
+  // One vector per thread for narrow rows, four or five for wide ones: fewer
+  // warps meet at a row's barrier, and more rows are worked on at once.  4096
+  // rows of a bf16 stream with dh, 1 / 4 vectors: 11.3 / 11.6 us at 1152 values,
+  // 18.6 / 18.3 us at 2560, 23.6 / 24.4 us at 3584, 28.3 / 26.5 us at 4096 (without
+  // dh 10.6 / 10.7, 17.5 / 17.8, 22.8 / 20.3 and 25.9 / 22.5 us); at 7168, 2 / 4:
+  // 42.6 / 42.3 us (36.7 / 33.4 us).  2048 rows of 16384, 4 / 5: 58.9 / 51.2 us.
+  const int vpt = d <= 2560 ? 1 : d <= 8192 ? 4 : 5;
+  const int warps = (d / 8 + 32 * vpt - 1) / (32 * vpt);
+  BwdPlan b = {vpt, warps, bwd_max_warps(vpt) / warps, 0, 1};
+  // Each group has two rows in flight at least, where they fit: fp32 stream with
+  // dh, 4096 rows of 7168, one group of two 66.6 us against two of one 83.9 us.
+  const int fit = kRingSmem / row;
+  if (b.groups > fit / 2) b.groups = fit > 1 ? fit / 2 : 1;
+  b.stages = fit / b.groups < kRingMaxStages ? fit / b.groups : kRingMaxStages;
   const int need = (T + b.groups - 1) / b.groups;
   b.grid = need < kRingCtas ? need : kRingCtas;
   return b;
@@ -563,22 +575,17 @@ cudaError_t launch_bwd_vpt(const NormBwdParams& p, int grid, cudaStream_t s) {
 }
 template <class R, bool HAS_DH>
 cudaError_t launch_bwd(NormBwdParams& p, const BwdPlan& b, cudaStream_t s) {
-  const int row = p.d * (2 + static_cast<int>(sizeof(R)) * (HAS_DH ? 2 : 1));
-  const int fit = kRingSmem / (b.groups * row);
-  if (fit < 1) return cudaErrorInvalidValue;        // not for d <= kNormMaxWidth
-  p.stages = fit < kRingMaxStages ? fit : kRingMaxStages;
   switch (b.vpt) {
     case 1: return launch_bwd_vpt<R, HAS_DH, 1>(p, b.grid, s);
-    case 2: return launch_bwd_vpt<R, HAS_DH, 2>(p, b.grid, s);
-    default: return launch_bwd_vpt<R, HAS_DH, 4>(p, b.grid, s);
+    case 4: return launch_bwd_vpt<R, HAS_DH, 4>(p, b.grid, s);
+    default: return launch_bwd_vpt<R, HAS_DH, 5>(p, b.grid, s);
   }
 }
 
 }  // namespace
 
 size_t rms_norm_bwd_partials(int T, int d) {
-  const BwdPlan b = bwd_plan(T, d);
-  return static_cast<size_t>(b.grid) * d;
+  return static_cast<size_t>(T < kRingCtas ? T : kRingCtas) * d;
 }
 
 cudaError_t launch_add_rms_norm(const void* x, long long ldx, const void* r, long long ldr, bool r_fp32, int T, int d,
@@ -616,9 +623,11 @@ cudaError_t launch_rms_norm_bwd(const void* dy, long long lddy, const void* h, l
   p.T = T;
   p.d = d;
   p.eps = eps;
-  const BwdPlan b = bwd_plan(T, d);
+  const BwdPlan b = bwd_plan(T, d, d * (2 + (h_fp32 ? 4 : 2) * (dh ? 2 : 1)));
+  if (b.stages < 1) return cudaErrorInvalidValue;      // not for d <= kNormMaxWidth
   p.warps = b.warps;
   p.groups = b.groups;
+  p.stages = b.stages;
   cudaError_t e;
   if (h_fp32)
     e = dh ? launch_bwd<float, true>(p, b, s) : launch_bwd<float, false>(p, b, s);
