@@ -90,8 +90,11 @@ struct NormParams {
   int groups, stages;   // ring form: rows at a time, rows in flight for each
   float eps;
 };
-// Ring forms: compute warps of a CTA, rows in flight of a group, shared memory.
+// Ring forms: compute warps of a CTA at most, rows in flight of a group, shared
+// memory.  Many vectors per thread leave fewer warps their registers: a thread
+// has 64 with 28 warps and the copying one, 128 with 15.
 constexpr int kRingMaxWarps = 28, kRingMaxStages = 8;
+constexpr int ring_warps(int vpt) { return vpt <= 2 ? kRingMaxWarps : 15; }
 constexpr int kRingSmem = 208 * 1024;
 static_assert(10 * kNormMaxWidth <= kRingSmem, "a row of the widest types fits");
 
@@ -187,7 +190,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const __grid_constan
 // of its own fills by bulk copies, several rows ahead; a slot is free again as
 // soon as its row is in registers.
 template <class R, bool HAS_R, bool MX, int VPT>
-__global__ void __launch_bounds__(32 * kRingMaxWarps + 32)
+__global__ void __launch_bounds__(32 * ring_warps(VPT) + 32)
     add_rms_norm_ring_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kRingMaxWarps * kRingMaxStages], empty[kRingMaxWarps * kRingMaxStages];
@@ -290,12 +293,8 @@ struct NormBwdParams {
   int T, d, warps, groups, stages;   // warps per row, rows at a time, rows in flight for each
   float eps;
 };
-// Compute warps of a CTA: what leaves a thread the registers of its vectors
-// (64 of them with 28 warps and the copying one, 128 with 15).
-constexpr int bwd_max_warps(int vpt) { return vpt == 1 ? kRingMaxWarps : 15; }
-
 template <class R, bool HAS_DH, int VPT>
-__global__ void __launch_bounds__(32 * bwd_max_warps(VPT) + 32)
+__global__ void __launch_bounds__(32 * ring_warps(VPT) + 32)
     rms_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kRingMaxWarps * kRingMaxStages], empty[kRingMaxWarps * kRingMaxStages];
@@ -512,7 +511,7 @@ cudaError_t launch_ring(NormParams& p, cudaStream_t s) {
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
   if (attr != cudaSuccess) return attr;
   const int row = p.d * (2 + (HAS_R ? static_cast<int>(sizeof(R)) : 0));
-  p.groups = kRingMaxWarps / p.warps;
+  p.groups = ring_warps(VPT) / p.warps;
   const int fit = kRingSmem / row;                 // rows of the ring; d <= kNormMaxWidth: two at least
   if (p.groups > fit) p.groups = fit;
   p.stages = fit / p.groups < kRingMaxStages ? fit / p.groups : kRingMaxStages;
@@ -523,14 +522,24 @@ cudaError_t launch_ring(NormParams& p, cudaStream_t s) {
 
 template <class R, bool HAS_R, bool MX>
 cudaError_t launch_fwd(NormParams& p, cudaStream_t s) {
-  // From about two million values on the ring form: 512 rows of 7168 4.5 us
+  // From about two million values on the ring form: 512 rows of 7168 4.4 us
   // against 5.4 us, 8192 rows 75 us against 79 us (6.2 TB/s; MXFP8 73 us against
-  // 82 us), but 333 rows of 3584 3.0 us against 2.7 us.  It holds rows of up to
-  // 8192 values.
-  if (static_cast<long long>(p.T) * p.d >= 1 << 21 && p.d <= 8192) {
+  // 82 us), but 333 rows of 3584 3.0 us against 2.7 us.
+  const long long n = static_cast<long long>(p.T) * p.d;
+  if (n >= 1 << 21 && p.d <= 8192) {
     const RowPlan r = row_plan(p.d, 512);
     p.warps = r.warps;
     return r.vpt == 1 ? launch_ring<R, HAS_R, MX, 1>(p, s) : launch_ring<R, HAS_R, MX, 2>(p, s);
+  }
+  // Wider rows later (512 rows of 9216 as MXFP8 8.1 us against 7.4 us, 2048 rows
+  // 26.9 us against 31.1 us; 2048 rows of 16384 45 us against 52 us), and not
+  // those of an fp32 stream, of which the ring holds few (2048 rows of 16384 70 us
+  // against 67 us).
+  if constexpr (!(HAS_R && sizeof(R) == 4)) {
+    if (n >= 1 << 23 && p.d > 8192) {
+      p.warps = (p.d / 8 + 32 * 5 - 1) / (32 * 5);
+      return launch_ring<R, HAS_R, MX, 5>(p, s);
+    }
   }
   // One vector per thread up to 8192 values (8192 rows of 7168: 79 us against
   // 90 us with two), four beyond (2048 rows of 16384: 51 us against 57 us).
@@ -554,7 +563,7 @@ BwdPlan bwd_plan(int T, int d, int row) {
   // 42.6 / 42.3 us (36.7 / 33.4 us).  2048 rows of 16384, 4 / 5: 58.9 / 51.2 us.
   const int vpt = d <= 2560 ? 1 : d <= 8192 ? 4 : 5;
   const int warps = (d / 8 + 32 * vpt - 1) / (32 * vpt);
-  BwdPlan b = {vpt, warps, bwd_max_warps(vpt) / warps, 0, 1};
+  BwdPlan b = {vpt, warps, ring_warps(vpt) / warps, 0, 1};
   // Each group has two rows in flight at least, where they fit: fp32 stream with
   // dh, 4096 rows of 7168, one group of two 66.6 us against two of one 83.9 us.
   const int fit = kRingSmem / row;

@@ -88,6 +88,12 @@ def test_forward_many_rows(ops, T, d, rt):
         assert torch.equal(h2, href) and torch.equal(y2, y)
 
 
+@pytest.mark.parametrize("rt", [None, torch.bfloat16, torch.float32], ids=["none", "bf16", "fp32"])
+@pytest.mark.parametrize("T,d", [(1023, 8200), (911, 9216), (601, 16384)])
+def test_forward_many_wide_rows(ops, T, d, rt):
+    test_forward_many_rows(ops, T, d, rt)
+
+
 def test_strided_rows_in_place_and_none(ops):
     T, d = 37, 512
     wide_x, _, w = _make(T, 3 * d, 6)
@@ -150,6 +156,14 @@ def test_backward(ops, T, d, rt, dh):
     _check_bwd(dx, dw, dy, h, w, e)
     again = ops.lmoe_add_rms_norm_backward(dy, h, w, EPS, dh=e)
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+@pytest.mark.parametrize("dh", [False, True], ids=["alone", "with_stream"])
+@pytest.mark.parametrize("rt", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("T,d", [(2000, 2560), (1500, 2568), (1201, 7168), (911, 8192), (903, 8200), (601, 12288),
+                                 (457, 16384)])
+def test_backward_many_wide_rows(ops, T, d, rt, dh):
+    test_backward(ops, T, d, rt, dh)
 
 
 def test_backward_strided_and_empty(ops):
