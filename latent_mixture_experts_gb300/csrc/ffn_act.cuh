@@ -9,46 +9,126 @@
 
 namespace lmoe {
 
-// tanh to ~1e-6 relative: 1 - 2/(e^2x + 1), and the odd Taylor polynomial
-// through x^9 near zero, where that difference cancels (at |x| = 0.25 the
-// next term is 4e-9 of tanh; the quotient form there is off ~2.5e-7).
-__device__ __forceinline__ float tanh_acc(float x) {
-  const float x2 = x * x;
-  const float p =
-      x * (1.0f + x2 * (-1.0f / 3 + x2 * (2.0f / 15 + x2 * (-17.0f / 315 + x2 * (62.0f / 2835)))));
-  const float q = 1.0f - __fdividef(2.0f, __expf(2.0f * x) + 1.0f);
-  return fabsf(x) < 0.25f ? p : q;
+// The arithmetic on one value or, where a thread has two side by side, on both
+// by one instruction (fma.rn.f32x2 and its kin).  With six special-function
+// calls for each SiTU-GLU value one at a time, the epilogue of a short product
+// took longer than the product.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ float vmul(float a, float b) { return a * b; }
+__device__ __forceinline__ float vadd(float a, float b) { return a + b; }
+__device__ __forceinline__ float vfma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ F2 vmul(F2 a, F2 b) {
+  F2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ F2 vadd(F2 a, F2 b) {
+  F2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ F2 vfma(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+template <class V>
+__device__ __forceinline__ V splat(float c);
+template <>
+__device__ __forceinline__ float splat<float>(float c) { return c; }
+template <>
+__device__ __forceinline__ F2 splat<F2>(float c) { return {c, c}; }
+__device__ __forceinline__ float vex2(float a) {       // 2^a
+  float d;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(a));
+  return d;
+}
+__device__ __forceinline__ F2 vex2(F2 a) { return {vex2(a.x), vex2(a.y)}; }
+__device__ __forceinline__ float vrcp(float a) {
+  float d;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(a));
+  return d;
+}
+__device__ __forceinline__ F2 vrcp(F2 a) { return {vrcp(a.x), vrcp(a.y)}; }
+__device__ __forceinline__ float vmin(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ F2 vmin(F2 a, F2 b) { return {fminf(a.x, b.x), fminf(a.y, b.y)}; }
+// far for |x| >= 1/4, else (and for a NaN) near
+__device__ __forceinline__ float by_size(float x, float near, float far) { return fabsf(x) >= 0.25f ? far : near; }
+__device__ __forceinline__ F2 by_size(F2 x, F2 near, F2 far) {
+  return {by_size(x.x, near.x, far.x), by_size(x.y, near.y, far.y)};
+}
+
+constexpr float kLog2E = 1.44269504f;
+template <class V>
+__device__ __forceinline__ V sigmoid(V x) {
+  return vrcp(vadd(vex2(vmul(x, splat<V>(-kLog2E))), splat<V>(1.0f)));
+}
+// tanh of two values to ~1e-6 relative: 1 - 2/(e^2x + 1), both quotients from
+// one reciprocal (e^2x stops at 2^60, where tanh is 1 long since), and the odd
+// Taylor polynomial through x^9 near zero, where that difference cancels (at
+// |x| = 0.25 the next term is 4e-9 of tanh; the quotient form there is off ~5e-7).
+template <class V>
+__device__ __forceinline__ V tanh_near(V x) {
+  const V x2 = vmul(x, x);
+  V p = vfma(x2, splat<V>(62.0f / 2835), splat<V>(-17.0f / 315));
+  p = vfma(x2, p, splat<V>(2.0f / 15));
+  p = vfma(x2, p, splat<V>(-1.0f / 3));
+  return vfma(vmul(x, x2), p, x);
+}
+template <class V>
+__device__ __forceinline__ void tanh_both(V x, V y, V& tx, V& ty) {
+  const V k = splat<V>(2.0f * kLog2E), top = splat<V>(0x1p60f), one = splat<V>(1.0f), m2 = splat<V>(-2.0f);
+  const V a = vadd(vmin(vex2(vmul(x, k)), top), one), b = vadd(vmin(vex2(vmul(y, k)), top), one);
+  const V r = vmul(vrcp(vmul(a, b)), m2);
+  tx = by_size(x, tanh_near(x), vfma(b, r, one));
+  ty = by_size(y, tanh_near(y), vfma(a, r, one));
 }
 
 struct GluCaps {
   float b1, b2, r1, r2;   // caps and their reciprocals
 };
 
-template <int ACT>
-__device__ __forceinline__ float glu_hidden(float g, float u, const GluCaps& c) {
-  const float s = sigmoid_fast(g);
-  if constexpr (ACT == 1) return g * s * u;
-  return c.b1 * tanh_acc(g * c.r1) * s * (c.b2 * tanh_acc(u * c.r2));
+template <int ACT, class V>
+__device__ __forceinline__ V glu_hidden(V g, V u, const GluCaps& c) {
+  const V s = sigmoid(g);
+  if constexpr (ACT == 1) return vmul(vmul(g, s), u);
+  V tg, tu;
+  tanh_both(vmul(g, splat<V>(c.r1)), vmul(u, splat<V>(c.r2)), tg, tu);
+  return vmul(vmul(splat<V>(c.b1), vmul(tg, s)), vmul(splat<V>(c.b2), tu));
 }
 
 struct GluGrad {
-  float hid, dg, du;
+  F2 hid, dg, du;
 };
 template <int ACT>
-__device__ __forceinline__ GluGrad glu_grad(float g, float u, float dhid, const GluCaps& c) {
-  const float s = sigmoid_fast(g);
+__device__ __forceinline__ GluGrad glu_grad(F2 g, F2 u, F2 dhid, const GluCaps& c) {
+  const F2 s = sigmoid(g), one = splat<F2>(1.0f), minus = splat<F2>(-1.0f);
+  const F2 rest = vfma(s, minus, one);               // 1 - s
   GluGrad o;
   if constexpr (ACT == 1) {
-    const float a = g * s;
-    o.hid = a * u;
-    o.dg = dhid * u * (s + a * (1.0f - s));
-    o.du = dhid * a;
+    const F2 a = vmul(g, s);
+    o.hid = vmul(a, u);
+    o.dg = vmul(vmul(dhid, u), vfma(a, rest, s));
+    o.du = vmul(dhid, a);
   } else {
-    const float tg = tanh_acc(g * c.r1), tu = tanh_acc(u * c.r2);
-    const float a = c.b1 * tg * s, v = c.b2 * tu;
-    o.hid = a * v;
-    o.dg = dhid * v * ((1.0f - tg * tg) * s + a * (1.0f - s));
-    o.du = dhid * a * (1.0f - tu * tu);
+    F2 tg, tu;
+    tanh_both(vmul(g, splat<F2>(c.r1)), vmul(u, splat<F2>(c.r2)), tg, tu);
+    const F2 a = vmul(splat<F2>(c.b1), vmul(tg, s)), v = vmul(splat<F2>(c.b2), tu);
+    const F2 dtg = vfma(vmul(tg, minus), tg, one), dtu = vfma(vmul(tu, minus), tu, one);   // 1 - t^2
+    o.hid = vmul(a, v);
+    o.dg = vmul(vmul(dhid, v), vfma(a, rest, vmul(dtg, s)));
+    o.du = vmul(vmul(dhid, a), dtu);
   }
   return o;
 }
@@ -57,8 +137,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
+__device__ __forceinline__ uint32_t pack_bf16(F2 v) { return pack_bf16(v.x, v.y); }
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+__device__ __forceinline__ F2 bf16_both(uint32_t v) { return {bf16_lo(v), bf16_hi(v)}; }
+// Values 2j and 2j + 1 of 32 (as bits).
+__device__ __forceinline__ F2 pair_at(const uint32_t (&v)[32], int j) {
+  return {__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])};
+}
 
 // 32 fp32 values (as bits) -> bf16.
 __device__ __forceinline__ void pack32(const uint32_t (&v)[32], uint32_t (&w)[16]) {

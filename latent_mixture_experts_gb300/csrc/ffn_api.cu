@@ -18,6 +18,7 @@ struct lmoe_ffn_ctx {
   lmoe_ffn_config cfg;
   lmoe_ffn_weights w;
   int ctas = 0;                 // resident CTAs of the pair kernels
+  FfnSplitLimits split = {};
   void* pool = nullptr;
   int* err = nullptr;
   void *hid = nullptr, *dg = nullptr, *du = nullptr;
@@ -212,6 +213,7 @@ lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* 
   }
   const size_t bytes = 256 + act_bytes * (cfg->training ? 3 : 1) + (mx ? x_sf + hid_sf + w_sf : 0);
   cudaError_t e = ffn_pair_ctas(&h->ctas);
+  if (e == cudaSuccess) e = ffn_split_limits(&h->split);
   if (e == cudaSuccess) e = cudaMalloc(&h->pool, bytes);
   // the error flag, and the bytes of the scale atoms that nothing writes
   if (e == cudaSuccess) e = cudaMemsetAsync(h->pool, 0, 256, stream);
@@ -280,10 +282,12 @@ lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int 
   FFN_TRY_STATUS(row_args(x, ldx, d));
   if (!usable(out) || (gate == nullptr) != (up == nullptr) || !aligned16(gate) || !aligned16(up))
     return LMOE_ERR_INVALID_ARG;
-  // Up to 96 tokens stream the weights (ffn_skinny.cu), larger batches run on
-  // pair tiles.  Streaming against pair tiles, widths 7168 and 2048: 64 tokens
-  // 25 us and 33 us, 128 tokens 32 us and 34 us; 7168 and 6144: 64 tokens 56 us
-  // and 61 us, 128 tokens 68 us and 62 us.
+  // Up to 72 tokens stream the weights (ffn_skinny.cu), larger batches run on
+  // pair tiles, K split where they are few.  Streaming against pair tiles, 64
+  // and 80 tokens: widths 7168 and 6144 54.6 and 60.4 us against 60.1 and 60.5 us;
+  // 7168 and 2048 24.1 and 26.3 us against 26.3 and 27.1 us; 2048 and 2048 12.4
+  // and 13.7 us against 12.2 and 13.0 us; 1152 and 864 9.2 and 10.2 us against 8.6
+  // and 9.5 us.
   if (T <= kSkinnyMaxTokens) {
     FfnSkinnyParams g = {}, n = {};
     g.T = n.T = T;
@@ -319,21 +323,36 @@ lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int 
   p.out[0] = h->hid;
   p.out[1] = gate;
   p.out[2] = up;
-  int tn = ffn_pair_tiles(p, kFfnGateUp, h->ctas);
-  p.b[0] = h->gate[tn == 128];
-  p.b[1] = h->up[tn == 128];
-  p.b_half[0] = h->gate[1];
-  p.b_half[1] = h->up[1];
   if (!map_k(&p.a[0], x, d, T, ldx)) return LMOE_ERR_CUDA;
-  FFN_TRY(launch_ffn_pair(kFfnGateUp, p, tn, h->ctas, stream));
+  int splits = ffn_split_plan(p, kFfnGateUp, h->split);
+  if (splits > 1) {
+    p.b[0] = h->gate[1];
+    p.b[1] = h->up[1];
+    FFN_TRY(launch_ffn_split(kFfnGateUp, p, splits, stream));
+    p.early = 1;
+  } else {
+    const int tn = ffn_pair_tiles(p, kFfnGateUp, h->ctas);
+    p.b[0] = h->gate[tn == 128];
+    p.b[1] = h->up[tn == 128];
+    p.b_half[0] = h->gate[1];
+    p.b_half[1] = h->up[1];
+    FFN_TRY(launch_ffn_pair(kFfnGateUp, p, tn, h->ctas, stream));
+  }
   p.N[0] = d;
   p.nkb = ceil_div(F, 64);
   p.out[0] = out;
-  tn = ffn_pair_tiles(p, kFfnPlain, h->ctas);
-  p.b[0] = h->down[tn == 128];
-  p.b_half[0] = h->down[1];
   if (!map_k(&p.a[0], h->hid, F, T, F)) return LMOE_ERR_CUDA;
-  FFN_TRY(launch_ffn_pair(kFfnPlain, p, tn, h->ctas, stream));
+  splits = ffn_split_plan(p, kFfnPlain, h->split);
+  if (splits > 1) {
+    p.b[0] = h->down[1];
+    FFN_TRY(launch_ffn_split(kFfnPlain, p, splits, stream));
+  } else {
+    p.early = 0;
+    const int tn = ffn_pair_tiles(p, kFfnPlain, h->ctas);
+    p.b[0] = h->down[tn == 128];
+    p.b_half[0] = h->down[1];
+    FFN_TRY(launch_ffn_pair(kFfnPlain, p, tn, h->ctas, stream));
+  }
   h->launches = 2;
   return LMOE_OK;
 }
@@ -373,36 +392,61 @@ lmoe_status lmoe_ffn_backward(lmoe_ffn_handle h, const void* x, int64_t ldx, con
   p.N[0] = F;
   p.nkb = ceil_div(d, 64);
   if (!map_k(&p.a[0], dy, d, T, lddy)) return LMOE_ERR_CUDA;
-  FFN_TRY(launch_ffn_pair(kFfnDHid, p, ffn_pair_tiles(p, kFfnDHid, h->ctas), h->ctas, stream));
+  int splits = ffn_split_plan(p, kFfnDHid, h->split);
+  if (splits > 1) {
+    FFN_TRY(launch_ffn_split(kFfnDHid, p, splits, stream));
+  } else {
+    FFN_TRY(launch_ffn_pair(kFfnDHid, p, ffn_pair_tiles(p, kFfnDHid, h->ctas), h->ctas, stream));
+  }
   h->launches = 1;
-  // the gradients, in one launch: dx = [dg | du] [gate ; up], dw = dg^T x, du^T x, dy^T hid
-  p.nprod = 0;
-  const auto add = [&](int M, int N, void* out) {
-    p.M[p.nprod] = M;
-    p.N[p.nprod] = N;
-    p.out[p.nprod] = out;
-    return p.nprod++;
-  };
+  // the gradients: dx = [dg | du] [gate ; up], dw = dg^T x, du^T x, dy^T hid, in one launch unless dx is split
+  FfnPairParams w = p;
+  w.nprod = 0;
   bool ok = true;
   if (dx) {
-    add(T, d, dx);
-    p.cat = 1;
-    p.nkb_cat = ceil_div(F, 64);
-    p.b[0] = h->gate_n;
-    p.b_cat = h->up_n;
-    ok = map_k(&p.a[0], h->dg, F, T, F) && map_k(&p.a_cat, h->du, F, T, F);
+    w.M[0] = T;
+    w.N[0] = d;
+    w.out[0] = dx;
+    w.cat = 1;
+    w.nkb_cat = ceil_div(F, 64);
+    w.b[0] = h->gate_n;
+    w.b_cat = h->up_n;
+    ok = map_k(&w.a[0], h->dg, F, T, F) && map_k(&w.a_cat, h->du, F, T, F);
+    w.nprod = 1;
+    w.early = splits > 1;      // behind a split dhid
+    splits = ffn_split_plan(w, kFfnGrads, h->split);
+    if (splits > 1) {
+      p = w;
+      w.nprod = w.cat = 0;
+    }
   }
+  const bool apart = p.cat;    // p is dx, w the rest
   const auto add_dw = [&](const void* a, long long lda, int M, const void* b, long long ldb, int N, void* out) {
-    const int i = add(M, N, out);
-    return map_n(&p.a[i], a, M, T, lda) && map_n(&p.b[i], b, N, T, ldb);
+    const int i = w.nprod++;
+    w.M[i] = M;
+    w.N[i] = N;
+    w.out[i] = out;
+    return map_n(&w.a[i], a, M, T, lda) && map_n(&w.b[i], b, N, T, ldb);
   };
   if (dwg) ok = ok && add_dw(h->dg, F, F, x, ldx, d, dwg);
   if (dwu) ok = ok && add_dw(h->du, F, F, x, ldx, d, dwu);
   if (dwd) ok = ok && add_dw(dy, lddy, d, h->hid, F, F, dwd);
   if (!ok) return LMOE_ERR_CUDA;
-  p.nkb = ceil_div(T, 64);
-  FFN_TRY(launch_ffn_pair(kFfnGrads, p, ffn_pair_tiles(p, kFfnGrads, h->ctas), h->ctas, stream));
-  h->launches = 2;
+  w.nkb = ceil_div(T, 64);
+  w.early = apart;      // the weight gradients run beside dx
+  const int tn = w.nprod > 0 ? ffn_pair_tiles(w, kFfnGrads, h->ctas) : 0;
+  if (apart) {
+    // Two splits rather than four where dx then leaves the weight gradients the
+    // CTAs that they take: 256 tokens at 768 x 768 14.1 us against 15.8 us.
+    const int tiles = p.tile_end[0], others = w.nprod > 0 ? ffn_pair_grid(w, h->ctas) : 0;
+    if (splits == 4 && 8 * tiles + others > h->ctas && 4 * tiles + others <= h->ctas) splits = 2;
+    FFN_TRY(launch_ffn_split(kFfnGrads, p, splits, stream));
+    ++h->launches;
+  }
+  if (w.nprod > 0) {
+    FFN_TRY(launch_ffn_pair(kFfnGrads, w, tn, h->ctas, stream));
+    ++h->launches;
+  }
   return LMOE_OK;
 }
 

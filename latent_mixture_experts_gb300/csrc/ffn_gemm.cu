@@ -40,6 +40,7 @@ struct PairCfg {
 };
 constexpr int kEpiPairWarps = 8;             // two for each TMEM lane quarter
 constexpr int kPairThreads = 64 + 32 * kEpiPairWarps;
+constexpr int kTmemBarrier = 1;              // tmem_base is there for the epilogue warps
 // Tile rows of one raster group (4096 tokens at 7168 x 6144, backward: 1231 us;
 // with 4 rows 1288 us, with 16 rows 1277 us).
 constexpr int kTileRows = 8;
@@ -127,8 +128,7 @@ __device__ __forceinline__ bool epilogue_row(const FfnPairParams& p, const Tile&
       }
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        w[j] = pack_bf16(glu_hidden<ACT>(__uint_as_float(g[2 * j]), __uint_as_float(u[2 * j]), caps),
-                         glu_hidden<ACT>(__uint_as_float(g[2 * j + 1]), __uint_as_float(u[2 * j + 1]), caps));
+        w[j] = pack_bf16(glu_hidden<ACT>(pair_at(g, j), pair_at(u, j), caps));
       if (row_ok) store32(static_cast<__nv_bfloat16*>(p.out[0]) + at + c, w, left, wide);
     }
   } else {
@@ -154,11 +154,10 @@ __device__ __forceinline__ bool epilogue_row(const FfnPairParams& p, const Tile&
         uint32_t h[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const GluGrad x = glu_grad<ACT>(bf16_lo(g[j]), bf16_lo(u[j]), __uint_as_float(v[2 * j]), caps);
-          const GluGrad y = glu_grad<ACT>(bf16_hi(g[j]), bf16_hi(u[j]), __uint_as_float(v[2 * j + 1]), caps);
-          g[j] = pack_bf16(x.dg, y.dg);
-          u[j] = pack_bf16(x.du, y.du);
-          h[j] = pack_bf16(x.hid, y.hid);
+          const GluGrad x = glu_grad<ACT>(bf16_both(g[j]), bf16_both(u[j]), pair_at(v, j), caps);
+          g[j] = pack_bf16(x.dg);
+          u[j] = pack_bf16(x.du);
+          h[j] = pack_bf16(x.hid);
         }
         if (row_ok) {
           store32(static_cast<__nv_bfloat16*>(p.out[0]) + at + c, g, left, wide);
@@ -212,16 +211,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
     fence_mbar_init();
   }
   cluster_sync();
-  if (warp == 1) {
+  if (warp == 1) {      // under the first loads
     tmem_alloc_pair(&tmem_base, 2 * TN);
     tmem_relinquish_pair();
+    tc_fence_before();
   }
-  tc_fence_before();
-  cluster_sync();
-  tc_fence_after();
-  griddep_launch();
-  griddep_wait();
-  const uint32_t tbase = tmem_base;
+  if (!p.early) {
+    griddep_launch();
+    griddep_wait();
+  }
   const int pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
   const int total = 2 * p.tile_end[p.nprod - 1] - p.full;   // wide tiles, then halves
 
@@ -284,7 +282,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
       while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
     }
   } else if (warp == 1) {
+    named_arrive(kTmemBarrier, kPairThreads - 32);
     if (rank == 0) {
+      const uint32_t tbase = tmem_base;
       const uint32_t base = smem_u32(sm);
       const uint64_t b_desc = kBMn ? sdesc_sw128_mn(base + C::kA, 8192) : sdesc_sw128(base + C::kA);
       uint32_t it = 0, n = 0;
@@ -323,6 +323,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
       }
     }
   } else {
+    named_sync(kTmemBarrier, kPairThreads - 32);
+    tc_fence_after();
+    const uint32_t tbase = tmem_base;
     const int q = warp & 3;
     const uint32_t remote_empty[2] = {map_rank(&acc_empty[0], 0), map_rank(&acc_empty[1], 0)};
     uint32_t n = 0;
@@ -355,10 +358,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
       if (lane == 0) mbar_arrive_cluster(b ? remote_empty[1] : remote_empty[0]);
     }
   }
+  if (p.early) {      // what follows this kernel follows the one in front too
+    griddep_wait();
+    griddep_launch();
+  }
   __syncwarp();
   tc_fence_before();
   cluster_sync();
-  if (warp == 1) tmem_dealloc_pair(tbase, 2 * TN);
+  if (warp == 1) tmem_dealloc_pair(tmem_base, 2 * TN);
   cluster_sync();      // neither CTA leaves while the other still frees the pair's columns
 }
 
@@ -368,9 +375,8 @@ cudaError_t launch_tn(const FfnPairParams& p, int ctas, cudaStream_t s) {
   static const cudaError_t attr = cudaFuncSetAttribute(
       ffn_pair_kernel<MODE, ACT, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (attr != cudaSuccess) return attr;
-  const int tiles = 2 * p.tile_end[p.nprod - 1] - p.full;
-  return launch_pdl_cluster(ffn_pair_kernel<MODE, ACT, TN>, dim3(2 * tiles < ctas ? 2 * tiles : ctas),
-                            dim3(kPairThreads), C::kSmem, 2, s, p);
+  return launch_pdl_cluster(ffn_pair_kernel<MODE, ACT, TN>, dim3(ffn_pair_grid(p, ctas)), dim3(kPairThreads), C::kSmem,
+                            2, s, p);
 }
 template <int MODE, int ACT>
 cudaError_t launch(const FfnPairParams& p, int tn, int ctas, cudaStream_t s) {
@@ -422,6 +428,11 @@ int ffn_pair_tiles(FfnPairParams& p, FfnMode mode, int ctas) {
   }
   p.full = p.tile_end[p.nprod - 1] - (cut ? rest : 0);
   return 256;
+}
+
+int ffn_pair_grid(const FfnPairParams& p, int ctas) {
+  const int tiles = 2 * p.tile_end[p.nprod - 1] - p.full;
+  return 2 * tiles < ctas ? 2 * tiles : ctas;
 }
 
 cudaError_t launch_ffn_pair(FfnMode mode, const FfnPairParams& p, int tn, int ctas, cudaStream_t s) {

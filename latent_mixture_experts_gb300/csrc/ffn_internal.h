@@ -40,6 +40,10 @@ struct FfnPairParams {
   int wide[kPairProducts];    // outputs whose rows start on 32-byte boundaries
   int nkb;                    // 64-wide K blocks
   int cat, nkb_cat;           // kFfnGrads: the first product is dx, of 2 * nkb_cat K blocks
+  // What the kernel in front lets this one, which starts once everything
+  // before that kernel has finished: read b (split form), or do all of its work
+  // (pair form) before that kernel has finished.
+  int early;
   int n1, delta;              // its tiles, and how many of the others one of them counts for
   float b1, b2;
   int act;
@@ -49,13 +53,23 @@ struct FfnPairParams {
 // tiles_n, tile_end, full, n1, delta and wide; K-contiguous b maps have boxes
 // of half of it, b_half (width 256) of a quarter.
 int ffn_pair_tiles(FfnPairParams& p, FfnMode mode, int ctas);
+int ffn_pair_grid(const FfnPairParams& p, int ctas);      // CTAs of its launch
 cudaError_t launch_ffn_pair(FfnMode mode, const FfnPairParams& p, int tn, int ctas, cudaStream_t s);
+// The split form, for one product of few tiles (K split over the pairs of a
+// cluster; kFfnGrads: dx): fills tile_end, returns the splits, 1 where it does
+// not take the shape; K-contiguous b maps have boxes of 64 rows.
+struct FfnSplitLimits {
+  int clusters2, clusters4;   // clusters that run at once, of two and of four pairs
+};
+cudaError_t ffn_split_limits(FfnSplitLimits* l);
+int ffn_split_plan(FfnPairParams& p, FfnMode mode, const FfnSplitLimits& l);
+cudaError_t launch_ffn_split(FfnMode mode, const FfnPairParams& p, int splits, cudaStream_t s);
 // Largest number of CTAs (an even number) of the pair kernels that run at once.
 cudaError_t ffn_pair_ctas(int* ctas);
 
 // ------------------------------------------------------ small-batch passes
 // out[t][f] over all tokens of a batch of at most kSkinnyMaxTokens.
-constexpr int kSkinnyMaxTokens = 96;
+constexpr int kSkinnyMaxTokens = 72;
 constexpr int kSkinnyMaxStages = 16;
 constexpr int kSkinnyMaxSplits = 8;    // K splits: the portable cluster size
 // Two CTAs on an SM (one token at 7168 x 6144: 46.5 us; with 74 KB and three CTAs 48.6 us).
@@ -72,7 +86,7 @@ struct FfnSkinnyParams {
   int chunks, kc;      // 64-wide K chunks; chunks of a stage
   int stages;
   int splits;          // CTAs of a cluster, over K
-  int recv, reuse_ring;   // where in shared memory the partial sums meet: behind the ring, or over it
+  int recv;            // where in shared memory the partial sums meet, behind the ring
   int whole, apart;
   int swapped;         // swapped: the up matrix lies below the gate matrix in memory
   float b1, b2;

@@ -206,7 +206,11 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
             tmem_ld_wait();
             float h[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) h[j] = glu_hidden<ACT>(__uint_as_float(g[j]), __uint_as_float(u[j]), caps);
+            for (int j = 0; j < 16; ++j) {
+              const F2 v = glu_hidden<ACT>(pair_at(g, j), pair_at(u, j), caps);
+              h[2 * j] = v.x;
+              h[2 * j + 1] = v.y;
+            }
             if (row < p.M)
               store_hidden_block(h, static_cast<uint8_t*>(p.out) + static_cast<size_t>(row) * p.N + f,
                                  p.out_sf + atom_byte(row, f >> 5, p.out_nkb));

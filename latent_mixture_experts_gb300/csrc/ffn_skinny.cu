@@ -64,9 +64,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // Every CTA of the cluster runs (and, where the partial sums go into the
-  // ring, has finished with it) before another one writes to it.
-  if (!p.reuse_ring) cluster_arrive();
+  cluster_arrive();      // every CTA of the cluster runs before another one writes to it
   const uint32_t tacc = tmem_base;
   const bool producer = warp == 0;
   // The dependents are let in only after everything before this kernel has
@@ -161,7 +159,6 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
   const bool ok = mbar_wait(&done, 0, p.err, kErrTimeout);
   tc_fence_after();
   __syncwarp();
-  if (p.reuse_ring) cluster_arrive();
   cluster_wait();
   const int lfs = 31 - __clz(rows / p.splits), fs = 1 << lfs;
   const int pitch = N / p.splits + 4;   // 16-byte rows, four banks apart
@@ -209,7 +206,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
     if constexpr (GU) {
       const float2 g = p.swapped ? w : v, u = p.swapped ? v : w;
       *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at) =
-          pack_bf16(glu_hidden<ACT>(g.x, u.x, caps), glu_hidden<ACT>(g.y, u.y, caps));
+          pack_bf16(glu_hidden<ACT>(F2{g.x, g.y}, F2{u.x, u.y}, caps));
       if (p.save_g) {
         *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.save_g) + at) = pack_bf16(g.x, g.y);
         *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.save_u) + at) = pack_bf16(u.x, u.y);
@@ -238,8 +235,7 @@ bool ffn_skinny_plan(FfnSkinnyParams& p, bool gate_up) {
   const int tiles = (p.M + p.rows - 1) / p.rows;
   p.tb = (p.T + 7) / 8 * 8;
   const int chunk = (p.tb + N) * 128;
-  // K chunks per stage: up to about 24 KB a stage
-  p.kc = chunk <= 6 * 1024 ? 4 : chunk <= 12 * 1024 ? 2 : 1;
+  p.kc = chunk <= 12 * 1024 ? 2 : 1;    // K chunks of a stage: up to 24 KB
   const int all = (p.chunks + p.kc - 1) / p.kc;
   // Split K until there is a CTA for most SMs, and on to two for each while
   // that leaves a CTA 12 chunks of K or more (a CTA's fixed costs against what
@@ -253,15 +249,12 @@ bool ffn_skinny_plan(FfnSkinnyParams& p, bool gate_up) {
   }
   const int budget = kSkinnySmem - 1024;
   const int recv = 4 * p.T * (N + 4 * p.splits);
-  // the partial sums meet behind the ring, or over it where room behind would leave fewer than four stages
-  p.reuse_ring = (budget - recv) / (chunk * p.kc) < 4;
-  const int ring = p.reuse_ring ? budget : (budget - recv) / 1024 * 1024;
-  p.recv = p.reuse_ring ? 0 : ring;
-  p.stages = ring / (chunk * p.kc);
+  p.recv = (budget - recv) / 1024 * 1024;
+  p.stages = p.recv / (chunk * p.kc);      // four at least
   if (p.stages > kSkinnyMaxStages) p.stages = kSkinnyMaxStages;
   // the joined sums, and the MMA's reads of up to 128 rows from the last chunk, stay inside
   const int a_end = p.stages * p.kc * p.tb * 128 + (128 - p.tb) * 128;
-  return p.stages >= 2 && recv <= budget && a_end <= budget;
+  return p.stages >= 2 && a_end <= budget;
 }
 
 cudaError_t launch_ffn_skinny(const FfnSkinnyParams& p, bool gate_up, int act, cudaStream_t s) {

@@ -112,18 +112,18 @@ __device__ __forceinline__ void w_copy_atom_pair(uint32_t taddr, uint64_t sdesc)
   asm volatile(LMOE_ELECT "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 // Arrive once the MMAs that the electing lane issued so far are done: on a
-// barrier of this CTA, or on the same barrier of both CTAs of the pair.  The
-// lane that elect.sync names is the same for the same member mask.
+// barrier of this CTA, or on the same barrier of both CTAs of the pair (`even`:
+// the cluster rank of its even CTA).  The lane that elect.sync names is the same for the same member mask.
 __device__ __forceinline__ void w_commit(uint64_t* bar) {
   asm volatile(LMOE_ELECT "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
                    smem_u32(bar))
                : "memory");
 }
-__device__ __forceinline__ void w_commit_pair(uint64_t* bar) {
+__device__ __forceinline__ void w_commit_pair(uint64_t* bar, uint32_t even = 0) {
   asm volatile(LMOE_ELECT
                "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
                "%1;\n\t}" ::"r"(smem_u32(bar)),
-               "h"(static_cast<uint16_t>(3))
+               "h"(static_cast<uint16_t>(3u << even))
                : "memory");
 }
 #undef LMOE_ELECT

@@ -21,6 +21,13 @@ __device__ __forceinline__ void cluster_sync() {
   cluster_arrive();
   cluster_wait();
 }
+// Barrier `id` of the CTA over `threads` threads: arrive and go on, or wait.
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 // Address of CTA `rank`'s copy of a shared variable.
 __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
   uint32_t a;

@@ -92,6 +92,40 @@ def test_model_widths(ops, T, d, F):
     layer.lmoe_ffn_sync_status()
 
 
+# K split over two or four pairs of CTAs: every tail of tokens, K blocks, features and columns, one tile and many
+@pytest.mark.parametrize("act", ["situ", "swiglu"])
+@pytest.mark.parametrize("T,d,F", [(73, 256, 256), (128, 264, 520), (130, 1000, 712), (256, 2048, 2048),
+                                   (257, 512, 1288), (300, 768, 768), (500, 4104, 1032), (513, 520, 8),
+                                   (700, 72, 3080), (1003, 1152, 864), (256, 7168, 512)])
+def test_split_products(ops, T, d, F, act):
+    test_forward_and_backward(ops, T, d, F, act)
+
+
+@pytest.mark.parametrize("T,d,F", [(100, 1024, 512), (200, 768, 768), (300, 2048, 2048), (1003, 1152, 864)])
+def test_split_products_back_to_back(ops, T, d, F):
+    """The workspace and the products that run beside one another: calls that follow at once, each form of the
+    backward pass among them, give the bits of calls alone."""
+    x, W, dy = _make(T, d, F, 31)
+    x2, _, dy2 = _make(T, d, F, 32)
+    layer = ops.GatedFFN(W, max_tokens=T, training=True)
+    calls = []
+    for a, b in ((x, dy), (x2, dy2)):
+        _, g, u = layer.lmoe_ffn_forward(a, save=True)
+        calls += [lambda a=a, g=g, u=u, b=b, kw=kw: layer.lmoe_ffn_backward(a, g, u, b, **kw)
+                  for kw in ({}, {"need_dw": False}, {"need_dx": False})]
+        calls.append(lambda a=a: (layer.lmoe_ffn_forward(a),))
+    alone = []
+    for call in calls:
+        torch.cuda.synchronize()
+        alone.append(call())
+    torch.cuda.synchronize()
+    got = [(call(), want) for _ in range(8) for call, want in zip(calls, alone)]
+    layer.lmoe_ffn_sync_status()
+    for have, want in got:
+        for p, q in zip(have, want):
+            assert (p is None) == (q is None) and (p is None or torch.equal(p, q))
+
+
 def test_large_preactivations(ops):
     """Saturated gates: tanh and sigmoid at their ends, caps other than the default."""
     x, W, dy = _make(40, 256, 192, 21, scale=30.0)
