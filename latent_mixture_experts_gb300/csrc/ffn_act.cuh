@@ -170,4 +170,26 @@ __device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&w)[
     }
   }
 }
+
+// A warp's 32 rows of 64 bf16 columns, lane = row, to the matrix [.][ld] at dst,
+// of which `rows` and `cols` (a multiple of 8) are left, by way of `buf` (4 KB of
+// shared memory), so that eight lanes store a row's 128 bytes side by side.  In
+// `buf` a 16-byte chunk's place depends on its row: no two of eight lanes meet in
+// a bank.  Against store32, 256 tokens at 7168 x 2048, all gradients: 64.1 us, 67.6 us.
+__device__ __forceinline__ void store_rows(uint8_t* buf, const uint32_t (&w)[32], __nv_bfloat16* dst, int ld, int rows,
+                                           int cols) {
+  const int lane = threadIdx.x & 31, ch = lane & 7;
+  const auto at = [&](int row, int c) { return reinterpret_cast<uint4*>(buf + 128 * row + 16 * (c ^ (row & 7))); };
+#pragma unroll
+  for (int j = 0; j < 8; ++j) *at(lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = 4 * i + lane / 8;
+    const uint4 v = *at(row, ch);
+    if (row < rows && 8 * ch < cols) *reinterpret_cast<uint4*>(dst + static_cast<size_t>(row) * ld + 8 * ch) = v;
+  }
+  __syncwarp();
+}
+
 }  // namespace lmoe

@@ -29,6 +29,8 @@
 namespace lmoe {
 namespace {
 
+constexpr int kEpiPairWarps = 8;             // two for each TMEM lane quarter
+constexpr int kRowsBuf = 4096;               // each one's for turning its rows: 32 rows x 64 bf16
 // TN: columns of a tile.
 template <int TN>
 struct PairCfg {
@@ -36,9 +38,8 @@ struct PairCfg {
   static constexpr int kB = TN / 2 * 128;
   static constexpr int kStage = kA + kB;
   static constexpr int kStages = TN == 256 ? 6 : 8;
-  static constexpr int kSmem = kStages * kStage + 1024;
+  static constexpr int kSmem = kStages * kStage + kEpiPairWarps * kRowsBuf + 1024;
 };
-constexpr int kEpiPairWarps = 8;             // two for each TMEM lane quarter
 constexpr int kPairThreads = 64 + 32 * kEpiPairWarps;
 constexpr int kTmemBarrier = 1;              // tmem_base is there for the epilogue warps
 // Tile rows of one raster group (4096 tokens at 7168 x 6144, backward: 1231 us;
@@ -98,19 +99,21 @@ __device__ __forceinline__ void load32(const __nv_bfloat16* src, uint32_t (&w)[1
     w[i] = a.x, w[i + 1] = a.y, w[i + 2] = a.z, w[i + 3] = a.w;
   }
 }
-// One row (this thread's) of half a tile's columns, from the CTA's TN-column
+// The warp's 32 rows of half a tile's columns, from the CTA's TN-column
 // accumulator at `acc`.  N is a multiple of 8, so a row ends on a 16-byte
 // boundary.  `ready`: waits for the accumulator; what the epilogue reads from
 // memory is requested before, and then one step ahead.
 template <int MODE, int ACT, int TN, class Ready>
-__device__ __forceinline__ bool epilogue_row(const FfnPairParams& p, const Tile& t, uint32_t acc, int row,
-                                             bool row_ok, int half, Ready ready) {
+__device__ __forceinline__ bool epilogue_rows(const FfnPairParams& p, const Tile& t, uint32_t acc, int row0, int half,
+                                              uint8_t* buf, Ready ready) {
   const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
-  const bool wide = p.wide[t.prod];
+  const int row = threadIdx.x & 31, rows = p.M[t.prod] - row0;
+  const bool row_ok = row < rows;
+  const auto out = [&](int i, size_t at) { return static_cast<__nv_bfloat16*>(p.out[i]) + at; };
   if constexpr (MODE == kFfnGateUp) {
     constexpr int kF = TN / 2;      // features of a tile
     const int n0 = t.n * kF, N = p.N[0];
-    const size_t at = static_cast<size_t>(row) * N + n0;
+    const size_t at = static_cast<size_t>(row0 + row) * N + n0;
     if (!ready()) return false;
 #pragma unroll 1
     for (int c = kF / 2 * half; c < kF / 2 * (half + 1); c += 32) {
@@ -122,19 +125,18 @@ __device__ __forceinline__ bool epilogue_row(const FfnPairParams& p, const Tile&
       tmem_ld_wait();
       if (p.out[1] && row_ok) {
         pack32(g, w);
-        store32(static_cast<__nv_bfloat16*>(p.out[1]) + at + c, w, left, wide);
+        store32(out(1, at + c), w, left, p.wide);
         pack32(u, w);
-        store32(static_cast<__nv_bfloat16*>(p.out[2]) + at + c, w, left, wide);
+        store32(out(2, at + c), w, left, p.wide);
       }
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        w[j] = pack_bf16(glu_hidden<ACT>(pair_at(g, j), pair_at(u, j), caps));
-      if (row_ok) store32(static_cast<__nv_bfloat16*>(p.out[0]) + at + c, w, left, wide);
+      for (int j = 0; j < 16; ++j) w[j] = pack_bf16(glu_hidden<ACT>(pair_at(g, j), pair_at(u, j), caps));
+      if (row_ok) store32(out(0, at + c), w, left, p.wide);
     }
   } else {
     const int n0 = t.n * TN, N = p.N[t.prod], c0 = TN / 2 * half;
-    const size_t at = static_cast<size_t>(row) * N + n0;
     if constexpr (MODE == kFfnDHid) {
+      const size_t at = static_cast<size_t>(row0 + row) * N + n0;
       const __nv_bfloat16* gp = static_cast<const __nv_bfloat16*>(p.in_g) + at;
       const __nv_bfloat16* up = static_cast<const __nv_bfloat16*>(p.in_u) + at;
       uint32_t g[16], u[16], v[32];
@@ -160,9 +162,9 @@ __device__ __forceinline__ bool epilogue_row(const FfnPairParams& p, const Tile&
           h[j] = pack_bf16(x.hid);
         }
         if (row_ok) {
-          store32(static_cast<__nv_bfloat16*>(p.out[0]) + at + c, g, left, wide);
-          store32(static_cast<__nv_bfloat16*>(p.out[1]) + at + c, u, left, wide);
-          store32(static_cast<__nv_bfloat16*>(p.out[2]) + at + c, h, left, wide);
+          store32(out(0, at + c), g, left, p.wide);
+          store32(out(1, at + c), u, left, p.wide);
+          store32(out(2, at + c), h, left, p.wide);
         }
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -171,16 +173,19 @@ __device__ __forceinline__ bool epilogue_row(const FfnPairParams& p, const Tile&
         }
       }
     } else {
+      const size_t at = static_cast<size_t>(row0) * N + n0;
       if (!ready()) return false;
 #pragma unroll 1
-      for (int c = c0; c < c0 + TN / 2; c += 32) {
+      for (int c = c0; c < c0 + TN / 2; c += 64) {
         const int left = N - n0 - c;
         if (left <= 0) break;
-        uint32_t v[32], w[16];
-        tmem_ld32(acc + c, v);
+        uint32_t v[2][32], w[32];
+        tmem_ld32(acc + c, v[0]);
+        tmem_ld32(acc + c + 32, v[1]);
         tmem_ld_wait();
-        pack32(v, w);
-        if (row_ok) store32(static_cast<__nv_bfloat16*>(p.out[t.prod]) + at + c, w, left, wide);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) w[j] = pack_bf16(pair_at(v[j / 16], j % 16));
+        store_rows(buf, w, out(t.prod, at + c), N, rows, left);
       }
     }
   }
@@ -327,6 +332,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
     tc_fence_after();
     const uint32_t tbase = tmem_base;
     const int q = warp & 3;
+    uint8_t* buf = sm + kStages * C::kStage + (warp - 2) * kRowsBuf;
     const uint32_t remote_empty[2] = {map_rank(&acc_empty[0], 0), map_rank(&acc_empty[1], 0)};
     uint32_t n = 0;
     for (int round = 0;; ++round) {
@@ -343,15 +349,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
       const Tile t = tile_of(p, i);
       const int row0 = t.m * 256 + 128 * static_cast<int>(rank) + 32 * q;
       const uint32_t acc = tbase + b * TN + (static_cast<uint32_t>(32 * q) << 16);
-      const int row = row0 + lane, half = (warp - 2) >> 2;
-      const bool row_ok = row < p.M[t.prod];
+      const int half = (warp - 2) >> 2;
       bool ok;
       if (row0 >= p.M[t.prod])
         ok = ready();
       else if (TN == 256 && t.narrow)
-        ok = epilogue_row<MODE, ACT, 128>(p, t, acc, row, row_ok, half, ready);
+        ok = epilogue_rows<MODE, ACT, 128>(p, t, acc, row0, half, buf, ready);
       else
-        ok = epilogue_row<MODE, ACT, TN>(p, t, acc, row, row_ok, half, ready);
+        ok = epilogue_rows<MODE, ACT, TN>(p, t, acc, row0, half, buf, ready);
       if (!ok) break;
       tc_fence_before();
       __syncwarp();
@@ -396,10 +401,9 @@ int ffn_pair_tiles(FfnPairParams& p, FfnMode mode, int ctas) {
     }
     return n;
   };
-  // 1 where every output row starts on a 32-byte boundary
-  for (int i = 0; i < p.nprod; ++i) p.wide[i] = p.N[i] % 16 == 0 && reinterpret_cast<uintptr_t>(p.out[i]) % 32 == 0;
-  if (mode == kFfnGateUp || mode == kFfnDHid)           // three outputs of one product
-    for (int i = 1; i < 3; ++i) p.wide[0] = p.wide[0] && reinterpret_cast<uintptr_t>(p.out[i]) % 32 == 0;
+  // activations: 1 where every output row starts on a 32-byte boundary
+  p.wide = p.N[0] % 16 == 0;
+  for (int i = 0; i < 3; ++i) p.wide = p.wide && reinterpret_cast<uintptr_t>(p.out[i]) % 32 == 0;
   // With all SMs busy a narrow tile takes 0.55 to 0.58 of a wide one's time
   // (4096 tokens at 7168 x 6144: forward 650 us against 593 us); 1003 tokens at
   // 1152 x 864, which leave half of the wide grid idle: 15.9 us against

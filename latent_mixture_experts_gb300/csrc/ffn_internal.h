@@ -37,7 +37,7 @@ struct FfnPairParams {
   int M[kPairProducts], N[kPairProducts];   // output rows and columns of each product
   int tiles_n[kPairProducts], tile_end[kPairProducts], nprod;
   int full;                   // tiles from here on are worked in halves of their columns
-  int wide[kPairProducts];    // outputs whose rows start on 32-byte boundaries
+  int wide;                   // gate/up, dhid: output rows start on 32-byte boundaries
   int nkb;                    // 64-wide K blocks
   int cat, nkb_cat;           // kFfnGrads: the first product is dx, of 2 * nkb_cat K blocks
   // What the kernel in front lets this one, which starts once everything

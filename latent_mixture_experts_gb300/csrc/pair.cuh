@@ -40,8 +40,12 @@ __device__ __forceinline__ void st_cluster4(uint32_t addr, const uint32_t* v) {
                "r"(v[3])
                : "memory");
 }
+// Without release: for what the arriving thread has waited for itself (loads
+// from tensor memory).  A release at cluster scope waits until the thread's
+// global stores have arrived: 256 tokens' weight gradients at 7168 x 2048 took
+// 50.6 us with it, 42.5 us without.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Waits of the pair acquire at cluster scope: the arrivals may be the other CTA's.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
