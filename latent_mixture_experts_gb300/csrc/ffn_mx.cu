@@ -39,6 +39,7 @@ struct MxCfg {
   static_assert(kStage % 1024 == 0 && kSmem <= 227 * 1024 && kSfBase + kStages * kSfCols <= 512, "budgets");
 };
 constexpr int kThreads = 320;                        // TMA, MMA, 8 epilogue warps: two for each lane quarter
+constexpr int kTmemBarrier = 1;                      // tmem_base is there for the epilogue warps
 constexpr int kTileRows = 16;     // 4096 tokens at 7168 x 6144: 318 us; 8 rows 325 us, 4 rows 333 us
 
 __device__ __forceinline__ void tile_of(const FfnMxParams& p, int i, int& m, int& n) {
@@ -101,16 +102,13 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
     fence_mbar_init();
   }
   cluster_sync();
-  if (warp == 1) {
+  griddep_launch();
+  if (warp == 1) {      // under the first loads
     tmem_alloc_pair(&tmem_base, 512);
     tmem_relinquish_pair();
+    tc_fence_before();
   }
-  tc_fence_before();
-  cluster_sync();
-  tc_fence_after();
-  griddep_launch();
-  griddep_wait();
-  const uint32_t tbase = tmem_base;
+  if (warp != 0) griddep_wait();
   const int pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
 
   if (warp == 0) {
@@ -121,22 +119,32 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
       tile_of(p, i, m, n);
       const int m0 = m * 256 + 128 * rank;
       const int atom_a = (2 * m + rank) * p.nkb, atom_b = C::kAtoms * n * p.nkb;
+      const auto load_b = [&](int kb, uint32_t s) {
+        if (rank == 0) w_arrive_expect_tx(&full[s], 2 * (kStage + kSf));
+        const uint32_t bar = map_rank(&full[s], 0);
+        uint8_t* sb = sm + s * kStage + C::kA;
+        if constexpr (GU)      // gate rows in the even CTA, up rows in the odd one
+          w_load_2d_pair(sb, &p.b[rank], bar, kb * 128, n * kHalfN);
+        else
+          w_load_2d_pair(sb, &p.b[0], bar, kb * 128, n * TN + rank * kHalfN);
+        w_load_2d_pair(sf + s * kSf + 512, &p.sfb, bar, 0, atom_b + C::kAtoms * kb);   // both CTAs need all N scales
+      };
+      // weights do not change: the first stages' are on their way while the kernel before finishes
+      const int pre = i == first ? (p.nkb < kStages ? p.nkb : kStages) : 0;
+      if (i == first) {
+        for (int kb = 0; kb < pre; ++kb) load_b(kb, kb);
+        griddep_wait();
+      }
       for (int kb = 0; kb < p.nkb; ++kb, ++it) {
         const uint32_t s = it % kStages;
         if (it >= kStages && !warp_wait(&empty[s], ((it / kStages) - 1) & 1, p.err)) {
           ok = false;
           break;
         }
-        if (rank == 0) w_arrive_expect_tx(&full[s], 2 * (kStage + kSf));
+        if (kb >= pre) load_b(kb, s);
         const uint32_t bar = map_rank(&full[s], 0);
-        uint8_t* sa = sm + s * kStage;
-        w_load_2d_pair(sa, &p.a, bar, kb * 128, m0);
-        if constexpr (GU)      // gate rows in the even CTA, up rows in the odd one
-          w_load_2d_pair(sa + C::kA, &p.b[rank], bar, kb * 128, n * kHalfN);
-        else
-          w_load_2d_pair(sa + C::kA, &p.b[0], bar, kb * 128, n * TN + rank * kHalfN);
+        w_load_2d_pair(sm + s * kStage, &p.a, bar, kb * 128, m0);
         w_load_2d_pair(sf + s * kSf, &p.sfa, bar, 0, atom_a + kb);
-        w_load_2d_pair(sf + s * kSf + 512, &p.sfb, bar, 0, atom_b + C::kAtoms * kb);   // both CTAs need all N scales
       }
     }
     // every stage has been read before the pair may leave; after a wait that
@@ -148,7 +156,9 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
       while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
     }
   } else if (warp == 1) {
+    named_arrive(kTmemBarrier, kThreads - 32);
     if (rank == 0) {
+      const uint32_t tbase = tmem_base;
       const uint64_t a_desc = sdesc_sw128(smem_u32(sm)), b_desc = sdesc_sw128(smem_u32(sm) + C::kA);
       const uint64_t sf_desc = sdesc_noswz(smem_u32(sf), 16, 128);
       uint32_t it = 0, n = 0;
@@ -180,6 +190,9 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
       }
     }
   } else {
+    named_sync(kTmemBarrier, kThreads - 32);
+    tc_fence_after();
+    const uint32_t tbase = tmem_base;
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t remote_empty[2] = {map_rank(&acc_empty[0], 0), map_rank(&acc_empty[1], 0)};
     const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
@@ -237,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
   __syncwarp();
   tc_fence_before();
   cluster_sync();
-  if (warp == 1) tmem_dealloc_pair(tbase, 512);
+  if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
   cluster_sync();
 }
 
