@@ -42,8 +42,8 @@ struct PairCfg {
 };
 constexpr int kPairThreads = 64 + 32 * kEpiPairWarps;
 constexpr int kTmemBarrier = 1;              // tmem_base is there for the epilogue warps
-// Tile rows of one raster group (4096 tokens at 7168 x 6144, backward: 1231 us;
-// with 4 rows 1288 us, with 16 rows 1277 us).
+// Tile rows of one raster group (4096 tokens at 7168 x 6144, backward: 1155 us;
+// with 4 rows 1175 us, with 16 rows 1176 us).
 constexpr int kTileRows = 8;
 
 // narrow: half a wide tile, at the end of the wide grid; n counts half tiles.
@@ -405,12 +405,14 @@ int ffn_pair_tiles(FfnPairParams& p, FfnMode mode, int ctas) {
   p.wide = p.N[0] % 16 == 0;
   for (int i = 0; i < 3; ++i) p.wide = p.wide && reinterpret_cast<uintptr_t>(p.out[i]) % 32 == 0;
   // With all SMs busy a narrow tile takes 0.55 to 0.58 of a wide one's time
-  // (4096 tokens at 7168 x 6144: forward 650 us against 593 us); 1003 tokens at
-  // 1152 x 864, which leave half of the wide grid idle: 15.9 us against
-  // 22.8 us.  A last round of wide tiles that fills at most half of the pairs
-  // is cut into halves.  Tiles cost their K blocks, the epilogue's time at least.
-  constexpr float kNarrow = 0.57f;
-  const auto cost = [](int nkb) { return static_cast<float>(nkb < 12 ? 14 : nkb + 2); };
+  // (4096 tokens at 7168 x 6144: forward 601 us against 546 us), of the gradients'
+  // 0.67 (backward 1500 us against 1155 us); 1003 tokens at 1152 x 864, which leave
+  // half of the wide grid idle: forward 16.8 us against 22.8 us.  A last round of
+  // wide tiles that fills at most half of the pairs is cut into halves.  Tiles
+  // cost their K blocks, and eight of them at least: 256 tokens at 5120 x 3584,
+  // backward, 64.4 us; with 14 at least 72.0 us.
+  const float ratio = mode == kFfnGrads ? 0.67f : 0.57f;
+  const auto cost = [](int nkb) { return static_cast<float>(nkb < 6 ? 8 : nkb + 2); };
   const int pairs = ctas / 2;
   const float c2 = cost(p.nkb), c1 = p.cat ? cost(2 * p.nkb_cat) : c2;
   p.delta = c1 > c2 ? static_cast<int>(c1 / c2 + 0.5f) : 1;
@@ -421,10 +423,10 @@ int ffn_pair_tiles(FfnPairParams& p, FfnMode mode, int ctas) {
     const int k1 = p.n1 / pairs, r = p.n1 % pairs, slots = all - p.n1 + r * p.delta, n = slots / pairs;
     rest = slots % pairs;
     cut = tn == 256 && rest > 0 && 2 * rest <= pairs && rest <= all - p.n1 && n >= (r > 0 ? p.delta : k1 > 0 ? 0 : 1);
-    const float others = n + (rest == 0 ? 0.0f : cut ? kNarrow : 1.0f), dx = r > 0 ? c1 / c2 : 0.0f;
+    const float others = n + (rest == 0 ? 0.0f : cut ? ratio : 1.0f), dx = r > 0 ? c1 / c2 : 0.0f;
     return k1 * c1 / c2 + (others > dx ? others : dx);
   };
-  const float narrow = kNarrow * rounds(128), wide = rounds(256);   // leaves the wide tiling in p
+  const float narrow = ratio * rounds(128), wide = rounds(256);   // leaves the wide tiling in p
   if (narrow < wide) {
     rounds(128);
     p.full = p.tile_end[p.nprod - 1];

@@ -40,7 +40,7 @@ struct MxCfg {
 };
 constexpr int kThreads = 320;                        // TMA, MMA, 8 epilogue warps: two for each lane quarter
 constexpr int kTmemBarrier = 1;                      // tmem_base is there for the epilogue warps
-constexpr int kTileRows = 16;     // 4096 tokens at 7168 x 6144: 318 us; 8 rows 325 us, 4 rows 333 us
+constexpr int kTileRows = 16;     // 4096 tokens at 7168 x 6144: 307 us; 8 rows 312 us, 4 rows 319 us
 
 __device__ __forceinline__ void tile_of(const FfnMxParams& p, int i, int& m, int& n) {
   const int tm = p.tiles / p.tiles_n;
@@ -341,7 +341,7 @@ int ffn_mx_tiles(FfnMxParams& p, bool gate_up, int ctas) {
     return (p.tiles + ctas / 2 - 1) / (ctas / 2);
   };
   // With all SMs busy a 128-row tile takes 0.76 of a 192-row one's time (4096
-  // tokens at 7168 x 6144: 362 us against 319 us); where both leave pairs idle
+  // tokens at 7168 x 6144: 360 us against 307 us); where both leave pairs idle
   // the narrow ones win (300 tokens at 1152 x 864: 13.4 us against 15.8 us).
   const int narrow = rounds(128), wide = rounds(192);      // leaves the wide tiling in p
   if (wide <= 0.76f * narrow) return 192;
