@@ -55,7 +55,8 @@ LMOE_API lmoe_status lmoe_add_rms_norm(const void* x_bf16, int64_t ldx, const vo
  * dh_opt [T][d] (h's type): the gradient that reaches h along the residual
  * stream, or NULL.  dx may be dh (lddh = d).  workspace: 16-byte aligned,
  * lmoe_add_rms_norm_backward_workspace bytes, contents irrelevant.  The sums
- * over rows are added in an order that depends on T, d and the types only.
+ * over rows are added in an order that depends on T, d, the types and whether
+ * dh is given only.
  * T = 0 writes dw = 0.  A bounded wait of the kernel that runs out (there is
  * no handle to report it by) leaves NaN in dw.  Errors as above. */
 LMOE_API lmoe_status lmoe_add_rms_norm_backward_workspace(int T, int d, size_t* bytes);
@@ -117,7 +118,8 @@ LMOE_API lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x_bf16, int
  * [T][d_model] (stride lddy): dx [T][d_model], dw_gate and dw_up
  * [d_ff][d_model], dw_down [d_model][d_ff], bf16, overwritten; any of the
  * four may be NULL and is then not computed.  dhid, dg, du and hid are
- * rounded to bf16 between the products.  The same inputs give the same bits.
+ * rounded to bf16 between the products.  The same inputs and the same gradients
+ * asked for give the same bits.
  * T = 0 writes zero weight gradients. */
 LMOE_API lmoe_status lmoe_ffn_backward(lmoe_ffn_handle h, const void* x_bf16, int64_t ldx, const void* gate,
                                        const void* up, const void* dy_bf16, int64_t lddy, int T, void* dx_opt,
