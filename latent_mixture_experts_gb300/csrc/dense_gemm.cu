@@ -202,12 +202,10 @@ __global__ void __launch_bounds__(128, 1) dense_gemm_kernel(const __grid_constan
 template <int BN, int MT>
 cudaError_t launch_bn(const DenseParams& p, int mtiles, cudaStream_t s) {
   using C = DenseCfg<BN, MT>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(dense_gemm_kernel<BN, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         C::kSmem);
+  static std::atomic<uint64_t> limit;
+  {
+    const cudaError_t e = allow_smem(limit, dense_gemm_kernel<BN, MT>, C::kSmem);
     if (e != cudaSuccess) return e;
-    attr_set = true;
   }
   // CTA tiles: MT 128-row tiles each, counted per M segment (a gate/up pair
   // CTA covers one 128-row tile of each segment)

@@ -377,9 +377,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
 template <int MODE, int ACT, int TN>
 cudaError_t launch_tn(const FfnPairParams& p, int ctas, cudaStream_t s) {
   using C = PairCfg<TN>;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      ffn_pair_kernel<MODE, ACT, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> limit;
+  const cudaError_t e = allow_smem(limit, ffn_pair_kernel<MODE, ACT, TN>, C::kSmem);
+  if (e != cudaSuccess) return e;
   return launch_pdl_cluster(ffn_pair_kernel<MODE, ACT, TN>, dim3(ffn_pair_grid(p, ctas)), dim3(kPairThreads), C::kSmem,
                             2, s, p);
 }

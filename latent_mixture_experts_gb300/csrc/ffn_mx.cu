@@ -301,9 +301,9 @@ __global__ void mx_weight_atoms_kernel(const uint8_t* __restrict__ a, const uint
 
 template <bool GU, int ACT, int TN>
 cudaError_t launch_tn(const FfnMxParams& p, int ctas, cudaStream_t s) {
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      ffn_mx_pair_kernel<GU, ACT, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, MxCfg<TN>::kSmem);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> limit;
+  const cudaError_t e = allow_smem(limit, ffn_mx_pair_kernel<GU, ACT, TN>, MxCfg<TN>::kSmem);
+  if (e != cudaSuccess) return e;
   return launch_pdl_cluster(ffn_mx_pair_kernel<GU, ACT, TN>, dim3(2 * p.tiles < ctas ? 2 * p.tiles : ctas),
                             dim3(kThreads), MxCfg<TN>::kSmem, 2, s, p);
 }

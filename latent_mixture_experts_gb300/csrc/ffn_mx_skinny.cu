@@ -217,9 +217,9 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
 
 template <bool GU, int ACT>
 cudaError_t launch(const FfnMxSkinnyParams& p, cudaStream_t s) {
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(ffn_mx_skinny_kernel<GU, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSkinnySmem);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> limit;
+  const cudaError_t e = allow_smem(limit, ffn_mx_skinny_kernel<GU, ACT>, kMxSkinnySmem);
+  if (e != cudaSuccess) return e;
   return launch_pdl_cluster(ffn_mx_skinny_kernel<GU, ACT>, dim3(p.tiles * p.splits),
                             dim3(p.T > kManyTokens ? kManyThreads : kThreads), kMxSkinnySmem,
                             p.splits, s, p);

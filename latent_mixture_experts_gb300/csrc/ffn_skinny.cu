@@ -219,9 +219,9 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
 
 template <bool GU, int ACT>
 cudaError_t launch(const FfnSkinnyParams& p, cudaStream_t s) {
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(ffn_skinny_kernel<GU, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSkinnySmem);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> limit;
+  const cudaError_t e = allow_smem(limit, ffn_skinny_kernel<GU, ACT>, kSkinnySmem);
+  if (e != cudaSuccess) return e;
   return launch_pdl_cluster(ffn_skinny_kernel<GU, ACT>, dim3((p.M + p.rows - 1) / p.rows * p.splits),
                             dim3(p.T > kManyTokens ? kManyThreads : kThreads), kSkinnySmem, p.splits, s, p);
 }

@@ -226,9 +226,9 @@ __global__ void __launch_bounds__(kThreads) ffn_split_kernel(const __grid_consta
 
 template <int MODE, int ACT, int S>
 cudaError_t launch(const FfnPairParams& p, cudaStream_t s) {
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(ffn_split_kernel<MODE, ACT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> limit;
+  const cudaError_t e = allow_smem(limit, ffn_split_kernel<MODE, ACT, S>, kSmem);
+  if (e != cudaSuccess) return e;
   return launch_pdl_cluster(ffn_split_kernel<MODE, ACT, S>, dim3(2 * S * p.tile_end[0]), dim3(kThreads), kSmem, 2 * S,
                             s, p);
 }

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <atomic>
 #include <cstdint>
 
 namespace lmoe {
@@ -152,6 +153,21 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// Raises the limit of `kernel`'s dynamic shared memory, which the runtime keeps
+// for each device, to `bytes` on the current device.  `done`: the kernel's own
+// set of devices that have it; a device whose call failed is asked again.
+template <class... KArgs>
+inline cudaError_t allow_smem(std::atomic<uint64_t>& done, void (*kernel)(KArgs...), int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // launch_pdl for a kernel whose CTAs form clusters of cluster_x along x.

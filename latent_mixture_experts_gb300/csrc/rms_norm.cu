@@ -507,9 +507,9 @@ constexpr int kRingCtas = 152;       // one per SM
 
 template <class R, bool HAS_R, bool MX, int VPT>
 cudaError_t launch_ring(NormParams& p, cudaStream_t s) {
-  static const cudaError_t attr = cudaFuncSetAttribute(add_rms_norm_ring_kernel<R, HAS_R, MX, VPT>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> limit;
+  const cudaError_t e = allow_smem(limit, add_rms_norm_ring_kernel<R, HAS_R, MX, VPT>, kRingSmem);
+  if (e != cudaSuccess) return e;
   const int row = p.d * (2 + (HAS_R ? static_cast<int>(sizeof(R)) : 0));
   p.groups = ring_warps(VPT) / p.warps;
   const int fit = kRingSmem / row;                 // rows of the ring; d <= kNormMaxWidth: two at least
@@ -576,9 +576,9 @@ BwdPlan bwd_plan(int T, int d, int row) {
 
 template <class R, bool HAS_DH, int VPT>
 cudaError_t launch_bwd_vpt(const NormBwdParams& p, int grid, cudaStream_t s) {
-  static const cudaError_t attr = cudaFuncSetAttribute(rms_norm_bwd_kernel<R, HAS_DH, VPT>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> limit;
+  const cudaError_t e = allow_smem(limit, rms_norm_bwd_kernel<R, HAS_DH, VPT>, kRingSmem);
+  if (e != cudaSuccess) return e;
   const size_t smem = static_cast<size_t>(p.groups) * p.stages * p.d * (2 + sizeof(R) * (HAS_DH ? 2 : 1));
   return launch_pdl(rms_norm_bwd_kernel<R, HAS_DH, VPT>, dim3(grid), dim3(32 * (p.warps * p.groups + 1)), smem, s, p);
 }

@@ -1,0 +1,85 @@
+"""Calls of include/lmoe_ffn.h with two devices and with a failing runtime
+call, on a stand-in for the CUDA runtime."""
+import ctypes
+
+import pytest
+
+from tests import _fake_cuda
+
+A = 0x10000      # an aligned address that nothing reads
+
+
+@pytest.fixture
+def lib(tmp_path_factory):
+    lib = _fake_cuda.load(tmp_path_factory)
+    yield lib
+    lib.fake_set_device(0)
+
+
+@pytest.fixture(scope="module")
+def b():
+    from latent_mixture_experts_gb300 import binding
+    return binding
+
+
+def _block(lib, b, mx=False, d=512, F=768, max_tokens=4096, training=1):
+    h = ctypes.c_void_p()
+    cfg = b.LmoeFfnConfig(d_model=d, d_ff=F, act=0, situ_beta=4.0, situ_linear_beta=25.0, wfmt=int(mx),
+                          max_tokens=max_tokens, training=0 if mx else training)
+    w = b.LmoeFfnWeights(**{n: A + (i << 20) for i, n in enumerate(b._FFN_WEIGHT_FIELDS)})
+    assert lib.lmoe_ffn_create(ctypes.byref(cfg), ctypes.byref(w), None, ctypes.byref(h)) == b.LMOE_OK
+    return h
+
+
+def _calls(lib, h, mx, T, d=512):
+    if mx:
+        return [lambda: lib.lmoe_ffn_forward_mx(h, A, A, T, A, None)]
+    return [lambda: lib.lmoe_ffn_forward(h, A, d, T, A, None, None, None),
+            lambda: lib.lmoe_ffn_backward(h, A, d, A, A, A, d, T, A, A, A, A, None)]
+
+
+# a token and small, middle and large batches: each form of the products
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp8"])
+def test_block_on_each_of_two_devices(lib, b, mx):
+    """A process may keep blocks on both of its devices: the second one's launches are as good as the first one's."""
+    for dev in (0, 1):
+        lib.fake_set_device(dev)
+        h = _block(lib, b, mx)
+        for T in (1, 40, 100, 300, 4096):
+            for call in _calls(lib, h, mx, T):
+                assert call() == b.LMOE_OK, (dev, T)
+                assert lib.fake_last_device() == dev
+        assert lib.lmoe_ffn_destroy(h) == b.LMOE_OK
+
+
+@pytest.mark.parametrize("T,d", [(1, 256), (4000, 7168), (2000, 1152), (1023, 16384)])
+def test_norm_on_each_of_two_devices(lib, b, T, d):
+    for dev in (0, 1):
+        lib.fake_set_device(dev)
+        for st in (0, 1):
+            for r in (None, A):
+                for fmt in (0, 1):
+                    assert lib.lmoe_add_rms_norm(A, d, r, d, st, T, d, A, 1e-6, A, A, fmt, A, None) == b.LMOE_OK
+            for dh in (None, A):
+                assert lib.lmoe_add_rms_norm_backward(A, d, A, d, dh, d, st, T, d, A, 1e-6, A, A, A, 1 << 30,
+                                                      None) == b.LMOE_OK
+        assert lib.fake_last_device() == dev
+
+
+def test_a_failed_call_is_not_kept(lib, b):
+    """A limit that could not be raised once is asked for again by the next call; then not any more."""
+    def norm():
+        return lib.lmoe_add_rms_norm_backward(A, 1152, A, 1152, None, 1152, 0, 2000, 1152, A, 1e-6, A, A, A, 1 << 30, None)
+    lib.fake_fail_attributes(1)
+    assert norm() == b.LMOE_ERR_OOM
+    assert norm() == b.LMOE_OK
+    n = lib.fake_attribute_calls()
+    assert norm() == b.LMOE_OK and lib.fake_attribute_calls() == n
+    h = _block(lib, b)
+    for T in (1, 100, 4096):
+        for call in _calls(lib, h, False, T):
+            lib.fake_fail_attributes(1)      # of a kernel that no call before has launched, if there is one
+            assert call() in (b.LMOE_ERR_OOM, b.LMOE_OK)
+            lib.fake_fail_attributes(0)
+            assert call() == b.LMOE_OK
+    assert lib.lmoe_ffn_destroy(h) == b.LMOE_OK
