@@ -103,8 +103,10 @@ typedef struct lmoe_ffn_ctx* lmoe_ffn_handle;
 
 /* Errors: INVALID_ARG (NULL, misaligned, sizes < 1, bad enum, caps not
  * positive), UNSUPPORTED (shapes above; training with MXFP8; not an sm_103
- * GPU), OOM, CUDA.  Synchronises `stream`.  *out is NULL on error.  One handle is used by one
- * stream at a time. */
+ * GPU), OOM, CUDA.  Synchronises `stream`.  *out is NULL on error.  One handle
+ * is used by one stream at a time, and belongs to the device that is current
+ * here: the calls below return INVALID_ARG while another one is (destroy
+ * excepted). */
 LMOE_API lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* w, cudaStream_t stream,
                                      lmoe_ffn_handle* out);
 

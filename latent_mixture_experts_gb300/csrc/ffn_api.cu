@@ -17,6 +17,7 @@ using namespace lmoe;
 struct lmoe_ffn_ctx {
   lmoe_ffn_config cfg;
   lmoe_ffn_weights w;
+  int device = 0;               // where the workspace lies
   int ctas = 0;                 // resident CTAs of the pair kernels
   FfnSplitLimits split = {};
   void* pool = nullptr;
@@ -49,6 +50,12 @@ lmoe_status cuda_status(cudaError_t e) {
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 bool usable(const void* p) { return p && aligned16(p); }
+// The stream of a call, which may be NULL, is one of the current device: the
+// handle's memory has to lie there.
+bool on_its_device(lmoe_ffn_handle h) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // K-contiguous bf16 operand [rows][K]: boxes of 64 K values x `box` rows.
@@ -194,6 +201,7 @@ lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* 
   if (!h) return LMOE_ERR_OOM;
   h->cfg = *cfg;
   h->w = *w;
+  h->device = dev;
   const size_t Tm = cfg->max_tokens, T256 = (Tm + 255) / 256 * 256;
   const auto pad = [](size_t v) { return (v + 255) / 256 * 256; };
   const size_t act_bytes = pad(Tm * F * (mx ? 1 : 2));
@@ -274,7 +282,7 @@ lmoe_status lmoe_ffn_destroy(lmoe_ffn_handle h) {
 
 lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int T, void* out, void* gate, void* up,
                              cudaStream_t stream) {
-  if (!h || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
+  if (!h || !on_its_device(h) || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
   if (h->cfg.wfmt != LMOE_FFN_W_BF16) return LMOE_ERR_UNSUPPORTED;
   h->launches = 0;
   if (T == 0) return LMOE_OK;
@@ -360,7 +368,7 @@ lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int 
 lmoe_status lmoe_ffn_backward(lmoe_ffn_handle h, const void* x, int64_t ldx, const void* gate, const void* up,
                               const void* dy, int64_t lddy, int T, void* dx, void* dwg, void* dwu, void* dwd,
                               cudaStream_t stream) {
-  if (!h || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
+  if (!h || !on_its_device(h) || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
   if (h->cfg.wfmt != LMOE_FFN_W_BF16 || !h->cfg.training) return LMOE_ERR_UNSUPPORTED;
   h->launches = 0;
   const int d = h->cfg.d_model, F = h->cfg.d_ff;
@@ -452,7 +460,7 @@ lmoe_status lmoe_ffn_backward(lmoe_ffn_handle h, const void* x, int64_t ldx, con
 
 lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8_t* x_scales, int T, void* out,
                                 cudaStream_t stream) {
-  if (!h || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
+  if (!h || !on_its_device(h) || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
   if (h->cfg.wfmt != LMOE_FFN_W_MXFP8) return LMOE_ERR_UNSUPPORTED;
   h->launches = 0;
   if (T == 0) return LMOE_OK;
@@ -520,7 +528,7 @@ lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8
 }
 
 lmoe_status lmoe_ffn_sync_status(lmoe_ffn_handle h, cudaStream_t stream) {
-  if (!h) return LMOE_ERR_INVALID_ARG;
+  if (!h || !on_its_device(h)) return LMOE_ERR_INVALID_ARG;
   FFN_TRY(cudaStreamSynchronize(stream));
   int flag = 0;
   FFN_TRY(cudaMemcpy(&flag, h->err, sizeof(flag), cudaMemcpyDeviceToHost));

@@ -206,6 +206,10 @@ class GatedFFN:
                                                         ctypes.byref(h)))
         self._h, self._lib = h, lib
 
+    def _current(self):
+        if _raw_device() != self._dev:
+            raise ValueError(f"the block is on {self._device}, which is not the current CUDA device")
+
     def _tokens(self, t: torch.Tensor, name: str, T: int) -> int:
         ld = _rows(name, t, (_BF16,), (T, self.d_model))
         if t.get_device() != self._dev:
@@ -225,6 +229,7 @@ class GatedFFN:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.lmoe_ffn_forward(x, save, out)
+        self._current()
         T = x.shape[0]
         ldx = self._tokens(x, "x", T)
         y = torch.empty_like(x, memory_format=_PACKED) if out is None else self._out(T, out)
@@ -248,6 +253,7 @@ class GatedFFN:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.lmoe_ffn_backward(x, g, u, dy, need_dx, need_dw)
+        self._current()
         T, shape = x.shape[0], (x.shape[0], self.d_ff)
         ldx = self._tokens(x, "x", T)
         lddy = self._tokens(dy, "dy", T)
@@ -275,6 +281,7 @@ class GatedFFN:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.lmoe_ffn_forward_mx(x_codes, x_scales, out)
+        self._current()
         T = x_codes.shape[0]
         _packed("x_codes", x_codes, _U8, (T, self.d_model))
         _packed("x_scales", x_scales, _U8, (T, self.d_model // 32))
@@ -287,6 +294,7 @@ class GatedFFN:
         return y
 
     def lmoe_ffn_sync_status(self, stream=None):
+        self._current()
         B._check("lmoe_ffn_sync_status", self._lib.lmoe_ffn_sync_status(self._h, B._stream(stream)))
 
     def lmoe_ffn_last_launch_count(self) -> int:

@@ -3,8 +3,11 @@ call, on a stand-in for the CUDA runtime."""
 import ctypes
 
 import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
 
 from tests import _fake_cuda
+from tests._harness import built_library
 
 A = 0x10000      # an aligned address that nothing reads
 
@@ -83,3 +86,40 @@ def test_a_failed_call_is_not_kept(lib, b):
             lib.fake_fail_attributes(0)
             assert call() == b.LMOE_OK
     assert lib.lmoe_ffn_destroy(h) == b.LMOE_OK
+
+
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp8"])
+def test_a_block_is_refused_while_another_device_is_current(lib, b, mx):
+    """Its memory lies on the other one, and a NULL stream would be this one's: nothing is launched."""
+    h = _block(lib, b, mx)
+    calls = _calls(lib, h, mx, 4) + _calls(lib, h, mx, 300) + [lambda: lib.lmoe_ffn_sync_status(h, None)]
+    lib.fake_set_device(1)
+    n = lib.fake_launches()
+    for call in calls:
+        assert call() == b.LMOE_ERR_INVALID_ARG
+    assert lib.fake_launches() == n
+    lib.fake_set_device(0)
+    assert all(call() == b.LMOE_OK for call in calls)
+    lib.fake_set_device(1)
+    assert lib.lmoe_ffn_destroy(h) == b.LMOE_OK
+
+
+def test_binding_refuses_a_block_while_another_device_is_current(monkeypatch):
+    built_library()
+    from latent_mixture_experts_gb300 import GatedFFN, feed_forward
+
+    class Lib:                       # reached by none of the calls
+        def __getattr__(self, name):
+            raise AssertionError(name)
+    block = GatedFFN.__new__(GatedFFN)
+    block._lib, block._h, block._dev, block._device = Lib(), None, 1, torch.device("cuda:1")
+    block.d_model, block.d_ff, block.max_tokens = 64, 128, 8
+    with FakeTensorMode():           # tensors of a device that this machine need not have
+        x, g = (torch.empty(4, n, device="cuda:1", dtype=torch.bfloat16) for n in (64, 128))
+        q, s = (torch.empty(4, n, device="cuda:1", dtype=torch.uint8) for n in (64, 2))
+    monkeypatch.setattr(feed_forward, "_raw_device", lambda: 0)
+    for call in (lambda: block.lmoe_ffn_forward(x), lambda: block.lmoe_ffn_forward(x, save=True),
+                 lambda: block.lmoe_ffn_backward(x, g, g, x), lambda: block.lmoe_ffn_forward_mx(q, s),
+                 lambda: block.lmoe_ffn_sync_status()):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
