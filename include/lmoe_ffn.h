@@ -133,8 +133,17 @@ LMOE_API lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x_cod
                                          void* out_bf16, cudaStream_t stream);
 
 /* Synchronise `stream` and return the first deferred error (a CUDA error, or
- * TIMEOUT of a kernel's bounded wait); clears the kernel-side flag. */
+ * TIMEOUT of a kernel's bounded wait); clears the kernel-side flag.  What the
+ * calls up to a TIMEOUT wrote is not valid; where a product's partial sums are
+ * joined, outputs of sums that are not whole are NaN. */
 LMOE_API lmoe_status lmoe_ffn_sync_status(lmoe_ffn_handle h, cudaStream_t stream);
+
+/* Self-test of the bounded waits: a forward pass on packed x (MXFP8: codes and
+ * scales) of whose rows each copy of the first product brings only half, so
+ * that its waits run out, after 2 s each, and lmoe_ffn_sync_status returns
+ * TIMEOUT.  The handle stays usable.  Errors as of the forward calls; T >= 1. */
+LMOE_API lmoe_status lmoe_ffn_selftest_timeout(lmoe_ffn_handle h, const void* x, const uint8_t* x_scales_opt, int T,
+                                               void* out_bf16, cudaStream_t stream);
 
 /* Kernels the last call on this handle launched. */
 LMOE_API int lmoe_ffn_last_launch_count(lmoe_ffn_handle h);

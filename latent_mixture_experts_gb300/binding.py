@@ -29,7 +29,7 @@ EXPORTS = ("lmoe_create", "lmoe_route", "lmoe_forward", "lmoe_forward_host", "lm
            "lmoe_ep_dispatch", "lmoe_ep_experts", "lmoe_ep_combine",
            "lmoe_add_rms_norm", "lmoe_add_rms_norm_backward_workspace", "lmoe_add_rms_norm_backward",
            "lmoe_ffn_create", "lmoe_ffn_forward", "lmoe_ffn_backward", "lmoe_ffn_forward_mx",
-           "lmoe_ffn_sync_status", "lmoe_ffn_last_launch_count", "lmoe_ffn_destroy")
+           "lmoe_ffn_sync_status", "lmoe_ffn_selftest_timeout", "lmoe_ffn_last_launch_count", "lmoe_ffn_destroy")
 NOALLOC_MAX_ASSIGNMENTS = 65536
 NOALLOC_MAX_EXPERTS = 2048
 PROFILE_ALL_STAGES = 0x1FF
@@ -123,6 +123,7 @@ def load_library(path: str = LIB_PATH):
             "lmoe_ffn_backward": (I, [P, P, L, P, P, P, L, I, P, P, P, P, P]),
             "lmoe_ffn_forward_mx": (I, [P, P, P, I, P, P]),
             "lmoe_ffn_sync_status": (I, [P, P]),
+            "lmoe_ffn_selftest_timeout": (I, [P, P, P, I, P, P]),
             "lmoe_ffn_last_launch_count": (I, [P]),
             "lmoe_ffn_destroy": (I, [P]),
         }

@@ -79,9 +79,13 @@ bool map_atoms(CUtensorMap* m, const void* base, size_t bytes, int box) {
                       CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// Rows that one copy of the tokens brings, of the `rows` that a stage waits for:
+// all of them, but half in the self-test of the waits.
+int token_rows(int rows, bool whole) { return whole ? rows : rows / 2; }
+
 // Weight-streaming passes: x (or hid) and the weights of one pass.  `whole`
 // maps split K into 64-wide chunks as an outer dimension.
-bool skinny_maps(FfnSkinnyParams& p, const void* a, long long lda, const void* w0, const void* w1, int K) {
+bool skinny_maps(FfnSkinnyParams& p, const void* a, long long lda, const void* w0, const void* w1, int K, int tb) {
   constexpr CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   constexpr CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const uint64_t k = K, row = 2 * k, rows = p.rows, M = p.M, T = p.T;
@@ -107,12 +111,12 @@ bool skinny_maps(FfnSkinnyParams& p, const void* a, long long lda, const void* w
     const bool b = p.apart ? true
                    : w1    ? make_tmap_4d(&p.b, dt, base, 64, M, 2, k / 64, row, step, 128, 64, rows, 2, p.kc, sw)
                            : make_tmap_3d(&p.b, dt, base, 64, M, k / 64, row, 128, 64, rows, p.kc, sw);
-    return b && make_tmap_3d(&p.a, dt, a, 64, T, k / 64, 2 * lda, 128, 64, p.tb, p.kc, sw);
+    return b && make_tmap_3d(&p.a, dt, a, 64, T, k / 64, 2 * lda, 128, 64, tb, p.kc, sw);
   }
   const bool b = p.apart ? true
                  : w1    ? make_tmap_3d(&p.b, dt, base, k, M, 2, row, step, 64, rows, 2, sw)
                          : make_tmap_2d(&p.b, dt, base, k, M, row, 64, rows, sw);
-  return b && make_tmap_2d(&p.a, dt, a, k, T, 2 * lda, 64, p.tb, sw);
+  return b && make_tmap_2d(&p.a, dt, a, k, T, 2 * lda, 64, tb, sw);
 }
 
 lmoe_status norm_args(int T, int d, const void* w, float eps, bool mx) {
@@ -129,6 +133,162 @@ lmoe_status row_args(const void* p, int64_t ld, int d) {
     const lmoe_status s_ = (expr);      \
     if (s_ != LMOE_OK) return s_;       \
   } while (0)
+
+// whole: false in the self-test.
+lmoe_status forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int T, void* out, void* gate, void* up, bool whole,
+                    cudaStream_t stream) {
+  if (!h || !on_its_device(h) || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
+  if (h->cfg.wfmt != LMOE_FFN_W_BF16) return LMOE_ERR_UNSUPPORTED;
+  h->launches = 0;
+  if (T == 0) return LMOE_OK;
+  const int d = h->cfg.d_model, F = h->cfg.d_ff;
+  FFN_TRY_STATUS(row_args(x, ldx, d));
+  if (!usable(out) || (gate == nullptr) != (up == nullptr) || !aligned16(gate) || !aligned16(up))
+    return LMOE_ERR_INVALID_ARG;
+  // Up to 72 tokens stream the weights (ffn_skinny.cu), larger batches run on
+  // pair tiles, K split where they are few.  Streaming against pair tiles, 64
+  // and 80 tokens: widths 7168 and 6144 54.6 and 60.4 us against 60.1 and 60.5 us;
+  // 7168 and 2048 24.1 and 26.3 us against 26.3 and 27.1 us; 2048 and 2048 12.4
+  // and 13.7 us against 12.2 and 13.0 us; 1152 and 864 9.2 and 10.2 us against 8.6
+  // and 9.5 us.
+  if (T <= kSkinnyMaxTokens) {
+    FfnSkinnyParams g = {}, n = {};
+    g.T = n.T = T;
+    g.M = F;
+    n.M = d;
+    g.chunks = ceil_div(d, 64);
+    n.chunks = ceil_div(F, 64);
+    if (ffn_skinny_plan(g, true) && ffn_skinny_plan(n, false)) {
+      g.b1 = h->cfg.situ_beta;
+      g.b2 = h->cfg.situ_linear_beta;
+      g.err = n.err = h->err;
+      g.out = h->hid;
+      g.save_g = gate;
+      g.save_u = up;
+      n.out = out;
+      if (!skinny_maps(g, x, ldx, h->w.gate, h->w.up, d, token_rows(g.tb, whole)) ||
+          !skinny_maps(n, h->hid, F, h->w.down, nullptr, F, n.tb))
+        return LMOE_ERR_CUDA;
+      FFN_TRY(launch_ffn_skinny(g, true, h->cfg.act == LMOE_ACT_SWIGLU, stream));
+      FFN_TRY(launch_ffn_skinny(n, false, 0, stream));
+      h->launches = 2;
+      return LMOE_OK;
+    }
+  }
+  FfnPairParams p = {};
+  p.b1 = h->cfg.situ_beta;
+  p.b2 = h->cfg.situ_linear_beta;
+  p.act = h->cfg.act == LMOE_ACT_SWIGLU;
+  p.err = h->err;
+  p.nprod = 1;
+  p.M[0] = T;
+  p.N[0] = F;
+  p.nkb = ceil_div(d, 64);
+  p.out[0] = h->hid;
+  p.out[1] = gate;
+  p.out[2] = up;
+  if (!map_k(&p.a[0], x, d, T, ldx, token_rows(128, whole))) return LMOE_ERR_CUDA;
+  int splits = ffn_split_plan(p, kFfnGateUp, h->split);
+  if (splits > 1) {
+    p.b[0] = h->gate[1];
+    p.b[1] = h->up[1];
+    FFN_TRY(launch_ffn_split(kFfnGateUp, p, splits, stream));
+    p.early = 1;
+  } else {
+    const int tn = ffn_pair_tiles(p, kFfnGateUp, h->ctas);
+    p.b[0] = h->gate[tn == 128];
+    p.b[1] = h->up[tn == 128];
+    p.b_half[0] = h->gate[1];
+    p.b_half[1] = h->up[1];
+    FFN_TRY(launch_ffn_pair(kFfnGateUp, p, tn, h->ctas, stream));
+  }
+  p.N[0] = d;
+  p.nkb = ceil_div(F, 64);
+  p.out[0] = out;
+  if (!map_k(&p.a[0], h->hid, F, T, F)) return LMOE_ERR_CUDA;
+  splits = ffn_split_plan(p, kFfnPlain, h->split);
+  if (splits > 1) {
+    p.b[0] = h->down[1];
+    FFN_TRY(launch_ffn_split(kFfnPlain, p, splits, stream));
+  } else {
+    p.early = 0;
+    const int tn = ffn_pair_tiles(p, kFfnPlain, h->ctas);
+    p.b[0] = h->down[tn == 128];
+    p.b_half[0] = h->down[1];
+    FFN_TRY(launch_ffn_pair(kFfnPlain, p, tn, h->ctas, stream));
+  }
+  h->launches = 2;
+  return LMOE_OK;
+}
+
+lmoe_status forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8_t* x_scales, int T, void* out, bool whole,
+                       cudaStream_t stream) {
+  if (!h || !on_its_device(h) || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
+  if (h->cfg.wfmt != LMOE_FFN_W_MXFP8) return LMOE_ERR_UNSUPPORTED;
+  h->launches = 0;
+  if (T == 0) return LMOE_OK;
+  if (!usable(x) || !usable(x_scales) || !usable(out)) return LMOE_ERR_INVALID_ARG;
+  const int d = h->cfg.d_model, F = h->cfg.d_ff;
+  FfnMxSkinnyParams g = {}, n = {};
+  g.T = n.T = T;
+  g.M = F;
+  n.M = d;
+  g.nkb = ceil_div(d, 128);
+  n.nkb = ceil_div(F, 128);
+  if (ffn_mx_skinny_plan(g, true) && ffn_mx_skinny_plan(n, false)) {
+    g.b1 = h->cfg.situ_beta;
+    g.b2 = h->cfg.situ_linear_beta;
+    g.err = n.err = h->err;
+    g.kblks = d / 32;
+    g.b[0] = h->gate[1];
+    g.b[1] = h->up[1];
+    g.sfb = h->m_gu_sf[1];
+    g.row_sf = x_scales;
+    g.out = h->hid;
+    g.out_sf = h->hid_sf;
+    n.b[0] = h->down[1];
+    n.sfb = h->m_down_sf[1];
+    n.row_sf = h->hid_sf;
+    n.out = out;
+    if (!map_mx(&g.a, x, d, T, token_rows(g.tb, whole)) || !map_mx(&n.a, h->hid, F, T, n.tb)) return LMOE_ERR_CUDA;
+    FFN_TRY(launch_ffn_mx_skinny(g, true, h->cfg.act == LMOE_ACT_SWIGLU, stream));
+    FFN_TRY(launch_ffn_mx_skinny(n, false, 0, stream));
+    h->launches = 2;
+    return LMOE_OK;
+  }
+  FFN_TRY(launch_mx_row_atoms(x_scales, T, d, h->x_sf, stream));
+  FfnMxParams p = {};
+  p.b1 = h->cfg.situ_beta;
+  p.b2 = h->cfg.situ_linear_beta;
+  p.act = h->cfg.act == LMOE_ACT_SWIGLU;
+  p.err = h->err;
+  p.sfa = h->m_x_sf;
+  p.out = h->hid;
+  p.out_sf = h->hid_sf;
+  p.out_nkb = ceil_div(F, 128);
+  p.M = T;
+  p.N = F;
+  p.nkb = ceil_div(d, 128);
+  int tn = ffn_mx_tiles(p, true, h->ctas), i = tn == kMxTileN[1];
+  p.b[0] = h->gate[i];
+  p.b[1] = h->up[i];
+  p.sfb = h->m_gu_sf[i];
+  if (!map_mx(&p.a, x, d, T, token_rows(128, whole))) return LMOE_ERR_CUDA;
+  FFN_TRY(launch_ffn_mx_pair(p, true, tn, h->ctas, stream));
+  p.sfa = h->m_hid_sf;
+  p.out = out;
+  p.wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;   // d is a multiple of 32
+  p.N = d;
+  p.nkb = ceil_div(F, 128);
+  tn = ffn_mx_tiles(p, false, h->ctas);
+  i = tn == kMxTileN[1];
+  p.b[0] = h->down[i];
+  p.sfb = h->m_down_sf[i];
+  if (!map_mx(&p.a, h->hid, F, T, 128)) return LMOE_ERR_CUDA;
+  FFN_TRY(launch_ffn_mx_pair(p, false, tn, h->ctas, stream));
+  h->launches = 3;
+  return LMOE_OK;
+}
 
 }  // namespace
 
@@ -282,87 +442,7 @@ lmoe_status lmoe_ffn_destroy(lmoe_ffn_handle h) {
 
 lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int T, void* out, void* gate, void* up,
                              cudaStream_t stream) {
-  if (!h || !on_its_device(h) || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
-  if (h->cfg.wfmt != LMOE_FFN_W_BF16) return LMOE_ERR_UNSUPPORTED;
-  h->launches = 0;
-  if (T == 0) return LMOE_OK;
-  const int d = h->cfg.d_model, F = h->cfg.d_ff;
-  FFN_TRY_STATUS(row_args(x, ldx, d));
-  if (!usable(out) || (gate == nullptr) != (up == nullptr) || !aligned16(gate) || !aligned16(up))
-    return LMOE_ERR_INVALID_ARG;
-  // Up to 72 tokens stream the weights (ffn_skinny.cu), larger batches run on
-  // pair tiles, K split where they are few.  Streaming against pair tiles, 64
-  // and 80 tokens: widths 7168 and 6144 54.6 and 60.4 us against 60.1 and 60.5 us;
-  // 7168 and 2048 24.1 and 26.3 us against 26.3 and 27.1 us; 2048 and 2048 12.4
-  // and 13.7 us against 12.2 and 13.0 us; 1152 and 864 9.2 and 10.2 us against 8.6
-  // and 9.5 us.
-  if (T <= kSkinnyMaxTokens) {
-    FfnSkinnyParams g = {}, n = {};
-    g.T = n.T = T;
-    g.M = F;
-    n.M = d;
-    g.chunks = ceil_div(d, 64);
-    n.chunks = ceil_div(F, 64);
-    if (ffn_skinny_plan(g, true) && ffn_skinny_plan(n, false)) {
-      g.b1 = h->cfg.situ_beta;
-      g.b2 = h->cfg.situ_linear_beta;
-      g.err = n.err = h->err;
-      g.out = h->hid;
-      g.save_g = gate;
-      g.save_u = up;
-      n.out = out;
-      if (!skinny_maps(g, x, ldx, h->w.gate, h->w.up, d) || !skinny_maps(n, h->hid, F, h->w.down, nullptr, F))
-        return LMOE_ERR_CUDA;
-      FFN_TRY(launch_ffn_skinny(g, true, h->cfg.act == LMOE_ACT_SWIGLU, stream));
-      FFN_TRY(launch_ffn_skinny(n, false, 0, stream));
-      h->launches = 2;
-      return LMOE_OK;
-    }
-  }
-  FfnPairParams p = {};
-  p.b1 = h->cfg.situ_beta;
-  p.b2 = h->cfg.situ_linear_beta;
-  p.act = h->cfg.act == LMOE_ACT_SWIGLU;
-  p.err = h->err;
-  p.nprod = 1;
-  p.M[0] = T;
-  p.N[0] = F;
-  p.nkb = ceil_div(d, 64);
-  p.out[0] = h->hid;
-  p.out[1] = gate;
-  p.out[2] = up;
-  if (!map_k(&p.a[0], x, d, T, ldx)) return LMOE_ERR_CUDA;
-  int splits = ffn_split_plan(p, kFfnGateUp, h->split);
-  if (splits > 1) {
-    p.b[0] = h->gate[1];
-    p.b[1] = h->up[1];
-    FFN_TRY(launch_ffn_split(kFfnGateUp, p, splits, stream));
-    p.early = 1;
-  } else {
-    const int tn = ffn_pair_tiles(p, kFfnGateUp, h->ctas);
-    p.b[0] = h->gate[tn == 128];
-    p.b[1] = h->up[tn == 128];
-    p.b_half[0] = h->gate[1];
-    p.b_half[1] = h->up[1];
-    FFN_TRY(launch_ffn_pair(kFfnGateUp, p, tn, h->ctas, stream));
-  }
-  p.N[0] = d;
-  p.nkb = ceil_div(F, 64);
-  p.out[0] = out;
-  if (!map_k(&p.a[0], h->hid, F, T, F)) return LMOE_ERR_CUDA;
-  splits = ffn_split_plan(p, kFfnPlain, h->split);
-  if (splits > 1) {
-    p.b[0] = h->down[1];
-    FFN_TRY(launch_ffn_split(kFfnPlain, p, splits, stream));
-  } else {
-    p.early = 0;
-    const int tn = ffn_pair_tiles(p, kFfnPlain, h->ctas);
-    p.b[0] = h->down[tn == 128];
-    p.b_half[0] = h->down[1];
-    FFN_TRY(launch_ffn_pair(kFfnPlain, p, tn, h->ctas, stream));
-  }
-  h->launches = 2;
-  return LMOE_OK;
+  return forward(h, x, ldx, T, out, gate, up, true, stream);
 }
 
 lmoe_status lmoe_ffn_backward(lmoe_ffn_handle h, const void* x, int64_t ldx, const void* gate, const void* up,
@@ -460,71 +540,15 @@ lmoe_status lmoe_ffn_backward(lmoe_ffn_handle h, const void* x, int64_t ldx, con
 
 lmoe_status lmoe_ffn_forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8_t* x_scales, int T, void* out,
                                 cudaStream_t stream) {
-  if (!h || !on_its_device(h) || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
-  if (h->cfg.wfmt != LMOE_FFN_W_MXFP8) return LMOE_ERR_UNSUPPORTED;
-  h->launches = 0;
-  if (T == 0) return LMOE_OK;
-  if (!usable(x) || !usable(x_scales) || !usable(out)) return LMOE_ERR_INVALID_ARG;
-  const int d = h->cfg.d_model, F = h->cfg.d_ff;
-  FfnMxSkinnyParams g = {}, n = {};
-  g.T = n.T = T;
-  g.M = F;
-  n.M = d;
-  g.nkb = ceil_div(d, 128);
-  n.nkb = ceil_div(F, 128);
-  if (ffn_mx_skinny_plan(g, true) && ffn_mx_skinny_plan(n, false)) {
-    g.b1 = h->cfg.situ_beta;
-    g.b2 = h->cfg.situ_linear_beta;
-    g.err = n.err = h->err;
-    g.kblks = d / 32;
-    g.b[0] = h->gate[1];
-    g.b[1] = h->up[1];
-    g.sfb = h->m_gu_sf[1];
-    g.row_sf = x_scales;
-    g.out = h->hid;
-    g.out_sf = h->hid_sf;
-    n.b[0] = h->down[1];
-    n.sfb = h->m_down_sf[1];
-    n.row_sf = h->hid_sf;
-    n.out = out;
-    if (!map_mx(&g.a, x, d, T, g.tb) || !map_mx(&n.a, h->hid, F, T, n.tb)) return LMOE_ERR_CUDA;
-    FFN_TRY(launch_ffn_mx_skinny(g, true, h->cfg.act == LMOE_ACT_SWIGLU, stream));
-    FFN_TRY(launch_ffn_mx_skinny(n, false, 0, stream));
-    h->launches = 2;
-    return LMOE_OK;
-  }
-  FFN_TRY(launch_mx_row_atoms(x_scales, T, d, h->x_sf, stream));
-  FfnMxParams p = {};
-  p.b1 = h->cfg.situ_beta;
-  p.b2 = h->cfg.situ_linear_beta;
-  p.act = h->cfg.act == LMOE_ACT_SWIGLU;
-  p.err = h->err;
-  p.sfa = h->m_x_sf;
-  p.out = h->hid;
-  p.out_sf = h->hid_sf;
-  p.out_nkb = ceil_div(F, 128);
-  p.M = T;
-  p.N = F;
-  p.nkb = ceil_div(d, 128);
-  int tn = ffn_mx_tiles(p, true, h->ctas), i = tn == kMxTileN[1];
-  p.b[0] = h->gate[i];
-  p.b[1] = h->up[i];
-  p.sfb = h->m_gu_sf[i];
-  if (!map_mx(&p.a, x, d, T, 128)) return LMOE_ERR_CUDA;
-  FFN_TRY(launch_ffn_mx_pair(p, true, tn, h->ctas, stream));
-  p.sfa = h->m_hid_sf;
-  p.out = out;
-  p.wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;   // d is a multiple of 32
-  p.N = d;
-  p.nkb = ceil_div(F, 128);
-  tn = ffn_mx_tiles(p, false, h->ctas);
-  i = tn == kMxTileN[1];
-  p.b[0] = h->down[i];
-  p.sfb = h->m_down_sf[i];
-  if (!map_mx(&p.a, h->hid, F, T, 128)) return LMOE_ERR_CUDA;
-  FFN_TRY(launch_ffn_mx_pair(p, false, tn, h->ctas, stream));
-  h->launches = 3;
-  return LMOE_OK;
+  return forward_mx(h, x, x_scales, T, out, true, stream);
+}
+
+lmoe_status lmoe_ffn_selftest_timeout(lmoe_ffn_handle h, const void* x, const uint8_t* x_scales, int T, void* out,
+                                      cudaStream_t stream) {
+  if (!h || T < 1) return LMOE_ERR_INVALID_ARG;
+  if (h->cfg.wfmt == LMOE_FFN_W_MXFP8)
+    return forward_mx(h, static_cast<const uint8_t*>(x), x_scales, T, out, false, stream);
+  return forward(h, x, h->cfg.d_model, T, out, nullptr, nullptr, false, stream);
 }
 
 lmoe_status lmoe_ffn_sync_status(lmoe_ffn_handle h, cudaStream_t stream) {

@@ -151,10 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
     // ran out, the copies in flight get a millisecond to land
     const uint32_t used = it < kStages ? it : kStages;
     for (uint32_t j = it - used; j < it && ok; ++j) ok = warp_wait(&empty[j % kStages], (j / kStages) & 1, p.err);
-    if (!ok) {
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
-    }
+    if (!ok) let_copies_land();
   } else if (warp == 1) {
     named_arrive(kTmemBarrier, kThreads - 32);
     if (rank == 0) {

@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
   uint8_t* sm = align1024(smem_raw);
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done, rows_ready;
   __shared__ uint32_t tmem_base;
+  __shared__ int lost;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known uniform
   const int rank = static_cast<int>(cluster_rank());
   const int tile = static_cast<int>(blockIdx.x) / p.splits;
@@ -58,6 +59,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
       mbar_init(&empty[i], 1);
     }
     mbar_init(&done, 1);
+    lost = 0;
     mbar_init(&rows_ready, GU ? blockDim.x / 32 - 2 : 1);
     fence_mbar_init();
   }
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
       w_commit(&empty[s]);
       if (++s == p.stages) s = 0, phase ^= 1;
     }
-    w_commit(&done);
+    if (ok) w_commit(&done);
   } else if constexpr (GU) {
     // x's scales of this K range, from rows [T][K/32] to the MMA's image
     const int t0 = threadIdx.x - 64;
@@ -149,10 +151,13 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
   __syncwarp();
 
   const bool ok = mbar_wait(&done, 0, p.err, kErrTimeout);
+  if (!ok) let_copies_land();
   tc_fence_after();
   __syncwarp();
   if (p.reuse_ring) cluster_arrive();
   cluster_wait();
+  if (!ok) cluster_lost(&lost, p.splits);
+  __syncwarp();
   // Token t is finished by CTA t / per: its row of partial sums goes to that
   // CTA's shared memory, one block [per][kPitch] for each source rank.
   const int per = (p.T + p.splits - 1) / p.splits;
@@ -176,6 +181,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
   cluster_arrive();
   cluster_wait();
   const int tok0 = rank * per, ntok = min(per, p.T - tok0);
+  const float nan = __int_as_float(0x7FC00000);      // of sums that are not whole
   if constexpr (GU) {
     // one warp for each token and block of 32 features, lane = feature
     constexpr int kBlocks = kHalf / 32;
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
         g += src[0];
         u += src[kHalf];
       }
-      const float h = ok ? glu_hidden<ACT>(g, u, caps) : 0.0f;
+      const float h = lost ? nan : glu_hidden<ACT>(g, u, caps);
       const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h)));
       // an infinity or NaN makes the block NaN: E8M0 byte 255
       const uint32_t s = m >= 0x7F800000u ? 255u : e4m3_block_scale(__uint_as_float(m));
@@ -208,7 +214,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
         const float2 a = *reinterpret_cast<const float2*>(recv + (r * per + i) * kPitch + c);
         v.x += a.x, v.y += a.y;
       }
-      if (!ok) v = make_float2(0.f, 0.f);
+      if (lost) v = make_float2(nan, nan);
       *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(tok0 + i) * p.M + f) =
           pack_bf16(v.x, v.y);
     }

@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
   uint8_t* sm = align1024(smem_raw);
   __shared__ uint64_t full[kSkinnyMaxStages], empty[kSkinnyMaxStages], done;
   __shared__ uint32_t tmem_base;
+  __shared__ int lost;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known uniform
   constexpr int N = kCols, rows = GU ? N / 2 : N;     // features of the cluster
   const int rank = static_cast<int>(cluster_rank());  // K split of this CTA
@@ -55,6 +56,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
       mbar_init(&empty[i], 1);
     }
     mbar_init(&done, 1);
+    lost = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
       w_commit(&empty[s]);
       if (++s == p.stages) s = 0, phase ^= 1;
     }
-    w_commit(&done);
+    if (ok) w_commit(&done);
   }
   __syncwarp();
 
@@ -157,9 +159,12 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
   // [token][fs columns, GU: gate then up] per source rank, and are added in
   // rank order by all of its threads, features along threads.
   const bool ok = mbar_wait(&done, 0, p.err, kErrTimeout);
+  if (!ok) let_copies_land();
   tc_fence_after();
   __syncwarp();
   cluster_wait();
+  if (!ok) cluster_lost(&lost, p.splits);
+  __syncwarp();
   const int lfs = 31 - __clz(rows / p.splits), fs = 1 << lfs;
   const int pitch = N / p.splits + 4;   // 16-byte rows, four banks apart
   float* recv = reinterpret_cast<float*>(sm + p.recv);
@@ -186,6 +191,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
   cluster_arrive();
   cluster_wait();
   const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
+  const float nan = __int_as_float(0x7FC00000);      // of sums that are not whole
   const int shift = lfs - 1;        // log2 of the pairs of features
   const int f1 = f0 + rank * fs, left = p.M - f1;
   for (int e = threadIdx.x; e < p.T << shift; e += blockDim.x) {
@@ -201,7 +207,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
         w.x += b.x, w.y += b.y;
       }
     }
-    if (!ok) v = w = make_float2(0.f, 0.f);
+    if (lost) v = w = make_float2(nan, nan);
     const size_t at = static_cast<size_t>(t) * p.M + f1 + f;
     if constexpr (GU) {
       const float2 g = p.swapped ? w : v, u = p.swapped ? v : w;

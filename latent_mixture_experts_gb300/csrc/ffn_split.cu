@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(kThreads) ffn_split_kernel(const __grid_consta
   uint8_t* sm = align1024(smem_raw);
   __shared__ uint64_t full[kStages], empty[kStages], done;
   __shared__ uint32_t tmem_base;
+  __shared__ int lost;
 
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known uniform
   const uint32_t crank = cluster_rank(), rank = crank & 1, leader = crank & ~1u;
@@ -51,6 +52,7 @@ __global__ void __launch_bounds__(kThreads) ffn_split_kernel(const __grid_consta
       mbar_init(&empty[i], 1);
     }
     mbar_init(&done, 1);
+    lost = 0;
     fence_mbar_init();
   }
   __syncwarp();
@@ -145,14 +147,13 @@ __global__ void __launch_bounds__(kThreads) ffn_split_kernel(const __grid_consta
     }
   }
 
-  // The products are done, and so the ring's loads.  If a wait ran out, the
-  // copies in flight get a millisecond to land.
+  // The products are done, and so the ring's loads.
   __syncthreads();      // tmem_base
   const uint32_t tacc = tmem_base;
   const bool ok = mbar_wait_cluster(&done, 0, p.err, kErrTimeout);
   if (!ok) {
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    let_copies_land();
+    cluster_lost(&lost, 2 * S);
   }
   tc_fence_after();
   __syncwarp();
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(kThreads) ffn_split_kernel(const __grid_consta
 
   const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
   const float4* part = reinterpret_cast<const float4*>(recv);
+  const float nan = __int_as_float(0x7FC00000);      // of sums that are not whole
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int e = threadIdx.x + i * kThreads, r = e / kOwn, quad = e % kOwn, row = m0 + r, f = f0 + 4 * quad;
@@ -199,6 +201,7 @@ __global__ void __launch_bounds__(kThreads) ffn_split_kernel(const __grid_consta
         w.x += b.x, w.y += b.y, w.z += b.z, w.w += b.w;
       }
     }
+    if (lost) v = w = make_float4(nan, nan, nan, nan);
     const size_t at = static_cast<size_t>(row) * N + f;
     const auto put = [&](void* out, uint32_t lo, uint32_t hi) {
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) = make_uint2(lo, hi);

@@ -40,6 +40,14 @@ __device__ __forceinline__ void st_cluster4(uint32_t addr, const uint32_t* v) {
                "r"(v[3])
                : "memory");
 }
+// Partial sums that a cluster joins are whole only if no wait of any of its
+// CTAs ran out: a thread whose wait did sets `lost`, a flag in the shared memory
+// of each CTA, in all `ctas` of them, between the cluster's start and its last
+// barrier; behind that barrier every CTA reads its own.
+__device__ __forceinline__ void cluster_lost(int* lost, int ctas) {
+  for (int r = 0; r < ctas; ++r)
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(map_rank(lost, r)), "r"(1) : "memory");
+}
 // Without release: for what the arriving thread has waited for itself (loads
 // from tensor memory).  A release at cluster scope waits until the thread's
 // global stores have arrived: 256 tokens' weight gradients at 7168 x 2048 took

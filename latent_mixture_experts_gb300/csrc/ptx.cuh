@@ -68,6 +68,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
   }
 }
 
+// After a wait that ran out: the copies and products in flight get a
+// millisecond to end, before the shared memory that they use serves anything else.
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+}
+
 // --------------------------------------------------------------------- TMA
 // L2 prefetch of `bytes` (a multiple of 16) from a 16-byte-aligned global address.
 __device__ __forceinline__ void prefetch_l2_bulk(const void* src, uint32_t bytes) {

@@ -297,6 +297,19 @@ class GatedFFN:
         self._current()
         B._check("lmoe_ffn_sync_status", self._lib.lmoe_ffn_sync_status(self._h, B._stream(stream)))
 
+    def lmoe_ffn_selftest_timeout(self, x: torch.Tensor, x_scales: torch.Tensor | None = None, stream=None):
+        """A forward pass whose first product waits for rows that never come:
+        the next lmoe_ffn_sync_status reports a timeout.  Returns its output."""
+        self._current()
+        _packed("x", x, _U8 if self.mx else _BF16, (x.shape[0], self.d_model))
+        if self.mx:
+            _packed("x_scales", x_scales, _U8, (x.shape[0], self.d_model // 32))
+        y = torch.empty(x.shape[0], self.d_model, dtype=_BF16, device=self._device)
+        B._check("lmoe_ffn_selftest_timeout", self._lib.lmoe_ffn_selftest_timeout(
+            self._h, x.data_ptr(), x_scales.data_ptr() if self.mx else None, x.shape[0], y.data_ptr(),
+            B._stream(stream)))
+        return y
+
     def lmoe_ffn_last_launch_count(self) -> int:
         return int(self._lib.lmoe_ffn_last_launch_count(self._h))
 

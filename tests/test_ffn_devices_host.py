@@ -123,3 +123,17 @@ def test_binding_refuses_a_block_while_another_device_is_current(monkeypatch):
                  lambda: block.lmoe_ffn_sync_status()):
         with pytest.raises(ValueError, match="current CUDA device"):
             call()
+
+
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp8"])
+def test_self_test_arguments(lib, b, mx):
+    h = _block(lib, b, mx)
+    for T in (1, 16, 40, 300, 4096):
+        assert lib.lmoe_ffn_selftest_timeout(h, A, A, T, A, None) == b.LMOE_OK
+    for x, s, T, out in ((None, A, 4, A), (A, A, 0, A), (A, A, -1, A), (A, A, 4097, A), (A, A, 4, None), (A + 8, A, 4, A),
+                         (A, None if mx else A, 4, A if mx else A + 2)):
+        assert lib.lmoe_ffn_selftest_timeout(h, x, s, T, out, None) == b.LMOE_ERR_INVALID_ARG
+    lib.fake_set_device(1)
+    assert lib.lmoe_ffn_selftest_timeout(h, A, A, 4, A, None) == b.LMOE_ERR_INVALID_ARG
+    lib.fake_set_device(0)
+    assert lib.lmoe_ffn_destroy(h) == b.LMOE_OK

@@ -102,6 +102,7 @@ def test_ffn_null_handle(lib, b):
     assert lib.lmoe_ffn_backward(None, A, 64, A, A, A, 64, 1, A, A, A, A, None) == inv
     assert lib.lmoe_ffn_forward_mx(None, A, A, 1, A, None) == inv
     assert lib.lmoe_ffn_sync_status(None, None) == inv
+    assert lib.lmoe_ffn_selftest_timeout(None, A, A, 1, A, None) == inv
     assert lib.lmoe_ffn_last_launch_count(None) == 0
     assert lib.lmoe_ffn_destroy(None) == b.LMOE_OK
 
