@@ -151,12 +151,12 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
   __syncwarp();
 
   const bool ok = mbar_wait(&done, 0, p.err, kErrTimeout);
-  if (!ok) let_copies_land();
+  if (__builtin_expect(!ok, 0)) let_copies_land();
   tc_fence_after();
   __syncwarp();
   if (p.reuse_ring) cluster_arrive();
   cluster_wait();
-  if (!ok) cluster_lost(&lost, p.splits);
+  if (__builtin_expect(!ok, 0)) cluster_lost(&lost, p.splits);
   __syncwarp();
   // Token t is finished by CTA t / per: its row of partial sums goes to that
   // CTA's shared memory, one block [per][kPitch] for each source rank.
@@ -181,7 +181,10 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
   cluster_arrive();
   cluster_wait();
   const int tok0 = rank * per, ntok = min(per, p.T - tok0);
-  const float nan = __int_as_float(0x7FC00000);      // of sums that are not whole
+  if (__builtin_expect(lost, 0)) {      // sums that are not whole become NaN by their first part
+    for (int e = threadIdx.x; e < per * kPitch; e += blockDim.x) recv[e] = __int_as_float(0x7FC00000);
+    __syncthreads();
+  }
   if constexpr (GU) {
     // one warp for each token and block of 32 features, lane = feature
     constexpr int kBlocks = kHalf / 32;
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
         g += src[0];
         u += src[kHalf];
       }
-      const float h = lost ? nan : glu_hidden<ACT>(g, u, caps);
+      const float h = glu_hidden<ACT>(g, u, caps);
       const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h)));
       // an infinity or NaN makes the block NaN: E8M0 byte 255
       const uint32_t s = m >= 0x7F800000u ? 255u : e4m3_block_scale(__uint_as_float(m));
@@ -214,7 +217,6 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
         const float2 a = *reinterpret_cast<const float2*>(recv + (r * per + i) * kPitch + c);
         v.x += a.x, v.y += a.y;
       }
-      if (lost) v = make_float2(nan, nan);
       *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(tok0 + i) * p.M + f) =
           pack_bf16(v.x, v.y);
     }

@@ -159,11 +159,11 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
   // [token][fs columns, GU: gate then up] per source rank, and are added in
   // rank order by all of its threads, features along threads.
   const bool ok = mbar_wait(&done, 0, p.err, kErrTimeout);
-  if (!ok) let_copies_land();
+  if (__builtin_expect(!ok, 0)) let_copies_land();
   tc_fence_after();
   __syncwarp();
   cluster_wait();
-  if (!ok) cluster_lost(&lost, p.splits);
+  if (__builtin_expect(!ok, 0)) cluster_lost(&lost, p.splits);
   __syncwarp();
   const int lfs = 31 - __clz(rows / p.splits), fs = 1 << lfs;
   const int pitch = N / p.splits + 4;   // 16-byte rows, four banks apart
@@ -191,7 +191,10 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
   cluster_arrive();
   cluster_wait();
   const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
-  const float nan = __int_as_float(0x7FC00000);      // of sums that are not whole
+  if (__builtin_expect(lost, 0)) {      // sums that are not whole become NaN by their first part
+    for (int e = threadIdx.x; e < p.T * pitch; e += blockDim.x) recv[e] = __int_as_float(0x7FC00000);
+    __syncthreads();
+  }
   const int shift = lfs - 1;        // log2 of the pairs of features
   const int f1 = f0 + rank * fs, left = p.M - f1;
   for (int e = threadIdx.x; e < p.T << shift; e += blockDim.x) {
@@ -207,7 +210,6 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
         w.x += b.x, w.y += b.y;
       }
     }
-    if (lost) v = w = make_float2(nan, nan);
     const size_t at = static_cast<size_t>(t) * p.M + f1 + f;
     if constexpr (GU) {
       const float2 g = p.swapped ? w : v, u = p.swapped ? v : w;

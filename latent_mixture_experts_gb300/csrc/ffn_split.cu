@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) ffn_split_kernel(const __grid_consta
   __syncthreads();      // tmem_base
   const uint32_t tacc = tmem_base;
   const bool ok = mbar_wait_cluster(&done, 0, p.err, kErrTimeout);
-  if (!ok) {
+  if (__builtin_expect(!ok, 0)) {
     let_copies_land();
     cluster_lost(&lost, 2 * S);
   }
@@ -186,7 +186,12 @@ __global__ void __launch_bounds__(kThreads) ffn_split_kernel(const __grid_consta
 
   const GluCaps caps = {p.b1, p.b2, 1.0f / p.b1, 1.0f / p.b2};
   const float4* part = reinterpret_cast<const float4*>(recv);
-  const float nan = __int_as_float(0x7FC00000);      // of sums that are not whole
+  if (__builtin_expect(lost, 0)) {      // sums that are not whole become NaN by their first part
+    const float nan = __int_as_float(0x7FC00000);
+    for (int e = threadIdx.x; e < 128 * kQuads; e += kThreads)
+      reinterpret_cast<float4*>(recv)[e / 128 * kPitch + e % 128] = make_float4(nan, nan, nan, nan);
+    __syncthreads();
+  }
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int e = threadIdx.x + i * kThreads, r = e / kOwn, quad = e % kOwn, row = m0 + r, f = f0 + 4 * quad;
@@ -201,7 +206,6 @@ __global__ void __launch_bounds__(kThreads) ffn_split_kernel(const __grid_consta
         w.x += b.x, w.y += b.y, w.z += b.z, w.w += b.w;
       }
     }
-    if (lost) v = w = make_float4(nan, nan, nan, nan);
     const size_t at = static_cast<size_t>(row) * N + f;
     const auto put = [&](void* out, uint32_t lo, uint32_t hi) {
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) = make_uint2(lo, hi);
