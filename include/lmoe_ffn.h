@@ -58,12 +58,23 @@ LMOE_API lmoe_status lmoe_add_rms_norm(const void* x_bf16, int64_t ldx, const vo
  * over rows are added in an order that depends on T, d, the types and whether
  * dh is given only.
  * T = 0 writes dw = 0.  A bounded wait of the kernel that runs out (there is
- * no handle to report it by) leaves NaN in dw.  Errors as above. */
+ * no handle to report it by) leaves NaN in dw and dx, in the forward pass in
+ * the rows of y.  Errors as above. */
 LMOE_API lmoe_status lmoe_add_rms_norm_backward_workspace(int T, int d, size_t* bytes);
 LMOE_API lmoe_status lmoe_add_rms_norm_backward(const void* dy_bf16, int64_t lddy, const void* h, int64_t ldh,
                                                 const void* dh_opt, int64_t lddh, lmoe_stream_type stream_type,
                                                 int T, int d, const void* w_bf16, float eps, void* dx, float* dw,
                                                 void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Self-test of the norm kernels' bounded waits (2 s each): a pass over packed
+ * bf16 x [T][d] of whose rows 16 bytes are waited for that no copy brings, so
+ * that all waits run out.  Forward: all of y [T][d] is NaN.  backward != 0: x is
+ * dy and h, y is dx, and both y and dw are NaN.  Errors as above, and UNSUPPORTED for a
+ * forward pass on fewer than 2^23 values; T >= 1. */
+LMOE_API lmoe_status lmoe_add_rms_norm_selftest_timeout(int backward, const void* x_bf16, int T, int d,
+                                                        const void* w_bf16, void* y_bf16, float* dw_opt,
+                                                        void* workspace_opt, size_t workspace_bytes,
+                                                        cudaStream_t stream);
 
 /* ------------------------------------------- dense gated feed-forward */
 typedef enum { LMOE_FFN_W_BF16 = 0, LMOE_FFN_W_MXFP8 = 1 } lmoe_ffn_wfmt;

@@ -28,6 +28,7 @@ EXPORTS = ("lmoe_create", "lmoe_route", "lmoe_forward", "lmoe_forward_host", "lm
            "lmoe_qb_update", "lmoe_qb_histogram", "lmoe_qb_update_from_histogram",
            "lmoe_ep_dispatch", "lmoe_ep_experts", "lmoe_ep_combine",
            "lmoe_add_rms_norm", "lmoe_add_rms_norm_backward_workspace", "lmoe_add_rms_norm_backward",
+           "lmoe_add_rms_norm_selftest_timeout",
            "lmoe_ffn_create", "lmoe_ffn_forward", "lmoe_ffn_backward", "lmoe_ffn_forward_mx",
            "lmoe_ffn_sync_status", "lmoe_ffn_selftest_timeout", "lmoe_ffn_last_launch_count", "lmoe_ffn_destroy")
 NOALLOC_MAX_ASSIGNMENTS = 65536
@@ -117,6 +118,7 @@ def load_library(path: str = LIB_PATH):
             "lmoe_add_rms_norm": (I, [P, L, P, L, I, I, I, P, F, P, P, I, P, P]),
             "lmoe_add_rms_norm_backward_workspace": (I, [I, I, ctypes.POINTER(S)]),
             "lmoe_add_rms_norm_backward": (I, [P, L, P, L, P, L, I, I, I, P, F, P, P, P, S, P]),
+            "lmoe_add_rms_norm_selftest_timeout": (I, [I, P, I, I, P, P, P, P, S, P]),
             "lmoe_ffn_create": (I, [ctypes.POINTER(LmoeFfnConfig), ctypes.POINTER(LmoeFfnWeights), P,
                                     ctypes.POINTER(P)]),
             "lmoe_ffn_forward": (I, [P, P, L, I, P, P, P, P]),

@@ -310,7 +310,7 @@ lmoe_status lmoe_add_rms_norm(const void* x, int64_t ldx, const void* r, int64_t
   }
   if (!usable(y) || (mx && !scale)) return LMOE_ERR_INVALID_ARG;
   return cuda_status(launch_add_rms_norm(x, ldx, r, ldr, stream_type == LMOE_STREAM_FP32, T, d, w, eps, h, y,
-                                         mx ? scale : nullptr, stream));
+                                         mx ? scale : nullptr, 0, stream));
 }
 
 lmoe_status lmoe_add_rms_norm_backward_workspace(int T, int d, size_t* bytes) {
@@ -333,7 +333,22 @@ lmoe_status lmoe_add_rms_norm_backward(const void* dy, int64_t lddy, const void*
   if (dh) FFN_TRY_STATUS(row_args(dh, lddh, d));
   if (!usable(dx) || !usable(ws) || ws_bytes < 4 * rms_norm_bwd_partials(T, d)) return LMOE_ERR_INVALID_ARG;
   return cuda_status(launch_rms_norm_bwd(dy, lddy, h, ldh, dh, lddh, stream_type == LMOE_STREAM_FP32, T, d, w, eps,
-                                         dx, static_cast<float*>(ws), dw, stream));
+                                         dx, static_cast<float*>(ws), dw, 0, stream));
+}
+
+lmoe_status lmoe_add_rms_norm_selftest_timeout(int backward, const void* x, int T, int d, const void* w, void* y,
+                                               float* dw, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  FFN_TRY_STATUS(norm_args(T, d, w, 0.0f, false));
+  FFN_TRY_STATUS(row_args(x, d, d));
+  if (T < 1 || !usable(y)) return LMOE_ERR_INVALID_ARG;
+  if (!backward) {
+    // fewer values may take the form that waits for nothing
+    if (static_cast<long long>(T) * d < 1 << 23) return LMOE_ERR_UNSUPPORTED;
+    return cuda_status(launch_add_rms_norm(x, d, nullptr, d, false, T, d, w, 0.0f, nullptr, y, nullptr, 16, stream));
+  }
+  if (!usable(dw) || !usable(ws) || ws_bytes < 4 * rms_norm_bwd_partials(T, d)) return LMOE_ERR_INVALID_ARG;
+  return cuda_status(launch_rms_norm_bwd(x, d, x, d, nullptr, d, false, T, d, w, 0.0f, y, static_cast<float*>(ws), dw,
+                                         16, stream));
 }
 
 lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* w, cudaStream_t stream,

@@ -88,6 +88,7 @@ struct NormParams {
   long long ldx, ldr;
   int T, d, warps;      // warps per row
   int groups, stages;   // ring form: rows at a time, rows in flight for each
+  int unsent;           // bytes of a row that are waited for and never copied: 0, or 16 in the self-test of the waits
   float eps;
 };
 // Ring forms: compute warps of a CTA at most, rows in flight of a group, shared
@@ -212,15 +213,17 @@ __global__ void __launch_bounds__(32 * ring_warps(VPT) + 32)
     if (lane < p.groups) {   // lane g feeds group g
       int s = 0;
       uint32_t phase = 1;    // the first round of the ring finds its slots empty
+      bool ok = true;
       for (long long row = static_cast<long long>(blockIdx.x) * p.groups + lane; row < p.T; row += step) {
         const int b = lane * p.stages + s;
-        if (!mbar_wait(&empty[b], phase)) break;
+        if (!(ok = mbar_wait(&empty[b], phase))) break;
         uint8_t* dst = ring + static_cast<size_t>(b) * row_bytes;
-        mbar_arrive_expect_tx(&full[b], row_bytes);
+        mbar_arrive_expect_tx(&full[b], row_bytes + p.unsent);
         bulk_g2s(dst, p.x + row * p.ldx, x_bytes, &full[b]);
         if constexpr (HAS_R) bulk_g2s(dst + x_bytes, static_cast<const R*>(p.r) + row * p.ldr, r_bytes, &full[b]);
         if (++s == p.stages) s = 0, phase ^= 1;
       }
+      if (__builtin_expect(!ok, 0)) let_copies_land();
     }
     return;
   }
@@ -267,19 +270,20 @@ __global__ void __launch_bounds__(32 * ring_warps(VPT) + 32)
     __syncwarp();
     if (lane == 0 && ok) mbar_arrive(&empty[b]);
     if (++s == p.stages) s = 0, phase ^= 1;
-    ss = warp_sum(ss);
+    // a bounded wait that ran out on any lane (no handle carries an error flag) makes this row and the group's next
+    // ones NaN by their sums
+    ss = warp_sum(ok ? ss : __int_as_float(0x7FC00000));
     if (p.warps > 1) {       // the slots alternate between rows
       float* at = slots[flip] + group * p.warps;
       if (lane == 0) at[warp - group * p.warps] = ss;
       asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(32 * p.warps) : "memory");
       ss = warp_sum(lane < p.warps ? at[lane] : 0.0f);
     }
-    // a bounded wait that ran out (no handle carries an error flag) makes this row and the group's next ones NaN;
-    // their slots are not given back, so no copy is issued any more that the CTA could leave in flight
-    const float rho = ok ? rsqrtf(ss * inv_d + p.eps) : __int_as_float(0x7FC00000);
+    const float rho = rsqrtf(ss * inv_d + p.eps);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) write_vec<MX>(p, row, (t + i * stride) * 8, true, v[i], wv[i], rho);
   }
+  if (__builtin_expect(!ok, 0)) let_copies_land();
 }
 
 struct NormBwdParams {
@@ -291,6 +295,7 @@ struct NormBwdParams {
   float* part;          // [gridDim.x][d] partial sums of dw
   long long lddy, ldh, lddh;
   int T, d, warps, groups, stages;   // warps per row, rows at a time, rows in flight for each
+  int unsent;           // as in the forward pass
   float eps;
 };
 template <class R, bool HAS_DH, int VPT>
@@ -318,17 +323,19 @@ __global__ void __launch_bounds__(32 * ring_warps(VPT) + 32)
     if (lane < p.groups) {
       int s = 0;
       uint32_t phase = 1;       // the first round of the ring finds its slots empty
+      bool ok = true;
       for (long long row = static_cast<long long>(blockIdx.x) * p.groups + lane; row < p.T; row += step) {
         const int b = lane * p.stages + s;
-        if (!mbar_wait(&empty[b], phase)) break;
+        if (!(ok = mbar_wait(&empty[b], phase))) break;
         uint8_t* dst = ring + static_cast<size_t>(b) * row_bytes;
-        mbar_arrive_expect_tx(&full[b], row_bytes);
+        mbar_arrive_expect_tx(&full[b], row_bytes + p.unsent);
         bulk_g2s(dst, p.dy + row * p.lddy, dy_bytes, &full[b]);
         bulk_g2s(dst + dy_bytes, static_cast<const R*>(p.h) + row * p.ldh, h_bytes, &full[b]);
         if constexpr (HAS_DH)
           bulk_g2s(dst + dy_bytes + h_bytes, static_cast<const R*>(p.dh) + row * p.lddh, h_bytes, &full[b]);
         if (++s == p.stages) s = 0, phase ^= 1;
       }
+      if (__builtin_expect(!ok, 0)) let_copies_land();
     }
     return;
   }
@@ -345,23 +352,10 @@ __global__ void __launch_bounds__(32 * ring_warps(VPT) + 32)
   const float inv_d = 1.0f / static_cast<float>(p.d);
   int s = 0, flip = 0;
   uint32_t phase = 0;
+  bool ok = true;
   for (long long row = static_cast<long long>(blockIdx.x) * p.groups + group; row < p.T; row += step, flip ^= 1) {
     const int b = group * p.stages + s;
-    if (!mbar_wait(&full[b], phase)) {
-      // A bounded wait ran out, and no handle carries an error flag: dw becomes
-      // NaN.  This warp still meets the group's others, which may not have given
-      // up, at each row's barrier; no slot is given back, so the copies end.
-      const float k = __int_as_float(0x7FC00000);
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = k;
-      if (lane < 4) slots[lane & 1][lane >> 1][warp] = k;
-      __syncwarp();
-      if (p.warps > 1)
-        for (; row < p.T; row += step) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(32 * p.warps) : "memory");
-      break;
-    }
+    ok = ok && mbar_wait(&full[b], phase);
     const uint8_t* src = ring + static_cast<size_t>(b) * row_bytes;
     const __nv_bfloat16* dy = reinterpret_cast<const __nv_bfloat16*>(src);
     const R* h = reinterpret_cast<const R*>(src + dy_bytes);
@@ -386,8 +380,10 @@ __global__ void __launch_bounds__(32 * ring_warps(VPT) + 32)
       }
     }
     // two sums behind one barrier of the group; the slots alternate between
-    // rows, so the next row's writes cannot meet this row's reads
-    ss = warp_sum(ss);
+    // rows, so the next row's writes cannot meet this row's reads.  A bounded wait
+    // that ran out on any lane (no handle carries an error flag) makes this row,
+    // the group's next ones and so dw NaN by their sums.
+    ss = warp_sum(ok ? ss : __int_as_float(0x7FC00000));
     sc = warp_sum(sc);
     if (p.warps > 1) {
       float* s0 = slots[flip][0] + group * p.warps;
@@ -423,9 +419,10 @@ __global__ void __launch_bounds__(32 * ring_warps(VPT) + 32)
       ov.store(static_cast<R*>(p.dx) + row * p.d + c);
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[b]);
+    if (lane == 0 && ok) mbar_arrive(&empty[b]);
     if (++s == p.stages) s = 0, phase ^= 1;
   }
+  if (__builtin_expect(!ok, 0)) let_copies_land();      // before the sums take the ring's place, or the CTA leaves
   // One row of partial sums per CTA: its groups' sums meet in the ring, once
   // all of them are done with it, and are added in order.
   float* const out = p.part + static_cast<size_t>(blockIdx.x) * p.d;
@@ -598,8 +595,9 @@ size_t rms_norm_bwd_partials(int T, int d) {
 }
 
 cudaError_t launch_add_rms_norm(const void* x, long long ldx, const void* r, long long ldr, bool r_fp32, int T, int d,
-                                const void* w, float eps, void* h, void* y, uint8_t* scale, cudaStream_t s) {
+                                const void* w, float eps, void* h, void* y, uint8_t* scale, int unsent, cudaStream_t s) {
   NormParams p = {};
+  p.unsent = unsent;
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.r = r;
   p.w = static_cast<const __nv_bfloat16*>(w);
@@ -618,8 +616,9 @@ cudaError_t launch_add_rms_norm(const void* x, long long ldx, const void* r, lon
 
 cudaError_t launch_rms_norm_bwd(const void* dy, long long lddy, const void* h, long long ldh, const void* dh,
                                 long long lddh, bool h_fp32, int T, int d, const void* w, float eps, void* dx,
-                                float* part, float* dw, cudaStream_t s) {
+                                float* part, float* dw, int unsent, cudaStream_t s) {
   NormBwdParams p = {};
+  p.unsent = unsent;
   p.dy = static_cast<const __nv_bfloat16*>(dy);
   p.h = h;
   p.dh = dh;

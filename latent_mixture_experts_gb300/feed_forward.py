@@ -160,6 +160,23 @@ def lmoe_add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, norm_w: torch.
     return dx, dw
 
 
+def lmoe_add_rms_norm_selftest_timeout(x: torch.Tensor, norm_w: torch.Tensor, backward: bool = False):
+    """A norm whose rows never are complete, so that its waits run out: (y,
+    None), or with backward=True (dx, dw), all NaN."""
+    T, d = x.shape
+    _packed("x", x, _BF16, x.shape)
+    _on_device(_device_of(x), norm_w)
+    _norm_weight(norm_w, x.shape[1:])
+    y = torch.empty_like(x)
+    n = _norm_backward_workspace(T, d)
+    dw = torch.empty(d, dtype=_F32, device=x.device) if backward else None
+    ws = torch.empty(n, dtype=_U8, device=x.device)
+    B._check("lmoe_add_rms_norm_selftest_timeout", B.load_library().lmoe_add_rms_norm_selftest_timeout(
+        int(backward), x.data_ptr(), T, d, norm_w.data_ptr(), y.data_ptr(), dw.data_ptr() if backward else None,
+        ws.data_ptr(), n, B._stream(None)))
+    return y, dw
+
+
 class GatedFFN:
     """One dense gated feed-forward block on the current CUDA device:
     y = (a(x gate^T) * v(x up^T)) down^T with SiTU-GLU or SwiGLU.

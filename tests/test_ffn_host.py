@@ -154,3 +154,14 @@ def test_reference_norm_gradient_against_differences():
               R.norm(h, None, base + s * eps * v, 1e-3)[0]).mul(dy).sum() for s in (1, -1)]
         num = float(f[0] - f[1]) / (2 * eps)
         assert abs(num - float((grad * v).sum())) <= 1e-7 * (1 + abs(num))
+
+
+def test_norm_self_test_refusals(lib, b):
+    def call(backward=0, x=A, T=2048, d=4096, w=A, y=A, dw=A, ws=A, n=1 << 30):
+        return lib.lmoe_add_rms_norm_selftest_timeout(backward, x, T, d, w, y, dw, ws, n, None)
+    inv, uns = b.LMOE_ERR_INVALID_ARG, b.LMOE_ERR_UNSUPPORTED
+    for kw in (dict(x=None), dict(w=None), dict(y=None), dict(T=0), dict(T=-1), dict(x=A + 2), dict(backward=1, dw=None),
+               dict(backward=1, ws=None), dict(backward=1, n=16)):
+        assert call(**kw) == inv, kw
+    for kw in (dict(d=4100), dict(d=16392), dict(T=2047)):
+        assert call(**kw) == uns, kw

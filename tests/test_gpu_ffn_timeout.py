@@ -54,3 +54,22 @@ def test_wait_that_runs_out(ops, make, T, d, F, joined):
     assert torch.equal(call(*x), want)
     layer.lmoe_ffn_sync_status()
     layer.close()
+
+
+# rows of one warp and of many, several groups of warps, one and five vectors per thread
+@pytest.mark.parametrize("T,d", [(40000, 256), (4000, 7168), (2000, 8192), (600, 16384)])
+def test_norm_rows_that_never_are_complete(ops, T, d):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, d, device="cuda", generator=g).bfloat16()
+    w = (1 + 0.1 * torch.randn(d, device="cuda", generator=g)).bfloat16()
+    want = ops.lmoe_add_rms_norm(x, w, 1e-6)[0]
+    dwant = ops.lmoe_add_rms_norm_backward(x, x, w, 1e-6)
+    y, _ = ops.lmoe_add_rms_norm_selftest_timeout(x, w)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(y).all())
+    dx, dw = ops.lmoe_add_rms_norm_selftest_timeout(x, w, backward=True)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(dx).all()) and bool(torch.isnan(dw).all())
+    assert torch.equal(ops.lmoe_add_rms_norm(x, w, 1e-6)[0], want)
+    got = ops.lmoe_add_rms_norm_backward(x, x, w, 1e-6)
+    assert torch.equal(got[0], dwant[0]) and torch.equal(got[1], dwant[1])
