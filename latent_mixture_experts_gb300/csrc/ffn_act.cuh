@@ -63,8 +63,12 @@ __device__ __forceinline__ float vrcp(float a) {
 __device__ __forceinline__ F2 vrcp(F2 a) { return {vrcp(a.x), vrcp(a.y)}; }
 __device__ __forceinline__ float vmin(float a, float b) { return fminf(a, b); }
 __device__ __forceinline__ F2 vmin(F2 a, F2 b) { return {fminf(a.x, b.x), fminf(a.y, b.y)}; }
-// far for |x| >= 1/4, else (and for a NaN) near
-__device__ __forceinline__ float by_size(float x, float near, float far) { return fabsf(x) >= 0.25f ? far : near; }
+__device__ __forceinline__ float minus_abs(float a) { return -fabsf(a); }
+__device__ __forceinline__ F2 minus_abs(F2 a) { return {-fabsf(a.x), -fabsf(a.y)}; }
+// far with the sign of x for |x| >= 1/4, else (and for a NaN) near
+__device__ __forceinline__ float by_size(float x, float near, float far) {
+  return fabsf(x) >= 0.25f ? copysignf(far, x) : near;
+}
 __device__ __forceinline__ F2 by_size(F2 x, F2 near, F2 far) {
   return {by_size(x.x, near.x, far.x), by_size(x.y, near.y, far.y)};
 }
@@ -74,10 +78,18 @@ template <class V>
 __device__ __forceinline__ V sigmoid(V x) {
   return vrcp(vadd(vex2(vmul(x, splat<V>(-kLog2E))), splat<V>(1.0f)));
 }
-// tanh of two values to ~1e-6 relative: 1 - 2/(e^2x + 1), both quotients from
-// one reciprocal (e^2x stops at 2^60, where tanh is 1 long since), and the odd
-// Taylor polynomial through x^9 near zero, where that difference cancels (at
-// |x| = 0.25 the next term is 4e-9 of tanh; the quotient form there is off ~5e-7).
+// sigma(x), and 1 - sigma(x) as e^-x sigma(x): from the rounded sigma alone its
+// tail would be lost (e^-x stops at 2^126, where sigma is zero).
+template <class V>
+__device__ __forceinline__ V sigmoid(V x, V& rest) {
+  const V e = vex2(vmul(x, splat<V>(-kLog2E))), s = vrcp(vadd(e, splat<V>(1.0f)));
+  rest = vmul(vmin(e, splat<V>(0x1p126f)), s);
+  return s;
+}
+// tanh of two values to ~1e-6 relative: with e = e^-2|x|, 2/(1 + e) - 1, both
+// quotients from one reciprocal, and the odd Taylor polynomial through x^9 near
+// zero, where that difference cancels (at |x| = 0.25 the next term is 4e-9 of
+// tanh; the quotient form there is off ~9e-7).
 template <class V>
 __device__ __forceinline__ V tanh_near(V x) {
   const V x2 = vmul(x, x);
@@ -87,13 +99,24 @@ __device__ __forceinline__ V tanh_near(V x) {
   return vfma(vmul(x, x2), p, x);
 }
 template <class V>
-__device__ __forceinline__ void tanh_both(V x, V y, V& tx, V& ty) {
-  const V k = splat<V>(2.0f * kLog2E), top = splat<V>(0x1p60f), one = splat<V>(1.0f), m2 = splat<V>(-2.0f);
-  const V a = vadd(vmin(vex2(vmul(x, k)), top), one), b = vadd(vmin(vex2(vmul(y, k)), top), one);
-  const V r = vmul(vrcp(vmul(a, b)), m2);
-  tx = by_size(x, tanh_near(x), vfma(b, r, one));
-  ty = by_size(y, tanh_near(y), vfma(a, r, one));
+struct Tanh {
+  V t, e, h;      // tanh x, e^-2|x|, 2/(1 + e)
+};
+template <class V>
+__device__ __forceinline__ void tanh_both(V x, V y, Tanh<V>& tx, Tanh<V>& ty) {
+  const V k = splat<V>(2.0f * kLog2E), one = splat<V>(1.0f), two = splat<V>(2.0f), minus = splat<V>(-1.0f);
+  tx.e = vex2(minus_abs(vmul(x, k)));
+  ty.e = vex2(minus_abs(vmul(y, k)));
+  const V a = vadd(tx.e, one), b = vadd(ty.e, one), r = vmul(vrcp(vmul(a, b)), two);
+  tx.h = vmul(b, r);
+  ty.h = vmul(a, r);
+  tx.t = by_size(x, tanh_near(x), vadd(tx.h, minus));
+  ty.t = by_size(y, tanh_near(y), vadd(ty.h, minus));
 }
+// 1 - tanh^2 = 4 e / (1 + e)^2.  From the rounded tanh it would be 1% off at
+// |x| = 6 and nothing but rounding from 8 on.
+template <class V>
+__device__ __forceinline__ V tanh_slope(const Tanh<V>& t) { return vmul(vmul(t.e, t.h), t.h); }
 
 struct GluCaps {
   float b1, b2, r1, r2;   // caps and their reciprocals
@@ -103,9 +126,9 @@ template <int ACT, class V>
 __device__ __forceinline__ V glu_hidden(V g, V u, const GluCaps& c) {
   const V s = sigmoid(g);
   if constexpr (ACT == 1) return vmul(vmul(g, s), u);
-  V tg, tu;
+  Tanh<V> tg, tu;
   tanh_both(vmul(g, splat<V>(c.r1)), vmul(u, splat<V>(c.r2)), tg, tu);
-  return vmul(vmul(splat<V>(c.b1), vmul(tg, s)), vmul(splat<V>(c.b2), tu));
+  return vmul(vmul(splat<V>(c.b1), vmul(tg.t, s)), vmul(splat<V>(c.b2), tu.t));
 }
 
 struct GluGrad {
@@ -113,19 +136,19 @@ struct GluGrad {
 };
 template <int ACT>
 __device__ __forceinline__ GluGrad glu_grad(F2 g, F2 u, F2 dhid, const GluCaps& c) {
-  const F2 s = sigmoid(g), one = splat<F2>(1.0f), minus = splat<F2>(-1.0f);
-  const F2 rest = vfma(s, minus, one);               // 1 - s
   GluGrad o;
   if constexpr (ACT == 1) {
-    const F2 a = vmul(g, s);
+    const F2 s = sigmoid(g), rest = vfma(s, splat<F2>(-1.0f), splat<F2>(1.0f)), a = vmul(g, s);
     o.hid = vmul(a, u);
     o.dg = vmul(vmul(dhid, u), vfma(a, rest, s));
     o.du = vmul(dhid, a);
   } else {
-    F2 tg, tu;
+    F2 rest;
+    const F2 s = sigmoid(g, rest);
+    Tanh<F2> tg, tu;
     tanh_both(vmul(g, splat<F2>(c.r1)), vmul(u, splat<F2>(c.r2)), tg, tu);
-    const F2 a = vmul(splat<F2>(c.b1), vmul(tg, s)), v = vmul(splat<F2>(c.b2), tu);
-    const F2 dtg = vfma(vmul(tg, minus), tg, one), dtu = vfma(vmul(tu, minus), tu, one);   // 1 - t^2
+    const F2 a = vmul(splat<F2>(c.b1), vmul(tg.t, s)), v = vmul(splat<F2>(c.b2), tu.t);
+    const F2 dtg = tanh_slope(tg), dtu = tanh_slope(tu);
     o.hid = vmul(a, v);
     o.dg = vmul(vmul(dhid, v), vfma(a, rest, vmul(dtg, s)));
     o.du = vmul(vmul(dhid, a), dtu);
