@@ -49,14 +49,20 @@ class FeedForwardSublayer:
         n, _, h = lmoe_add_rms_norm(x, self.norm_w, self.eps, residual=residual)
         return self.block.forward(n), h
 
+    def _trains(self):
+        if not (isinstance(self.block, GatedFFN) and self.block.training):
+            raise ValueError("only a sublayer whose block is a GatedFFN made with training=True trains")
+
     def forward_train(self, x: torch.Tensor, residual: torch.Tensor):
         """forward of a GatedFFN made with training=True, keeping what backward reads."""
+        self._trains()
         n, _, h = lmoe_add_rms_norm(x, self.norm_w, self.eps, residual=residual)
         y, g, u = self.block.lmoe_ffn_forward(n, save=True)
         return y, h, Saved(h, n, g, u)
 
     def backward(self, dy: torch.Tensor, dh: torch.Tensor | None, saved: Saved) -> Gradients:
         """Gradients from dy (of y, bf16) and dh (of h, its dtype; None: zero)."""
+        self._trains()
         dn, dg, du, dd = self.block.lmoe_ffn_backward(saved.n, saved.g, saved.u, dy)
         dx, dw = lmoe_add_rms_norm_backward(dn, saved.h, self.norm_w, self.eps, dh=dh)
         return Gradients(dx, dw, dg, du, dd)
