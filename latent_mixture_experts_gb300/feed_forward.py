@@ -36,6 +36,13 @@ def _rows(name: str, t: torch.Tensor, dtypes, shape) -> int:
     raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
+def _counts(what: str, *n: int):
+    """Row counts and widths cross the C ABI as ints of 32 bits, which ctypes would cut without a word."""
+    for v in n:
+        if v > 0x7FFFFFFF:
+            raise ValueError(f"{what} {v} does not fit 32 bits")
+
+
 def _packed(name: str, t: torch.Tensor, dtype, shape):
     if _rows(name, t, (dtype,), shape) != shape[1]:
         raise ValueError(f"{name} must be contiguous")
@@ -84,6 +91,7 @@ def lmoe_add_rms_norm(x: torch.Tensor, norm_w: torch.Tensor, eps: float, residua
     if len(shape) != 2:
         raise ValueError("x must be [T][d]")
     T, d = shape
+    _counts("a size of x,", T, d)
     ldx = _rows("x", x, (_BF16,), shape)
     dev = _device_of(x)
     _norm_weight(norm_w, shape[1:])
@@ -138,6 +146,7 @@ def lmoe_add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, norm_w: torch.
     if len(shape) != 2:
         raise ValueError("h must be [T][d]")
     T, d = shape
+    _counts("a size of h,", T, d)
     ldh = _rows("h", h, (_BF16, _F32), shape)
     lddy = _rows("dy", dy, (_BF16,), shape)
     dev = _device_of(h)
@@ -199,6 +208,7 @@ class GatedFFN:
         if gate.dim() != 2 or gate.dtype not in (torch.bfloat16, torch.uint8):
             raise ValueError("gate must be [d_ff][d_model], bfloat16 or uint8")
         F, d = gate.shape
+        _counts("a size of gate or max_tokens,", F, d, int(max_tokens))
         self.mx = gate.dtype == torch.uint8
         shapes = {"gate": (F, d), "up": (F, d), "down": (d, F)}
         if self.mx:
@@ -248,6 +258,7 @@ class GatedFFN:
                 return self.lmoe_ffn_forward(x, save, out)
         self._current()
         T = x.shape[0]
+        _counts("the number of tokens,", T)
         ldx = self._tokens(x, "x", T)
         y = torch.empty_like(x, memory_format=_PACKED) if out is None else self._out(T, out)
         if not save:
@@ -272,6 +283,7 @@ class GatedFFN:
                 return self.lmoe_ffn_backward(x, g, u, dy, need_dx, need_dw)
         self._current()
         T, shape = x.shape[0], (x.shape[0], self.d_ff)
+        _counts("the number of tokens,", T)
         ldx = self._tokens(x, "x", T)
         lddy = self._tokens(dy, "dy", T)
         _packed("g", g, _BF16, shape)
@@ -300,6 +312,7 @@ class GatedFFN:
                 return self.lmoe_ffn_forward_mx(x_codes, x_scales, out)
         self._current()
         T = x_codes.shape[0]
+        _counts("the number of tokens,", T)
         _packed("x_codes", x_codes, _U8, (T, self.d_model))
         _packed("x_scales", x_scales, _U8, (T, self.d_model // 32))
         _on_device(self._dev, x_codes, x_scales)

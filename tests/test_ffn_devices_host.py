@@ -137,3 +137,38 @@ def test_self_test_arguments(lib, b, mx):
     assert lib.lmoe_ffn_selftest_timeout(h, A, A, 4, A, None) == b.LMOE_ERR_INVALID_ARG
     lib.fake_set_device(0)
     assert lib.lmoe_ffn_destroy(h) == b.LMOE_OK
+
+
+def test_binding_refuses_sizes_beyond_32_bits(monkeypatch):
+    """They would reach the library cut to 32 bits: 2^32 + 4 rows as four."""
+    built_library()
+    from latent_mixture_experts_gb300 import GatedFFN, feed_forward, lmoe_add_rms_norm, lmoe_add_rms_norm_backward
+
+    class Lib:                       # reached by none of the calls
+        def __getattr__(self, name):
+            raise AssertionError(name)
+    monkeypatch.setattr(feed_forward.B, "load_library", lambda: Lib())
+    monkeypatch.setattr(feed_forward, "_raw_device", lambda: 0)
+    monkeypatch.setattr(feed_forward, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(feed_forward, "_norm_backward_workspace", lambda T, d: 32)
+    block = GatedFFN.__new__(GatedFFN)
+    block._lib, block._h, block._dev, block._device = Lib(), None, 0, torch.device("cuda:0")
+    block.d_model, block.d_ff, block.max_tokens = 64, 64, 8
+    n = 2 ** 32 + 4
+    with FakeTensorMode():           # no memory behind them
+        def empty(*shape, dtype=torch.bfloat16):
+            return torch.empty(*shape, device="cuda:0", dtype=dtype)
+        x8, w8, x1, w1 = empty(n, 8), empty(8), empty(1, n - 4 + 8), empty(n - 4 + 8)
+        x, q, s = empty(n, 64), empty(n, 64, dtype=torch.uint8), empty(n, 2, dtype=torch.uint8)
+        W = {"gate": empty(n + 4, 8), "up": empty(n + 4, 8), "down": empty(8, n + 4)}
+        W8 = {k: empty(8, 8) for k in W}
+        for call in (lambda: lmoe_add_rms_norm(x8, w8, 1e-6), lambda: lmoe_add_rms_norm(x8, w8, 1e-6, residual=x8),
+                     lambda: lmoe_add_rms_norm(x1, w1, 1e-6), lambda: lmoe_add_rms_norm_backward(x8, x8, w8, 1e-6),
+                     lambda: lmoe_add_rms_norm_backward(x1, x1, w1, 1e-6), lambda: block.lmoe_ffn_forward(x),
+                     lambda: block.lmoe_ffn_backward(x, x, x, x), lambda: block.lmoe_ffn_forward_mx(q, s)):
+            with pytest.raises(ValueError, match="32 bits"):
+                call()
+        monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+        for weights, tokens in ((W, 8), (W8, n)):
+            with pytest.raises(ValueError, match="32 bits"):
+                GatedFFN(weights, max_tokens=tokens)
