@@ -130,9 +130,10 @@ LMOE_API lmoe_status lmoe_ffn_forward(lmoe_ffn_handle h, const void* x_bf16, int
 /* Gradients from x, the saved g and u (bf16 [T][d_ff]) and dy bf16
  * [T][d_model] (stride lddy): dx [T][d_model], dw_gate and dw_up
  * [d_ff][d_model], dw_down [d_model][d_ff], bf16, overwritten; any of the
- * four may be NULL and is then not computed.  dhid, dg, du and hid are
- * rounded to bf16 between the products.  The same inputs and the same gradients
- * asked for give the same bits.
+ * four may be NULL and is then not computed.  dg, du and hid are rounded to
+ * bf16 between the products; dhid is fp32.  The gradients may not overlap an
+ * input, a weight or one another.  The same inputs and the same gradients asked
+ * for give the same bits.
  * T = 0 writes zero weight gradients. */
 LMOE_API lmoe_status lmoe_ffn_backward(lmoe_ffn_handle h, const void* x_bf16, int64_t ldx, const void* gate,
                                        const void* up, const void* dy_bf16, int64_t lddy, int T, void* dx_opt,

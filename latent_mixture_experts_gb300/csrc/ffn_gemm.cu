@@ -42,8 +42,9 @@ struct PairCfg {
 };
 constexpr int kPairThreads = 64 + 32 * kEpiPairWarps;
 constexpr int kTmemBarrier = 1;              // tmem_base is there for the epilogue warps
-// Tile rows of one raster group (4096 tokens at 7168 x 6144, backward: 1155 us;
-// with 4 rows 1175 us, with 16 rows 1176 us).
+// Tile rows of one raster group (4096 tokens at 7168 x 6144, backward, in short
+// runs, before the power limit sets in: 1155 us; with 4 rows 1175 us, with 16 rows
+// 1176 us.  In long ones 1325 us).
 constexpr int kTileRows = 8;
 
 // narrow: half a wide tile, at the end of the wide grid; n counts half tiles.
@@ -402,12 +403,12 @@ int ffn_pair_tiles(FfnPairParams& p, FfnMode mode, int ctas) {
   p.wide = p.N[0] % 16 == 0;
   for (int i = 0; i < 3; ++i) p.wide = p.wide && reinterpret_cast<uintptr_t>(p.out[i]) % 32 == 0;
   // With all SMs busy a narrow tile takes 0.55 to 0.58 of a wide one's time
-  // (4096 tokens at 7168 x 6144: forward 601 us against 546 us), of the gradients'
-  // 0.67 (backward 1500 us against 1155 us); 1003 tokens at 1152 x 864, which leave
-  // half of the wide grid idle: forward 16.8 us against 22.8 us.  A last round of
-  // wide tiles that fills at most half of the pairs is cut into halves.  Tiles
-  // cost their K blocks, and eight of them at least: 256 tokens at 5120 x 3584,
-  // backward, 64.4 us; with 14 at least 72.0 us.
+  // (4096 tokens at 7168 x 6144, short runs: forward 601 us against 546 us), of the
+  // gradients' 0.67 (backward 1500 us against 1155 us); 1003 tokens at 1152 x 864,
+  // which leave half of the wide grid idle: forward 16.8 us against 22.8 us.  A last
+  // round of wide tiles that fills at most half of the pairs is cut into halves.
+  // Tiles cost their K blocks, and eight of them at least: 256 tokens at 5120 x
+  // 3584, backward, 64.4 us; with 14 at least 72.0 us.
   const float ratio = mode == kFfnGrads ? 0.67f : 0.57f;
   const auto cost = [](int nkb) { return static_cast<float>(nkb < 6 ? 8 : nkb + 2); };
   const int pairs = ctas / 2;

@@ -21,6 +21,10 @@ cudaError_t launch_rms_norm_bwd(const void* dy, long long lddy, const void* h, l
                                 long long lddh, bool h_fp32, int T, int d, const void* w, float eps, void* dx,
                                 float* part, float* dw, int unsent, cudaStream_t s);
 
+// What the bf16 products of a block hand on is rounded to bf16, because a bf16 MMA
+// takes bf16 operands: hid in the forward pass, dg, du and hid in the backward
+// pass (the saved g and u as well).  One rounding each, of an fp32 value.
+//
 // ------------------------------------------------------ pair-tile bf16 GEMM
 // C[M][N] (bf16) = A B^T on tiles of CTA pairs, 256 rows x 256 or 128 columns.
 enum FfnMode {

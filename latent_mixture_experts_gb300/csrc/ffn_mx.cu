@@ -12,8 +12,9 @@
 // Scales live in memory in the image that the block-scaled MMA wants
 // ("atoms": 512 bytes for 128 rows x 4 blocks) and come with the operands;
 // the MMA thread copies them on to tensor memory (tcgen05.cp) ahead of each
-// stage's products (1957 TFLOP/s against 1123 with warps that moved them by
-// tcgen05.st, at 4096 tokens of 7168 x 6144).
+// stage's products (4096 tokens of 7168 x 6144, when one lane still issued the
+// loads and products: 553 us, against 964 us with a set of warps that moved them
+// by tcgen05.st and 564 us with three sets).
 // The weights' atoms are laid out once, when the handle is made; the hidden
 // activation's are written by the gate/up epilogue; x's by a small kernel in
 // front.
@@ -40,7 +41,9 @@ struct MxCfg {
 };
 constexpr int kThreads = 320;                        // TMA, MMA, 8 epilogue warps: two for each lane quarter
 constexpr int kTmemBarrier = 1;                      // tmem_base is there for the epilogue warps
-constexpr int kTileRows = 16;     // 4096 tokens at 7168 x 6144: 307 us; 8 rows 312 us, 4 rows 319 us
+// Short runs of 4096 tokens at 7168 x 6144, before the power limit sets in (358 us in
+// long ones): 307 us; 8 rows 312 us, 4 rows 319 us.
+constexpr int kTileRows = 16;
 
 __device__ __forceinline__ void tile_of(const FfnMxParams& p, int i, int& m, int& n) {
   const int tm = p.tiles / p.tiles_n;
@@ -338,7 +341,7 @@ int ffn_mx_tiles(FfnMxParams& p, bool gate_up, int ctas) {
     return (p.tiles + ctas / 2 - 1) / (ctas / 2);
   };
   // With all SMs busy a 128-row tile takes 0.76 of a 192-row one's time (4096
-  // tokens at 7168 x 6144: 360 us against 307 us); where both leave pairs idle
+  // tokens at 7168 x 6144, short runs: 360 us against 307 us); where both leave pairs idle
   // the narrow ones win (300 tokens at 1152 x 864: 13.4 us against 15.8 us).
   const int narrow = rounds(128), wide = rounds(192);      // leaves the wide tiling in p
   if (wide <= 0.76f * narrow) return 192;

@@ -28,10 +28,13 @@ constexpr int kTmem = 256, kSfCols = 8;
 constexpr int kSfb = 512;
 constexpr int kMxSkinnySmem = 110 * 1024;   // two CTAs on an SM
 constexpr int kPitch = kN + 4;           // floats of a token's partial sums: 16-byte rows, four banks apart
-// Up to here rather than the pair tiles: 48 tokens at widths 7168 and 6144 take
-// 37.6 us here and 37.0 us there, at 7168 and 2048 18.5 us and 23.7 us; 64 tokens
-// 41.9 us and 37.2 us, 21.2 us and 22.4 us.  16 tokens at 7168 and 6144: 29.3 us,
-// 4.7 TB/s of weights.
+// Up to here rather than the pair tiles: 40, 48 and 56 tokens at widths 7168 and
+// 6144 take 34.2, 35.9 and 37.4 us here and 35.4, 35.6 and 35.9 us there, at 7168 and
+// 2048 19.0, 20.0 and 21.1 us and 23.3, 23.2 and 23.1 us, at 512 and 3584 10.3, 11.4 and
+// 12.2 us and 13.3, 13.4 and 13.5 us.  One limit for all widths, too high a one where
+// both are 2048 or less: 48 tokens at 2048 and 2048 14.4 us here and 13.7 us there, at
+// 768 and 768 10.5 us and 9.9 us, at 256 and 256 11.7 us and 8.6 us.  16 tokens at 7168
+// and 6144: 29.8 us, 4.6 TB/s of weights.
 constexpr int kMxSkinnyMaxTokens = 48;
 static_assert(kN + kMaxStages * kSfCols <= kTmem, "tensor memory");
 

@@ -11,8 +11,8 @@
 // features arrive side by side, through one tensor map whose third dimension
 // steps from one matrix to the other.  A ring of about 100 KB per CTA puts two
 // CTAs on an SM, and lets the down pass's CTAs load their first weights while
-// the gate/up pass's last ones finish.  One token at 7168 and 6144: 46 us,
-// 5.7 TB/s of weights.
+// the gate/up pass's last ones finish.  One token at 7168 and 6144: 47 to
+// 48 us, 5.5 TB/s of weights.
 #include "ffn_act.cuh"
 #include "ffn_internal.h"
 #include "lmoe_internal.h"

@@ -72,7 +72,8 @@ def test_norm_on_each_of_two_devices(lib, b, T, d):
 def test_a_failed_call_is_not_kept(lib, b):
     """A limit that could not be raised once is asked for again by the next call; then not any more."""
     def norm():
-        return lib.lmoe_add_rms_norm_backward(A, 1152, A, 1152, None, 1152, 0, 2000, 1152, A, 1e-6, A, A, A, 1 << 30, None)
+        return lib.lmoe_add_rms_norm_backward(A, 1152, A, 1152, None, 1152, 0, 2000, 1152, A, 1e-6, A, A, A, 1 << 30,
+                                              None)
     lib.fake_fail_attributes(1)
     assert norm() == b.LMOE_ERR_OOM
     assert norm() == b.LMOE_OK
@@ -130,8 +131,8 @@ def test_self_test_arguments(lib, b, mx):
     h = _block(lib, b, mx)
     for T in (1, 16, 40, 300, 4096):
         assert lib.lmoe_ffn_selftest_timeout(h, A, A, T, A, None) == b.LMOE_OK
-    for x, s, T, out in ((None, A, 4, A), (A, A, 0, A), (A, A, -1, A), (A, A, 4097, A), (A, A, 4, None), (A + 8, A, 4, A),
-                         (A, None if mx else A, 4, A if mx else A + 2)):
+    for x, s, T, out in ((None, A, 4, A), (A, A, 0, A), (A, A, -1, A), (A, A, 4097, A), (A, A, 4, None),
+                         (A + 8, A, 4, A), (A, None if mx else A, 4, A if mx else A + 2)):
         assert lib.lmoe_ffn_selftest_timeout(h, x, s, T, out, None) == b.LMOE_ERR_INVALID_ARG
     lib.fake_set_device(1)
     assert lib.lmoe_ffn_selftest_timeout(h, A, A, 4, A, None) == b.LMOE_ERR_INVALID_ARG

@@ -44,9 +44,9 @@ def test_norm_backward_in_place(ops, T, d, rt):
     dy, h, w, e = norm._bwd_inputs(T, d, 5, rt, True)
     want, dwant = ops.lmoe_add_rms_norm_backward(dy, h, w, EPS, dh=e)
     dw, ws = torch.empty(d, device="cuda"), torch.empty(4 * 152 * d, device="cuda", dtype=torch.uint8)
-    assert lib.lmoe_add_rms_norm_backward(dy.data_ptr(), d, h.data_ptr(), d, e.data_ptr(), d, int(rt == torch.float32), T,
-                                          d, w.data_ptr(), EPS, e.data_ptr(), dw.data_ptr(), ws.data_ptr(), ws.numel(),
-                                          _stream()) == ops.LMOE_OK
+    assert lib.lmoe_add_rms_norm_backward(dy.data_ptr(), d, h.data_ptr(), d, e.data_ptr(), d, int(rt == torch.float32),
+                                          T, d, w.data_ptr(), EPS, e.data_ptr(), dw.data_ptr(), ws.data_ptr(),
+                                          ws.numel(), _stream()) == ops.LMOE_OK
     assert torch.equal(e, want) and torch.equal(dw, dwant)
 
 
