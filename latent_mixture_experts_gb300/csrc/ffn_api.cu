@@ -90,33 +90,15 @@ bool skinny_maps(FfnSkinnyParams& p, const void* a, long long lda, const void* w
   constexpr CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const uint64_t k = K, row = 2 * k, rows = p.rows, M = p.M, T = p.T;
   p.whole = K % 64 == 0;
-  const uint8_t* base = static_cast<const uint8_t*>(w0);
-  uint64_t step = 0;
-  p.swapped = p.apart = 0;
-  if (w1) {
-    const uint64_t u = reinterpret_cast<uint64_t>(w0), v = reinterpret_cast<uint64_t>(w1);
-    p.apart = u == v || (u < v ? v - u : u - v) >= (1ull << 40);
-  }
-  if (p.apart) {
-    if (!make_tmap_2d(&p.b, dt, w0, k, M, row, 64, rows, sw) ||
-        !make_tmap_2d(&p.b_up, dt, w1, k, M, row, 64, rows, sw))
+  if (w1) {      // two boxes of half a tile's rows each, side by side
+    if (!make_tmap_2d(&p.b, dt, w0, k, M, row, 64, rows, sw) || !make_tmap_2d(&p.b_up, dt, w1, k, M, row, 64, rows, sw))
       return false;
-  } else if (w1) {
-    const uint8_t* other = static_cast<const uint8_t*>(w1);
-    p.swapped = other < base;
-    step = p.swapped ? base - other : other - base;
-    if (p.swapped) base = other;
+  } else if (!(p.whole ? make_tmap_3d(&p.b, dt, w0, 64, M, k / 64, row, 128, 64, rows, p.kc, sw)
+                       : make_tmap_2d(&p.b, dt, w0, k, M, row, 64, rows, sw))) {
+    return false;
   }
-  if (p.whole) {
-    const bool b = p.apart ? true
-                   : w1    ? make_tmap_4d(&p.b, dt, base, 64, M, 2, k / 64, row, step, 128, 64, rows, 2, p.kc, sw)
-                           : make_tmap_3d(&p.b, dt, base, 64, M, k / 64, row, 128, 64, rows, p.kc, sw);
-    return b && make_tmap_3d(&p.a, dt, a, 64, T, k / 64, 2 * lda, 128, 64, tb, p.kc, sw);
-  }
-  const bool b = p.apart ? true
-                 : w1    ? make_tmap_3d(&p.b, dt, base, k, M, 2, row, step, 64, rows, 2, sw)
-                         : make_tmap_2d(&p.b, dt, base, k, M, row, 64, rows, sw);
-  return b && make_tmap_2d(&p.a, dt, a, k, T, 2 * lda, 64, tb, sw);
+  return p.whole ? make_tmap_3d(&p.a, dt, a, 64, T, k / 64, 2 * lda, 128, 64, tb, p.kc, sw)
+                 : make_tmap_2d(&p.a, dt, a, k, T, 2 * lda, 64, tb, sw);
 }
 
 lmoe_status norm_args(int T, int d, const void* w, float eps, bool mx) {

@@ -81,9 +81,8 @@ constexpr int kSkinnyMaxSplits = 8;    // K splits: the portable cluster size
 // Two CTAs on an SM (one token at 7168 x 6144: 46.5 us; with 74 KB and three CTAs 48.6 us).
 constexpr int kSkinnySmem = 110 * 1024;
 struct FfnSkinnyParams {
-  // whole (K a multiple of 64): a (64, T, K/64), b (64, features, K/64) or, gate/up, (64, features, 2, K/64),
-  // boxes of tb / rows and kc chunks; else a (K, T), b (K, features[, 2]), one box per 64-wide chunk
-  // apart: gate and up too far apart for one map (2^40 bytes): b, b_up (K, features), one box per chunk each
+  // whole (K a multiple of 64): a (64, T, K/64) and, down pass, b (64, features, K/64), boxes of tb / rows and kc
+  // chunks; else, and gate (b) and up (b_up) always, (K, T) and (K, features), one box per 64-wide chunk
   CUtensorMap a, b, b_up;
   void *out, *save_g, *save_u;
   int T, M;            // tokens; features of the output
@@ -93,8 +92,7 @@ struct FfnSkinnyParams {
   int stages;
   int splits;          // CTAs of a cluster, over K
   int recv;            // where in shared memory the partial sums meet, behind the ring
-  int whole, apart;
-  int swapped;         // swapped: the up matrix lies below the gate matrix in memory
+  int whole;
   float b1, b2;
   int* err;
 };

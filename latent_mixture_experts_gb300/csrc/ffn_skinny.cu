@@ -8,8 +8,12 @@
 // in rank order, by all of its CTAs: one token at widths 7168 and 2048 takes
 // 20 us, against 32 us with narrow tiles over the whole of K (an MMA reads its
 // 128 token rows whatever its width).  The gate and up rows of the same
-// features arrive side by side, through one tensor map whose third dimension
-// steps from one matrix to the other.  A ring of about 100 KB per CTA puts two
+// features lie side by side in a stage, each by a copy of its own.  (One tensor
+// map over both matrices, with a dimension that steps from one to the other,
+// would save half of the copies, but its copies also bring in memory behind the
+// first matrix, 80 KB for one of 2 KB, that need not be there: an illegal access.
+// Copies by maps of one matrix stayed within its 4 KB blocks, 188 maps measured.)
+// A ring of about 100 KB per CTA puts two
 // CTAs on an SM, and lets the down pass's CTAs load their first weights while
 // the gate/up pass's last ones finish.  One token at 7168 and 6144: 47 to
 // 48 us, 5.5 TB/s of weights.
@@ -80,22 +84,12 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
     auto load_b = [&](int i, int s) {
       i += first;
       uint8_t* dst = sb + s * b_slot;
-      if (GU && p.apart) {
-        for (int c = 0; c < p.kc; ++c) {
-          w_load_2d(dst + c * b_chunk, &p.b, &full[s], (i * p.kc + c) * 64, f0);
-          w_load_2d(dst + c * b_chunk + (b_chunk >> 1), &p.b_up, &full[s], (i * p.kc + c) * 64, f0);
-        }
-      } else if (p.whole) {
-        if constexpr (GU)
-          w_load_4d(dst, &p.b, &full[s], 0, f0, 0, i * p.kc);
-        else
-          w_load_3d(dst, &p.b, &full[s], 0, f0, i * p.kc);
+      if (!GU && p.whole) {
+        w_load_3d(dst, &p.b, &full[s], 0, f0, i * p.kc);
       } else {
         for (int c = 0; c < p.kc; ++c) {
-          if constexpr (GU)
-            w_load_3d(dst + c * b_chunk, &p.b, &full[s], (i * p.kc + c) * 64, f0, 0);
-          else
-            w_load_2d(dst + c * b_chunk, &p.b, &full[s], (i * p.kc + c) * 64, f0);
+          w_load_2d(dst + c * b_chunk, &p.b, &full[s], (i * p.kc + c) * 64, f0);
+          if constexpr (GU) w_load_2d(dst + c * b_chunk + (b_chunk >> 1), &p.b_up, &full[s], (i * p.kc + c) * 64, f0);
         }
       }
     };
@@ -212,12 +206,11 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
     }
     const size_t at = static_cast<size_t>(t) * p.M + f1 + f;
     if constexpr (GU) {
-      const float2 g = p.swapped ? w : v, u = p.swapped ? v : w;
       *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at) =
-          pack_bf16(glu_hidden<ACT>(F2{g.x, g.y}, F2{u.x, u.y}, caps));
+          pack_bf16(glu_hidden<ACT>(F2{v.x, v.y}, F2{w.x, w.y}, caps));
       if (p.save_g) {
-        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.save_g) + at) = pack_bf16(g.x, g.y);
-        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.save_u) + at) = pack_bf16(u.x, u.y);
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.save_g) + at) = pack_bf16(v.x, v.y);
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.save_u) + at) = pack_bf16(w.x, w.y);
       }
     } else {
       *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at) = pack_bf16(v.x, v.y);

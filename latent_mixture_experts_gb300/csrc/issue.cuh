@@ -44,14 +44,6 @@ __device__ __forceinline__ void w_load_3d(void* dst, const CUtensorMap* m, uint6
                "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
                : "memory");
 }
-__device__ __forceinline__ void w_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2,
-                                          int c3) {
-  asm volatile(LMOE_ELECT
-               "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
-               "%4, %5, %6}], [%2];\n\t}" ::"r"(smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-               : "memory");
-}
 // Counted on a barrier of either CTA of the pair (`bar`: a shared::cluster address).
 __device__ __forceinline__ void w_load_2d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
   asm volatile(LMOE_ELECT

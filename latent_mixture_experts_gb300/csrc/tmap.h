@@ -54,20 +54,4 @@ inline bool make_tmap_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* bas
   return r == CUDA_SUCCESS;
 }
 
-// 4-D tensor [d3][d2][d1][d0] (d0 contiguous) with explicit byte strides.
-inline bool make_tmap_4d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t d0, uint64_t d1,
-                         uint64_t d2, uint64_t d3, uint64_t stride1_bytes, uint64_t stride2_bytes,
-                         uint64_t stride3_bytes, uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3,
-                         CUtensorMapSwizzle swz) {
-  EncodeTiledFn fn = encode_tiled_fn();
-  if (!fn) return false;
-  cuuint64_t dims[4] = {d0, d1, d2, d3};
-  cuuint64_t strides[3] = {stride1_bytes, stride2_bytes, stride3_bytes};
-  cuuint32_t box[4] = {b0, b1, b2, b3};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = fn(m, dt, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 }  // namespace lmoe

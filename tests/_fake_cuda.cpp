@@ -2,7 +2,9 @@
 // kernels.  It keeps the rules that the host code has to keep: a launch of more
 // than 48 KB of dynamic shared memory fails unless the limit of that function
 // was raised on the current device, and tensor maps are checked as the driver
-// checks them.  Device memory is host memory that nothing writes.
+// checks them; maps that reach beyond the one tensor that they begin in are
+// counted (fake_tensor names the tensors).  Device memory is host memory that
+// nothing writes.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -18,6 +20,16 @@ int device = 0, launches = 0, last_device = -1, attribute_calls = 0, failing_att
 cudaError_t last_error = cudaSuccess;
 std::map<std::pair<int, const void*>, int> limits;
 
+std::map<uintptr_t, size_t> tensors;
+int maps = 0, outside = 0;
+
+bool within_one(uintptr_t from, uintptr_t to) {
+  auto it = tensors.upper_bound(from);
+  if (it == tensors.begin()) return false;
+  --it;
+  return to <= it->first + it->second;
+}
+
 cudaError_t answer(cudaError_t e) {
   if (e != cudaSuccess) last_error = e;
   return e;
@@ -32,6 +44,11 @@ CUresult encode(CUtensorMap*, CUtensorMapDataType dt, cuuint32_t rank, void* bas
   for (cuuint32_t i = 0; i < rank; ++i) ok = ok && dims[i] >= 1 && dims[i] <= 1ull << 32 && box[i] >= 1 &&
                                              box[i] <= 256 && steps[i] == 1;
   for (cuuint32_t i = 0; i + 1 < rank; ++i) ok = ok && strides[i] % 16 == 0 && strides[i] < 1ull << 40;
+  uint64_t bytes = dims[0] * size;
+  for (cuuint32_t i = 0; i + 1 < rank; ++i) bytes += (dims[i + 1] - 1) * strides[i];
+  const uintptr_t at = reinterpret_cast<uintptr_t>(base);
+  ++maps;
+  outside += !within_one(at, at + bytes);
   return ok ? CUDA_SUCCESS : CUDA_ERROR_INVALID_VALUE;
 }
 }  // namespace
@@ -40,6 +57,10 @@ EXPORT void fake_set_device(int d) { device = d; }
 EXPORT int fake_launches() { return launches; }
 EXPORT int fake_last_device() { return last_device; }
 EXPORT int fake_attribute_calls() { return attribute_calls; }
+EXPORT void fake_tensor(void* p, size_t bytes) { tensors[reinterpret_cast<uintptr_t>(p)] = bytes; }
+EXPORT void fake_forget_tensors() { tensors.clear(); }
+EXPORT int fake_maps() { return maps; }
+EXPORT int fake_maps_outside() { return outside; }
 EXPORT void fake_fail_attributes(int n) { failing_attributes = n; }
 EXPORT void fake_fail_launches(int n) { failing_launches = n; }
 
@@ -114,9 +135,11 @@ cudaError_t cudaGetLastError() {
 }
 cudaError_t cudaMalloc(void** p, size_t n) {
   *p = std::aligned_alloc(256, (n + 255) / 256 * 256);
+  if (*p) tensors[reinterpret_cast<uintptr_t>(*p)] = n;
   return *p ? cudaSuccess : answer(cudaErrorMemoryAllocation);
 }
 cudaError_t cudaFree(void* p) {
+  tensors.erase(reinterpret_cast<uintptr_t>(p));
   std::free(p);
   return cudaSuccess;
 }

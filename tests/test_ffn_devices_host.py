@@ -1,5 +1,5 @@
-"""Calls of include/lmoe_ffn.h with two devices and with a failing runtime
-call, on a stand-in for the CUDA runtime."""
+"""Calls of include/lmoe_ffn.h with two devices, with a failing runtime call and
+with tensors anywhere in memory, on a stand-in for the CUDA runtime."""
 import ctypes
 
 import pytest
@@ -173,3 +173,46 @@ def test_binding_refuses_sizes_beyond_32_bits(monkeypatch):
         for weights, tokens in ((W, 8), (W8, n)):
             with pytest.raises(ValueError, match="32 bits"):
                 GatedFFN(weights, max_tokens=tokens)
+
+
+@pytest.mark.parametrize("up_first", [False, True])
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp8"])
+def test_every_tensor_map_lies_within_one_tensor(lib, b, mx, up_first):
+    """The weights, the tokens and the workspace are allocations of their own, gigabytes apart or side by side: what a
+    copy may touch between them, or past their ends, need not be memory."""
+    lib.fake_tensor.argtypes = [ctypes.c_void_p, ctypes.c_size_t]
+    at = [1 << 40]
+
+    def tensor(nbytes, gap=0):
+        p = at[0]
+        at[0] += (nbytes + 511) // 512 * 512 + gap
+        lib.fake_tensor(p, nbytes)
+        return p
+    size = 1 if mx else 2
+    sizes = ((32, 96), (288, 160), (2048, 6144)) if mx else ((8, 128), (64, 16), (264, 136), (512, 768), (2048, 6144))
+    for d, F in sizes:
+        for gap in (0, 512, 1 << 21, 5 << 29):
+            for T in (1, 3, 8, 40, 72, 100, 300, 2100):
+                lib.fake_forget_tensors()
+                one, two, down = (tensor(size * d * F, gap) for _ in range(3))
+                scales = tensor(d * F // 32, gap)
+                gate, up = (two, one) if up_first else (one, two)
+                w = b.LmoeFfnWeights(gate=gate, up=up, down=down, gate_s=scales, up_s=scales, down_s=scales)
+                cfg = b.LmoeFfnConfig(d_model=d, d_ff=F, act=0, situ_beta=4.0, situ_linear_beta=25.0, wfmt=int(mx),
+                                      max_tokens=T, training=int(not mx))
+                h = ctypes.c_void_p()
+                assert lib.lmoe_ffn_create(ctypes.byref(cfg), ctypes.byref(w), None, ctypes.byref(h)) == b.LMOE_OK
+                n = lib.fake_maps()
+                if mx:
+                    x, s, y = tensor(T * d, gap), tensor(T * d // 32, gap), tensor(2 * T * d, gap)
+                    assert lib.lmoe_ffn_forward_mx(h, x, s, T, y, None) == b.LMOE_OK
+                else:
+                    ld = d + 24
+                    x, dy = (tensor(2 * ((T - 1) * ld + d), gap) for _ in range(2))
+                    y, dx = (tensor(2 * T * d, gap) for _ in range(2))
+                    g, u = (tensor(2 * T * F, gap) for _ in range(2))
+                    dw = [tensor(2 * d * F, gap) for _ in range(3)]
+                    assert lib.lmoe_ffn_forward(h, x, ld, T, y, g, u, None) == b.LMOE_OK
+                    assert lib.lmoe_ffn_backward(h, x, ld, g, u, dy, ld, T, dx, *dw, None) == b.LMOE_OK
+                assert lib.fake_maps() > n and lib.fake_maps_outside() == 0, (d, F, gap, T)
+                assert lib.lmoe_ffn_destroy(h) == b.LMOE_OK

@@ -94,3 +94,22 @@ def test_many_tokens(ops, T):
     bf16._check_backward(layer.lmoe_ffn_backward(x, g, u, dy), x, g, u, dy, W, "situ")
     assert R.rel_l2(y, R.forward(x, W["gate"], W["up"], W["down"], "situ")[0]) <= bf16.REL
     layer.lmoe_ffn_sync_status()
+
+
+@pytest.mark.parametrize("T,d,F", [(3, 8, 128), (8, 8, 128), (1, 24, 304), (40, 64, 16), (72, 264, 136)])
+def test_matrices_gigabytes_apart(ops, T, d, F):
+    """Small weights with other allocations between them, as layers loaded one after the other leave them."""
+    x, W, dy = bf16._make(T, d, F, T + d)
+    far, between = {}, []
+    for n in ("gate", "up", "down"):
+        far[n] = W[n].clone()
+        between.append(torch.empty(1 << 31, device="cuda", dtype=torch.uint8))
+        # the caching allocator's small blocks come 2 MB at a time: the next matrix lies in another such block
+        between += [torch.empty(1 << 20, device="cuda", dtype=torch.uint8) for _ in range(4)]
+    layer = ops.GatedFFN(far, max_tokens=T, training=True)
+    y, g, u = layer.lmoe_ffn_forward(x, save=True)
+    gref, uref = bf16._check_forward(y, x, W, "situ")
+    bf16._check_pre(g, gref, x, W["gate"])
+    bf16._check_pre(u, uref, x, W["up"])
+    bf16._check_backward(layer.lmoe_ffn_backward(x, g, u, dy), x, g, u, dy, W, "situ")
+    layer.lmoe_ffn_sync_status()
