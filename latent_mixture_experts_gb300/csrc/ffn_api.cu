@@ -129,13 +129,13 @@ lmoe_status forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int T, void* 
     return LMOE_ERR_INVALID_ARG;
   // Up to 72 tokens stream the weights (ffn_skinny.cu), larger batches run on
   // pair tiles, K split where they are few.  Streaming against pair tiles, 64,
-  // 72 and 80 tokens, weights from HBM: widths 7168 and 6144 56.1, 56.7 and 61.0 us
-  // against 60.9, 61.0 and 61.0 us; 7168 and 2048 24.2, 24.7 and 26.7 us against
-  // 26.1, 26.7 and 26.9 us; 2048 and 2048 13.7, 14.2 and 15.1 us against 14.0, 14.8
+  // 72 and 80 tokens, weights from HBM: widths 7168 and 6144 55.2, 56.0 and 60.8 us
+  // against 60.6, 60.9 and 61.0 us; 7168 and 2048 24.3, 24.9 and 26.4 us against
+  // 26.0, 26.6 and 26.7 us; 2048 and 2048 13.7, 14.3 and 15.3 us against 14.0, 14.8
   // and 14.8 us.  One limit serves all widths, too high a one for blocks of few
-  // weights: 1152 and 864 9.1, 9.7 and 10.2 us against 8.7, 9.8 and 9.6 us; 512 and
-  // 512 lose from 48 tokens on (64: 8.0 us against 7.5 us), 256 and 256 always (8
-  // tokens 6.5 us against 6.0 us, 72 tokens 9.1 us against 7.4 us).
+  // weights: 1152 and 864 9.0, 9.6 and 10.0 us against 8.8, 9.7 and 9.7 us; 512 and
+  // 512 7.8, 8.4 and 8.5 us against 7.6, 8.3 and 8.3 us; 256 and 256 lose at any
+  // number (8 tokens 6.8 us against 6.2 us, 72 tokens 9.4 us against 7.6 us).
   if (T <= kSkinnyMaxTokens) {
     FfnSkinnyParams g = {}, n = {};
     g.T = n.T = T;
