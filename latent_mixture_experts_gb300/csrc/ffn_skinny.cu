@@ -13,10 +13,9 @@
 // would save half of the copies, but its copies also bring in memory behind the
 // first matrix, 80 KB for one of 2 KB, that need not be there: an illegal access.
 // Copies by maps of one matrix stayed within its 4 KB blocks, 188 maps measured.)
-// A ring of about 100 KB per CTA puts two
-// CTAs on an SM, and lets the down pass's CTAs load their first weights while
-// the gate/up pass's last ones finish.  One token at 7168 and 6144: 47 to
-// 48 us, 5.5 TB/s of weights.
+// A ring of about 100 KB per CTA puts two CTAs on an SM, and lets the down
+// pass's CTAs load their first weights while the gate/up pass's last ones
+// finish.  One token at 7168 and 6144: 47 to 48 us, 5.5 TB/s of weights.
 #include "ffn_act.cuh"
 #include "ffn_internal.h"
 #include "lmoe_internal.h"
