@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(128, 1) dense_gemm_kernel(const __grid_constan
     mbar_init(&done, 1);
     fence_mbar_init();
   }
+  __syncwarp();
   if (warp == 0) {
     tmem_alloc(&tmem_base, C::kTmemCols);
     tmem_relinquish();
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(128, 1) dense_gemm_kernel(const __grid_constan
           if (t < p.T) o16[static_cast<size_t>(t) * p.ldo + f] = __float2bfloat16_rn(h);
         }
       }
+      __syncwarp();      // lanes part at the last features; whole warps load
     }
   }
 #pragma unroll 1
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(128, 1) dense_gemm_kernel(const __grid_constan
           if (t < p.T) outp[static_cast<size_t>(t) * p.ldo] = have ? __uint_as_float(r[j]) : 0.0f;
         }
       }
+      __syncwarp();
     }
   }
   tc_fence_before();

@@ -134,6 +134,7 @@ __device__ __forceinline__ bool epilogue_rows(const FfnPairParams& p, const Tile
 #pragma unroll
       for (int j = 0; j < 16; ++j) w[j] = pack_bf16(glu_hidden<ACT>(pair_at(g, j), pair_at(u, j), caps));
       if (row_ok) store32(out(0, at + c), w, left, p.wide);
+      __syncwarp();      // lanes part at the last rows; whole warps load
     }
   } else {
     const int n0 = t.n * TN, N = p.N[t.prod], c0 = TN / 2 * half;
@@ -154,6 +155,7 @@ __device__ __forceinline__ bool epilogue_rows(const FfnPairParams& p, const Tile
         const int next = row_ok && c + 32 < c0 + TN / 2 ? left - 32 : 0;
         load32(gp + c + 32, g1, next);
         load32(up + c + 32, u1, next);
+        __syncwarp();      // lanes part at the last rows; whole warps load and wait
         tmem_ld_wait();
         uint32_t h[16];
 #pragma unroll
@@ -173,6 +175,7 @@ __device__ __forceinline__ bool epilogue_rows(const FfnPairParams& p, const Tile
           g[j] = g1[j];
           u[j] = u1[j];
         }
+        __syncwarp();
       }
     } else if constexpr (MODE == kFfnLinear) {
       const size_t at = static_cast<size_t>(row0) * N + n0;
@@ -331,6 +334,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
     }
     fence_mbar_init();
   }
+  __syncwarp();
   cluster_sync();
   if (warp == 1) {      // under the first loads
     tmem_alloc_pair(&tmem_base, 2 * TN);

@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
     }
     fence_mbar_init();
   }
+  __syncwarp();
   cluster_sync();
   griddep_launch();
   if (warp == 1) {      // under the first loads
@@ -227,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
             if (row < p.M)
               store_hidden_block(h, static_cast<uint8_t*>(p.out) + static_cast<size_t>(row) * p.N + f,
                                  p.out_sf + atom_byte(row, f >> 5, p.out_nkb));
+            __syncwarp();      // lanes part at the last rows; whole warps load
           }
         } else {
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(row) * p.N + n * TN;
@@ -239,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_mx_pair_kernel(const __grid_c
             tmem_ld_wait();
             pack32(v, w);
             if (row < p.M) store32(dst + c, w, left, p.wide);
+            __syncwarp();
           }
         }
       }

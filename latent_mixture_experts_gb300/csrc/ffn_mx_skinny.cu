@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
     mbar_init(&rows_ready, GU ? blockDim.x / 32 - 2 : 1);
     fence_mbar_init();
   }
+  __syncwarp();
   if (warp == 0) {
     tmem_alloc(&tmem_base, kTmem);
     tmem_relinquish();
@@ -176,11 +177,13 @@ __global__ void __launch_bounds__(kManyThreads) ffn_mx_skinny_kernel(const __gri
       if (t < p.T)
 #pragma unroll
         for (int j = 0; j < 32; j += 4) st_cluster4(dst + 4 * (c + j), v + j);
+      __syncwarp();      // lanes part at the stores; whole warps load
     }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tacc, kTmem);
+  __syncwarp();
   cluster_arrive();
   cluster_wait();
   const int tok0 = rank * per, ntok = min(per, p.T - tok0);

@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
     lost = 0;
     fence_mbar_init();
   }
+  __syncwarp();
   if (warp == 0) {
     tmem_alloc(&tmem_base, N);
     tmem_relinquish();
@@ -209,8 +210,10 @@ __global__ void __launch_bounds__(kManyThreads) ffn_skinny_kernel(const __grid_c
           const int up = GU && c + j >= rows, f = c + j - (up ? rows : 0), o = f >> lfs;
           st_cluster4(map_rank(recv, o) + at + 4 * (f - o * fs + (up ? fs : 0)), v + j);
         }
+      __syncwarp();      // the last rows' lanes part at the stores; whole warps load and meet at the barrier
     }
   }
+  __syncwarp();
   tc_fence_before();
   cluster_arrive();
   cluster_wait();      // the sums are here, and every warp of this CTA is done with tensor memory

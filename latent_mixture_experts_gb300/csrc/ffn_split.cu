@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kThreads) ffn_split_kernel(const __grid_consta
       }
     }
   }
+  __syncwarp();
   tc_fence_before();
   cluster_arrive();
   cluster_wait();
