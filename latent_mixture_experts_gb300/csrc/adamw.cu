@@ -149,7 +149,8 @@ __device__ __forceinline__ void store(uint8_t* p, int left, const uint32_t (&w)[
 // scale of their block of four lanes.  Multiplied by 2^-120 a value in units of its scale
 // has E4M3's exponents in fp32, its subnormals among fp32's (2^-9 becomes 2^-129, 20 bits
 // above the last one), so the code lies in bits 20..26 whatever the value, and rounding
-// is one addition below them.  ROOT: no sign, and what is not zero stays so.
+// is one addition below them.  ROOT: no sign, and what is not zero stays so, however far
+// below the block's maximum (at 2^-38 of it the product with `down` is zero).
 template <bool ROOT>
 __device__ __forceinline__ uint32_t encode(float (&f)[8], const uint32_t (&word)[8], uint32_t (&codes)[2]) {
   float m = 0.0f;
@@ -164,7 +165,10 @@ __device__ __forceinline__ uint32_t encode(float (&f)[8], const uint32_t (&word)
   float down = __uint_as_float((134u - s) << 23);
   if (__builtin_expect(s > 133u, 0)) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] *= 0x1p-120f;
+    for (int j = 0; j < 8; ++j) {
+      const float x = f[j] * 0x1p-120f;
+      f[j] = ROOT && f[j] != 0.0f ? fmaxf(x, 0x1p-149f) : x;
+    }
     down = s == 255u ? 0.0f : __uint_as_float((254u - s) << 23);
   }
 #pragma unroll
@@ -174,7 +178,7 @@ __device__ __forceinline__ uint32_t encode(float (&f)[8], const uint32_t (&word)
     for (int j = 0; j < 4; ++j) {
       const uint32_t w = word[4 * i + j], a = __float_as_uint(fabsf(f[4 * i + j]) * down);
       c[j] = (a + (ROOT ? w & 0xFFFFFu : w >> 12)) >> 20;
-      if (ROOT && a != 0) c[j] = max(c[j], 1u);
+      if (ROOT && f[4 * i + j] != 0.0f) c[j] = max(c[j], 1u);
       x[j] = __float_as_uint(f[4 * i + j]);
     }
     // Not by shifts: compiled (ptxas 13.0, -O2 and up) they left nothing of c[3].
