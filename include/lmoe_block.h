@@ -157,11 +157,14 @@ LMOE_API lmoe_status lmoe_linear_destroy(lmoe_linear_handle h);
 /*   g = grad * grad_scale
  *   m = beta1 m + (1 - beta1) g,    v = beta2 v + (1 - beta2) g^2
  *   w = w (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
- * for every value of every tensor, in fp32 (the root of a v below 2^-126 is zero).  t:
- * the number of the step, kept on the device.  What is stored in fewer bits after that:
+ * for every value of every tensor, in fp32 (the root of a v below 2^-126 is zero; the
+ * root and the division are the card's approximations, each within 2^-22 of its value).
+ * What w changes by, the decay and the step together, is summed first and added to w
+ * once.  t: the number of the step, kept on the device.  What is stored in fewer bits
+ * after that:
  *   - a bf16 weight with an fp32 master: the master's value rounded to nearest;
  *   - a bf16 weight without one: rounded stochastically, so that updates far smaller
- *     than a step of the weight still arrive in the mean;
+ *     than a step of the weight still arrive in the mean (down to fp32's last bit of it);
  *   - MXFP8 states: m, and sqrt(v) in place of v (half the range of exponents), rounded
  *     stochastically: rounded to nearest they would never decay (a factor of 0.999 is
  *     less than half a step).  A root that is not zero is not rounded to zero: m is

@@ -199,7 +199,7 @@ struct Chunk {
   uint8_t *m_scale, *v_scale;
   long long at, rest;           // this thread's first value; values from there to the tensor's end
   unsigned long long first;
-  float keep;                   // 1 - lr weight_decay
+  float decay;                  // -lr weight_decay
   bool grad_fp32, fp32, rounded;
 };
 
@@ -324,7 +324,10 @@ __device__ __forceinline__ void update(const AdamParams& p, const Factors& f, co
     root[j] = fast_sqrt(v2.x), root[j + 1] = fast_sqrt(v2.y);
     const F2 d = vfma(F2{root[j], root[j + 1]}, splat<F2>(f.k2), splat<F2>(p.eps));
     const F2 u = vmul(m2, splat<F2>(f.k1));
-    const F2 w2 = vfma(u, F2{fast_rcp(d.x), fast_rcp(d.y)}, vmul(F2{w[j], w[j + 1]}, splat<F2>(c.keep)));
+    // The step and the decay are added first, and then the weight once: 1 - lr weight_decay would round the decay to
+    // fp32's grid below one, the same way for every weight (1e-7 would be 1.2e-7, 2e-8 nothing).
+    const F2 w1 = {w[j], w[j + 1]}, step = vfma(w1, splat<F2>(c.decay), vmul(u, F2{fast_rcp(d.x), fast_rcp(d.y)}));
+    const F2 w2 = vadd(w1, step);
     m[j] = m2.x, m[j + 1] = m2.y, v[j] = v2.x, v[j + 1] = v2.y, w[j] = w2.x, w[j + 1] = w2.y;
   }
   uint32_t word[8];
@@ -382,7 +385,7 @@ __device__ __forceinline__ void work(const AdamParams& p, const Factors& f, int 
   c.m_scale = x.m_scale;
   c.v_scale = x.v_scale;
   c.first = x.first;
-  c.keep = 1.0f - f.lr * x.decay;
+  c.decay = -f.lr * x.decay;
   c.grad_fp32 = p.fp32[id >> 5] >> (id & 31) & 1u;
   c.fp32 = x.fp32;
   c.rounded = !x.fp32 && !x.master;

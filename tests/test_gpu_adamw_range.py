@@ -39,3 +39,31 @@ def test_roots_far_below_their_block(ops, apart, size):
             small = x.reshape(-1).to(R.D) ** 2 * (1 - BETAS[1]) >= 2.0 ** -125
             assert bool((opt.state(i)["v"] != 0)[small].all()), i
         _check_step(opt, before, g, decay, t)
+
+
+@pytest.mark.parametrize("rate", [1e-5, 1e-6, 1e-7, 4e-8])
+@pytest.mark.parametrize("pt,masters", [(F32, True), (BF, True)], ids=["fp32", "master"])
+def test_decay_far_below_a_weight(ops, pt, masters, rate):
+    """Without a gradient a weight loses lr weight_decay of itself, rounded once: off by half a step of fp32 at the
+    weight's size, and by the rounding of the product lr weight_decay w (three of 2^-24)."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    p = (1 + torch.rand(1 << 16, device="cuda", generator=g)).to(pt)
+    lr = 1e-3
+    opt = ops.AdamW([p], lr=lr, weight_decay=rate / lr, masters=masters)
+    if pt is BF:
+        opt.master.copy_(1 + torch.rand(1 << 16, device="cuda", generator=g))
+    w = (opt.master if pt is BF else p).to(R.D).clone()
+    opt.step([torch.zeros_like(p)])
+    got = (opt.master if pt is BF else p).to(R.D)
+    want = w * (1 - rate)
+    assert bool(((got - want).abs() <= 2.0 ** -24 + 3 * 2.0 ** -24 * rate * w).all()), float((got - want).abs().max())
+
+
+def test_steps_and_decay_are_added_before_the_weight(ops):
+    """A step and a decay that each are less than half of a weight's last bit, and together more, arrive."""
+    n = 1 << 12
+    p = torch.full((n,), 1.5, device="cuda")
+    rate = 0.4 * 2.0 ** -23 / 1.5
+    opt = ops.AdamW([p], lr=0.4 * 2.0 ** -23, betas=(0.0, 0.0), eps=0.0, weight_decay=rate / (0.4 * 2.0 ** -23))
+    opt.step([torch.ones(n, device="cuda")])
+    assert bool((p == 1.5 - 2.0 ** -23).all())
