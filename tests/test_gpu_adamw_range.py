@@ -67,3 +67,29 @@ def test_steps_and_decay_are_added_before_the_weight(ops):
     opt = ops.AdamW([p], lr=0.4 * 2.0 ** -23, betas=(0.0, 0.0), eps=0.0, weight_decay=rate / (0.4 * 2.0 ** -23))
     opt.step([torch.ones(n, device="cuda")])
     assert bool((p == 1.5 - 2.0 ** -23).all())
+
+
+@pytest.mark.parametrize("first", [(1 << 32) - 2048 - 32, (1 << 32) - 32, 1 << 32, 5 << 32, (1 << 40) + 96])
+def test_numbers_beyond_32_bits(ops, first):
+    """A tensor whose values are numbered from `first` on, through the C call: the words of the numbers, of whole vectors
+    and of their last values, also where they pass 2^32."""
+    from latent_mixture_experts_gb300 import binding as b
+    lib, n = b.load_library(), 4096 + 77
+    params, grads = _make(22, shapes=[(n,)])
+    m, v = (torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ms, vs = (torch.zeros((n + 31) // 32, dtype=torch.uint8, device="cuda") for _ in range(2))
+    count = torch.zeros(1, dtype=torch.int64, device="cuda")
+    t = b.LmoeAdamwTensor(param=params[0].data_ptr(), n=n, first=first, weight_decay=DECAY, m=m.data_ptr(),
+                          v=v.data_ptr(), m_scale=ms.data_ptr(), v_scale=vs.data_ptr())
+    c = b.LmoeAdamwConfig(beta1=BETAS[0], beta2=BETAS[1], eps=EPS, states=1, seed=7, step=count.data_ptr())
+    h = ctypes.c_void_p()
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.lmoe_adamw_create(ctypes.byref(c), ctypes.byref(t), 1, stream, ctypes.byref(h)) == b.LMOE_OK
+    opt = SimpleNamespace(params=params, offsets=[first], seed=7, states="mxfp8",
+                          state=lambda i: {"m": m, "v": v, "m_scales": ms, "v_scales": vs})
+    for k, g in enumerate(grads, 1):
+        before = [_snapshot(opt, 0)]
+        assert lib.lmoe_adamw_step(h, (ctypes.c_void_p * 1)(g[0].data_ptr()), None, LR, None, None,
+                                   stream) == b.LMOE_OK
+        _check_step(opt, before, g, [DECAY], k)
+    assert int(count) == 3 and lib.lmoe_adamw_destroy(h) == b.LMOE_OK
