@@ -81,11 +81,12 @@ __device__ __forceinline__ F2 linear_act(F2 z) {
   return z;
 }
 
-// The derivative.  Beyond 16 silu's and gelu's terms are 0 or 1 within fp32 (gelu's) or
+// The derivative; a NaN stays one.  Beyond 16 silu's and gelu's terms are 0 or 1 within fp32 (gelu's) or
 // need no product of a huge and a zero factor.
+__device__ __forceinline__ float step(float z) { return z <= 0.0f ? 0.0f : z > 0.0f ? 1.0f : z; }
 template <int ACT>
 __device__ __forceinline__ F2 linear_slope(F2 z) {
-  if constexpr (ACT == kActRelu) return {z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f};
+  if constexpr (ACT == kActRelu) return {step(z.x), step(z.y)};
   if constexpr (ACT == kActSilu) {
     F2 rest;
     const F2 s = sigmoid(z, rest);

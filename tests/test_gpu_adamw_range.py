@@ -71,8 +71,8 @@ def test_steps_and_decay_are_added_before_the_weight(ops):
 
 @pytest.mark.parametrize("first", [(1 << 32) - 2048 - 32, (1 << 32) - 32, 1 << 32, 5 << 32, (1 << 40) + 96])
 def test_numbers_beyond_32_bits(ops, first):
-    """A tensor whose values are numbered from `first` on, through the C call: the words of the numbers, of whole vectors
-    and of their last values, also where they pass 2^32."""
+    """A tensor whose values are numbered from `first` on, through the C call: the words of the numbers, of whole
+    vectors and of the last values, also where they pass 2^32."""
     from latent_mixture_experts_gb300 import binding as b
     lib, n = b.load_library(), 4096 + 77
     params, grads = _make(22, shapes=[(n,)])

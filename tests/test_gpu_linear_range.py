@@ -1,5 +1,5 @@
 """The backward pass of Linear at the ends of its range: many rows for each thread of the
-bias gradient's sums."""
+bias gradient's sums, and pre-activations that are NaN."""
 import pytest
 import torch
 
@@ -44,3 +44,21 @@ def test_bias_gradient_of_random_rows(ops, T, N, dt):
     for c in range(0, N, 4096):
         d = dy[:, c:c + 4096].to(R.D)
         assert bool(((got[c:c + 4096] - d.sum(0)).abs() <= 2.0 ** -16 * d.abs().sum(0) + R.TINY).all())
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "fp32"])
+def test_slope_of_nan_is_nan(ops, act, dt):
+    """Where the forward pass gave NaN, so does the backward pass: a saved z of NaN is no zero slope."""
+    T, N = 40, 64
+    layer = ops.Linear(torch.eye(N, device="cuda").to(BF), torch.zeros(N, device="cuda", dtype=BF), act, max_tokens=T,
+                       training=True)
+    x = torch.randn(T, N, device="cuda").to(BF)
+    x[3, 5] = float("nan")
+    y, z = layer.lmoe_linear_forward(x, save=True)
+    assert bool(y[3].isnan().all()) and bool(y[4:].isfinite().all())
+    z[4:] = x[4:]
+    dx, dw, db = layer.lmoe_linear_backward(x.nan_to_num(0.0), torch.ones(T, N, device="cuda", dtype=dt), z)
+    keep = torch.arange(T, device="cuda") != 3
+    assert bool(dx[3].isnan().all()) and bool(dx[keep].isfinite().all())
+    assert bool(dw.isnan().all()) and bool(db.isnan().all())
