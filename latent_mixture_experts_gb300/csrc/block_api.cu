@@ -286,7 +286,7 @@ lmoe_status lmoe_linear_create(const lmoe_linear_config* cfg, const void* w, con
   if (K < 1 || N < 1 || cfg->max_tokens < 1 || cfg->act < LMOE_LINEAR_NONE || cfg->act > LMOE_LINEAR_GELU ||
       (cfg->training != 0 && cfg->training != 1) || !usable(w) || !aligned16(bias))
     return LMOE_ERR_INVALID_ARG;
-  if (K % 8 || N % 8) return LMOE_ERR_UNSUPPORTED;
+  if (K % 8 || N % 8 || K > kMostRows || N > kMostRows || cfg->max_tokens > kMostRows) return LMOE_ERR_UNSUPPORTED;
   int dev = 0;
   BLOCK_TRY_STATUS(this_device(&dev));
   lmoe_linear_ctx* h = new (std::nothrow) lmoe_linear_ctx;

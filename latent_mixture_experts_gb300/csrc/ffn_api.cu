@@ -351,7 +351,9 @@ lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* 
   const bool mx = cfg->wfmt == LMOE_FFN_W_MXFP8;
   if (!usable(w->gate) || !usable(w->up) || !usable(w->down)) return LMOE_ERR_INVALID_ARG;
   if (mx && (!usable(w->gate_s) || !usable(w->up_s) || !usable(w->down_s))) return LMOE_ERR_INVALID_ARG;
-  if (d % (mx ? 32 : 8) || F % (mx ? 32 : 8) || (mx && cfg->training)) return LMOE_ERR_UNSUPPORTED;
+  if (d % (mx ? 32 : 8) || F % (mx ? 32 : 8) || (mx && cfg->training) || d > kMostRows || F > kMostRows ||
+      cfg->max_tokens > kMostRows)
+    return LMOE_ERR_UNSUPPORTED;
   int dev = 0, major = 0, minor = 0;
   FFN_TRY(cudaGetDevice(&dev));
   FFN_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));

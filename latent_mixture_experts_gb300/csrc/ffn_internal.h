@@ -44,6 +44,8 @@ struct LinearEpilogue {
   int act;                    // lmoe_linear_act
 };
 constexpr int kPairProducts = 4;
+// Rows and columns of a product: they are counted in ints, and tiles reach past the last one.
+constexpr int kMostRows = 1 << 30;
 struct FfnPairParams {
   CUtensorMap a[kPairProducts], b[kPairProducts], a_cat, b_cat;
   CUtensorMap b_half[2];      // K-contiguous b with boxes of half as many rows

@@ -93,7 +93,8 @@ cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* f, void
   const auto it = limits.find({device, f});
   if (c->dynamicSmemBytes > 48 * 1024 && (it == limits.end() || static_cast<int>(c->dynamicSmemBytes) > it->second))
     return answer(cudaErrorInvalidValue);
-  if (!c->gridDim.x || !c->blockDim.x || c->blockDim.x > 1024) return answer(cudaErrorInvalidConfiguration);
+  if (!c->gridDim.x || c->gridDim.x > 0x7FFFFFFFu || c->gridDim.y > 65535 || !c->blockDim.x || c->blockDim.x > 1024)
+    return answer(cudaErrorInvalidConfiguration);
   for (unsigned i = 0; i < c->numAttrs; ++i)
     if (c->attrs[i].id == cudaLaunchAttributeClusterDimension && c->gridDim.x % c->attrs[i].val.clusterDim.x)
       return answer(cudaErrorInvalidConfiguration);

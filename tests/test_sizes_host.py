@@ -1,0 +1,52 @@
+"""Sizes near 2^31, which the C calls' ints still hold: taken or refused, on the stand-in
+for the CUDA runtime.  Rows of the products are counted in ints, tiles of 256 at a time, so
+that their handles refuse sizes over 2^30."""
+import ctypes
+
+import pytest
+
+from tests import _fake_block, _fake_cuda
+from tests._harness import built_library
+
+A = 0x10000      # an aligned address that nothing reads
+MOST, LAST = 1 << 30, (1 << 31) - 1
+
+
+@pytest.fixture(scope="module")
+def b():
+    built_library()
+    from latent_mixture_experts_gb300 import binding
+    return binding
+
+
+@pytest.mark.parametrize("training", [0, 1])
+@pytest.mark.parametrize("size", [dict(max_tokens=MOST + 1), dict(max_tokens=LAST), dict(d_in=MOST + 8),
+                                  dict(d_in=LAST - 7), dict(d_out=MOST + 8), dict(d_out=LAST - 7)])
+def test_products_over_2_30_are_refused(tmp_path_factory, b, size, training):
+    lib = _fake_block.load(tmp_path_factory)
+    c = b.LmoeLinearConfig(**(dict(d_in=8, d_out=8, act=0, max_tokens=1, training=training) | size))
+    h = ctypes.c_void_p()
+    assert lib.lmoe_linear_create(ctypes.byref(c), A, None, None, ctypes.byref(h)) == b.LMOE_ERR_UNSUPPORTED
+    assert not h.value
+
+
+@pytest.mark.parametrize("size", [dict(max_tokens=MOST), dict(d_in=MOST), dict(d_out=MOST)])
+def test_products_of_2_30_run(tmp_path_factory, b, size):
+    lib = _fake_block.load(tmp_path_factory)
+    kw = dict(d_in=8, d_out=8, act=1, max_tokens=1, training=0) | size
+    c, h = b.LmoeLinearConfig(**kw), ctypes.c_void_p()
+    assert lib.lmoe_linear_create(ctypes.byref(c), A, None, None, ctypes.byref(h)) == b.LMOE_OK
+    assert lib.lmoe_linear_forward(h, A, kw["d_in"], kw["max_tokens"], A, kw["d_out"], 0, A, A, None) == b.LMOE_OK
+    assert lib.lmoe_linear_destroy(h) == b.LMOE_OK
+
+
+@pytest.mark.parametrize("mx", [0, 1])
+@pytest.mark.parametrize("size", [dict(max_tokens=MOST + 1), dict(max_tokens=LAST), dict(d_model=MOST + 32),
+                                  dict(d_ff=LAST - 31)])
+def test_blocks_over_2_30_are_refused(tmp_path_factory, b, size, mx):
+    lib = _fake_cuda.load(tmp_path_factory)
+    c = b.LmoeFfnConfig(**(dict(d_model=32, d_ff=32, act=0, situ_beta=4.0, situ_linear_beta=25.0, wfmt=mx,
+                                max_tokens=1, training=0) | size))
+    w, h = b.LmoeFfnWeights(**{n: A for n in b._FFN_WEIGHT_FIELDS}), ctypes.c_void_p()
+    assert lib.lmoe_ffn_create(ctypes.byref(c), ctypes.byref(w), None, ctypes.byref(h)) == b.LMOE_ERR_UNSUPPORTED
+    assert not h.value
