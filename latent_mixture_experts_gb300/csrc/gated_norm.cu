@@ -568,7 +568,7 @@ bool plan(Plan& r, int T, int d, int vpt, int most, int row, int sums) {
   const int fit = kRing / row;
   if (r.groups > fit / 2) r.groups = fit > 1 ? fit / 2 : 1;      // each has two rows in flight at least, where they fit
   r.stages = fit / r.groups < kMaxStages ? fit / r.groups : kMaxStages;
-  const int need = (T + r.groups - 1) / r.groups;
+  const int need = (T - 1) / r.groups + 1;
   r.grid = need < kCtas ? need : kCtas;
   const size_t ring = static_cast<size_t>(r.groups) * r.stages * row;
   const size_t met = r.groups > 1 ? static_cast<size_t>(r.groups) * sums * 4 : 0;

@@ -481,7 +481,7 @@ BwdPlan bwd_plan(int T, int d, int row) {
   const int fit = kRingSmem / row;
   if (b.groups > fit / 2) b.groups = fit > 1 ? fit / 2 : 1;
   b.stages = fit / b.groups < kRingMaxStages ? fit / b.groups : kRingMaxStages;
-  const int need = (T + b.groups - 1) / b.groups;
+  const int need = (T - 1) / b.groups + 1;
   b.grid = need < kRingCtas ? need : kRingCtas;
   return b;
 }

@@ -1,6 +1,6 @@
 """Sizes near 2^31, which the C calls' ints still hold: taken or refused, on the stand-in
 for the CUDA runtime.  Rows of the products are counted in ints, tiles of 256 at a time, so
-that their handles refuse sizes over 2^30."""
+that their handles refuse sizes over 2^30; the norms take every T."""
 import ctypes
 
 import pytest
@@ -50,3 +50,17 @@ def test_blocks_over_2_30_are_refused(tmp_path_factory, b, size, mx):
     w, h = b.LmoeFfnWeights(**{n: A for n in b._FFN_WEIGHT_FIELDS}), ctypes.c_void_p()
     assert lib.lmoe_ffn_create(ctypes.byref(c), ctypes.byref(w), None, ctypes.byref(h)) == b.LMOE_ERR_UNSUPPORTED
     assert not h.value
+
+
+@pytest.mark.parametrize("T", [MOST, LAST])
+def test_norms_of_any_number_of_rows(tmp_path_factory, b, T):
+    lib = _fake_block.load(tmp_path_factory)
+    for gate in (0, 1, 2):
+        a = b.LmoeGatedNormArgs(T=T, d=8, y=A, ldy=8, stream=A, lds=8, stream_type=1, gate_type=gate, gate=A, ldgate=8,
+                                w_post=A, w_next=A, stream_scale=1.0, branch_scale=1.0, eps=1e-6)
+        assert lib.lmoe_gated_add_norm(ctypes.byref(a), A, A, 0, None, None) == b.LMOE_OK
+        assert lib.lmoe_gated_add_norm_backward(ctypes.byref(a), A, 8, A, 8, A, A, A, A, A, A, 1 << 30,
+                                                None) == b.LMOE_OK
+    lib = _fake_cuda.load(tmp_path_factory)
+    assert lib.lmoe_add_rms_norm(A, 8, A, 8, 0, T, 8, A, 1e-6, A, A, 0, A, None) == b.LMOE_OK
+    assert lib.lmoe_add_rms_norm_backward(A, 8, A, 8, A, 8, 0, T, 8, A, 1e-6, A, A, A, 1 << 30, None) == b.LMOE_OK
