@@ -55,8 +55,8 @@ class Gradients(NamedTuple):
 
 
 def _block_weights(block) -> list:
-    if not isinstance(block, GatedFFN):
-        raise ValueError("only a GatedFFN's weights are trained here")
+    if not isinstance(block, GatedFFN) or block.mx:
+        raise ValueError("only a GatedFFN's bf16 weights are trained here")
     return [block._weights[n] for n in ("gate", "up", "down")]
 
 
