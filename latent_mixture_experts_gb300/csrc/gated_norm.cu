@@ -577,23 +577,29 @@ bool plan(Plan& r, int T, int d, int vpt, int most, int row, int sums) {
 }
 
 // Vectors per thread.  8192 rows forward, 1 / 2 / 4, in us:
-//                              2560            3584            5120           7168       8192 wide
-//   bf16                     30 / 30 / 31    42 / 41 / 42    57 / 68 / 61    74 / 78 / 82   - / 84 / 98
-//   bf16, tokens' gate       38 / 36 / 38    52 / 52 / 52    72 / 74 / 69  105 / 103 / 95   - / 113 / 125
-//   fp32                     46 / 43 / 47    65 / 59 / 64    78 / 84 / 93  123 / 112 / 127  - / 133 / 131
-//   fp32, tokens' gate       52 / 50 / 51    72 / 73 / 71   89 / 105 / 101 144 / 143 / 132  - / 161 / 140
-//   to MXFP8                 33 / 30 / 37    41 / 42 / 54    65 / 71 / 62    82 / 80 / 89   - / 82 / 140
-//   to MXFP8, fp32 and gate  48 / 50 / 46    65 / 69 / 63    93 / 89 / 89  120 / 112 / 145  - / 145 / 150
-// Two take up to 19 warps: rows of ten or eleven leave room for one of them only (5120 wide, to MXFP8).
-// Few rows want many threads each: 333 rows 3584 wide 4.5 / 4.9 / 5.0 us.
+//                              2560          4096          5120           6144           7168        8192 wide
+//   bf16                     30/30/29      51/44/45      58/68/60       65/70/65       73/78/81      -/88/96
+//   bf16, gate               38/36/38      55/57/56      69/74/69       88/89/82     104/102/95      -/113/125
+//   fp32                     46/44/45      69/68/73      78/84/91       95/94/108    120/112/124     -/132/129
+//   fp32, gate               52/50/51      74/82/81      89/104/101   118/123/122    142/142/133     -/160/140
+//   to MXFP8                 33/30/35      58/43/53      65/71/60       73/73/78       82/80/87      -/82/137
+//   bf16, gate, to MXFP8     36/32/40      61/49/67      68/74/77       77/77/99      85/85/112      -/95/170
+//   fp32, to MXFP8           43/40/43      74/62/67      84/87/79      99/98/100    110/106/115      -/119/180
+//   fp32, gate, to MXFP8     48/50/46      79/80/69      93/89/89    107/100/101    120/112/145      -/141/150
+// (gate: of each token; 3584 wide within 6%, but for four to MXFP8.)  So two, except where another number is ahead:
+// rows over 4608 up to 5120 wide have ten of the 19 warps that two vectors take, one row at a time, and are faster with
+// one (20 of 28 warps) or four (three rows of five); bf16 rows to bf16, of which little is held, with one, unless that
+// leaves 10 to 13 of 28 warps without a row; tokens' gates as the table has it, onto fp32 from 4096 rows on (1024 rows
+// 5120 wide 16.2/-/14.8 us, 2048 26.8/-/25.8 us, 4096 47.0/-/50.1 us).  Few rows want many threads each: 333 rows 7168
+// wide 6.4/6.8/6.7 us, 8192 wide 7.0/7.4 us with two and four, 10.2/10.6 us onto fp32 with a gate.
 int forward_vectors(const GatedNorm& g, bool token, bool mx) {
-  if (g.d <= 2048 || (g.T < 1024 && g.d <= 7168)) return 1;
-  if (token && (g.fp32 || !mx)) return g.d <= 6144 || (!mx && (g.d <= 7168 || g.fp32)) ? 4 : 2;
-  if (mx) {
-    const int warps = (g.d + 511) / 512;
-    return warps == 10 || warps == 11 ? 4 : 2;
-  }
-  return g.d > 7168 || g.fp32 ? 2 : 1;
+  const int d = g.d;
+  if (d <= 2048 || (g.T < 1024 && d <= 7168)) return 1;
+  if (g.T < 1024) return 2;
+  if (token && g.fp32 && mx) return d <= 5120 ? 4 : 2;
+  if (token && !mx && d > 3584) return g.fp32 ? (d >= 4096 && d <= 6144 && g.T >= 4096 ? 1 : 4) : d <= 7168 ? 4 : 2;
+  if (d > 4608 && d <= 5120) return mx && !token ? 4 : 1;
+  return mx || token || g.fp32 || (d > 3584 && d <= 4608) || d > 7168 ? 2 : 1;
 }
 // 4096 rows backward, 1 / 2 / 3: 1024 wide 15.6 / 17.7 / 20.5 us, 2048 27.5 / 26.5 / 31.3
 // us, 3584 48.4 / 40.2 / 42.6 us, 7168 - / 66.4 / 67.6 us.  Two take up to 7680 values.
