@@ -181,8 +181,7 @@ __device__ __forceinline__ uint32_t encode(float (&f)[8], const uint32_t (&word)
       if (ROOT && f[4 * i + j] != 0.0f) c[j] = max(c[j], 1u);
       x[j] = __float_as_uint(f[4 * i + j]);
     }
-    // Not by shifts: compiled (ptxas 13.0, -O2 and up) they left nothing of c[3].
-    codes[i] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    codes[i] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
     if (!ROOT) {
       const uint32_t signs = __byte_perm(__byte_perm(x[0], x[1], 0x0073), __byte_perm(x[2], x[3], 0x0073), 0x5410);
       codes[i] |= signs & 0x80808080u;
