@@ -103,7 +103,7 @@ typedef enum {
 
 /*   z = x W^T + b,   y = act(z) + r
  * Products accumulate in fp32; z, act and the sum are fp32 and y is rounded once.
- * d_in and d_out multiples of 8; they and max_tokens at most 2^30. */
+ * d_in and d_out multiples of 8; they and T at most 2^30. */
 typedef struct {
   int d_in;
   int d_out;

@@ -84,7 +84,7 @@ typedef enum { LMOE_FFN_W_BF16 = 0, LMOE_FFN_W_MXFP8 = 1 } lmoe_ffn_wfmt;
  *   SwiGLU:   a = g sigmoid(g),             v = u
  * Products accumulate in fp32; hid is rounded to bf16 (MXFP8 blocks: encoded
  * as MXFP8) between the two passes.
- * Shapes: d_model and d_ff multiples of 8 (MXFP8: of 32); they and max_tokens at most 2^30. */
+ * Shapes: d_model and d_ff multiples of 8 (MXFP8: of 32); they and T at most 2^30. */
 typedef struct {
   int d_model;
   int d_ff;

@@ -136,6 +136,7 @@ lmoe_status linear_forward(lmoe_linear_handle h, const void* x, int64_t ldx, int
   if (!h || !on_its_device(h) || T < 0 || T > h->cfg.max_tokens ||
       (type != LMOE_STREAM_BF16 && type != LMOE_STREAM_FP32))
     return LMOE_ERR_INVALID_ARG;
+  if (T > kMostRows) return LMOE_ERR_UNSUPPORTED;
   h->launches = 0;
   if (T == 0) return LMOE_OK;
   const int K = h->cfg.d_in, N = h->cfg.d_out;
@@ -286,7 +287,7 @@ lmoe_status lmoe_linear_create(const lmoe_linear_config* cfg, const void* w, con
   if (K < 1 || N < 1 || cfg->max_tokens < 1 || cfg->act < LMOE_LINEAR_NONE || cfg->act > LMOE_LINEAR_GELU ||
       (cfg->training != 0 && cfg->training != 1) || !usable(w) || !aligned16(bias))
     return LMOE_ERR_INVALID_ARG;
-  if (K % 8 || N % 8 || K > kMostRows || N > kMostRows || cfg->max_tokens > kMostRows) return LMOE_ERR_UNSUPPORTED;
+  if (K % 8 || N % 8 || K > kMostRows || N > kMostRows) return LMOE_ERR_UNSUPPORTED;
   int dev = 0;
   BLOCK_TRY_STATUS(this_device(&dev));
   lmoe_linear_ctx* h = new (std::nothrow) lmoe_linear_ctx;
@@ -335,7 +336,7 @@ lmoe_status lmoe_linear_backward(lmoe_linear_handle h, const void* x, int64_t ld
   if (!h || !on_its_device(h) || T < 0 || T > h->cfg.max_tokens ||
       (type != LMOE_STREAM_BF16 && type != LMOE_STREAM_FP32))
     return LMOE_ERR_INVALID_ARG;
-  if (!h->cfg.training) return LMOE_ERR_UNSUPPORTED;
+  if (!h->cfg.training || T > kMostRows) return LMOE_ERR_UNSUPPORTED;
   h->launches = 0;
   const int K = h->cfg.d_in, N = h->cfg.d_out, act = h->cfg.act;
   if (!aligned16(dx) || !aligned16(dw) || !aligned16(dbias)) return LMOE_ERR_INVALID_ARG;

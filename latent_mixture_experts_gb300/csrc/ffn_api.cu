@@ -120,7 +120,7 @@ lmoe_status row_args(const void* p, int64_t ld, int d) {
 lmoe_status forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int T, void* out, void* gate, void* up, bool whole,
                     cudaStream_t stream) {
   if (!h || !on_its_device(h) || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
-  if (h->cfg.wfmt != LMOE_FFN_W_BF16) return LMOE_ERR_UNSUPPORTED;
+  if (h->cfg.wfmt != LMOE_FFN_W_BF16 || T > kMostRows) return LMOE_ERR_UNSUPPORTED;
   h->launches = 0;
   if (T == 0) return LMOE_OK;
   const int d = h->cfg.d_model, F = h->cfg.d_ff;
@@ -209,7 +209,7 @@ lmoe_status forward(lmoe_ffn_handle h, const void* x, int64_t ldx, int T, void* 
 lmoe_status forward_mx(lmoe_ffn_handle h, const uint8_t* x, const uint8_t* x_scales, int T, void* out, bool whole,
                        cudaStream_t stream) {
   if (!h || !on_its_device(h) || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
-  if (h->cfg.wfmt != LMOE_FFN_W_MXFP8) return LMOE_ERR_UNSUPPORTED;
+  if (h->cfg.wfmt != LMOE_FFN_W_MXFP8 || T > kMostRows) return LMOE_ERR_UNSUPPORTED;
   h->launches = 0;
   if (T == 0) return LMOE_OK;
   if (!usable(x) || !usable(x_scales) || !usable(out)) return LMOE_ERR_INVALID_ARG;
@@ -351,8 +351,7 @@ lmoe_status lmoe_ffn_create(const lmoe_ffn_config* cfg, const lmoe_ffn_weights* 
   const bool mx = cfg->wfmt == LMOE_FFN_W_MXFP8;
   if (!usable(w->gate) || !usable(w->up) || !usable(w->down)) return LMOE_ERR_INVALID_ARG;
   if (mx && (!usable(w->gate_s) || !usable(w->up_s) || !usable(w->down_s))) return LMOE_ERR_INVALID_ARG;
-  if (d % (mx ? 32 : 8) || F % (mx ? 32 : 8) || (mx && cfg->training) || d > kMostRows || F > kMostRows ||
-      cfg->max_tokens > kMostRows)
+  if (d % (mx ? 32 : 8) || F % (mx ? 32 : 8) || (mx && cfg->training) || d > kMostRows || F > kMostRows)
     return LMOE_ERR_UNSUPPORTED;
   int dev = 0, major = 0, minor = 0;
   FFN_TRY(cudaGetDevice(&dev));
@@ -451,7 +450,7 @@ lmoe_status lmoe_ffn_backward(lmoe_ffn_handle h, const void* x, int64_t ldx, con
                               const void* dy, int64_t lddy, int T, void* dx, void* dwg, void* dwu, void* dwd,
                               cudaStream_t stream) {
   if (!h || !on_its_device(h) || T < 0 || T > h->cfg.max_tokens) return LMOE_ERR_INVALID_ARG;
-  if (h->cfg.wfmt != LMOE_FFN_W_BF16 || !h->cfg.training) return LMOE_ERR_UNSUPPORTED;
+  if (h->cfg.wfmt != LMOE_FFN_W_BF16 || !h->cfg.training || T > kMostRows) return LMOE_ERR_UNSUPPORTED;
   h->launches = 0;
   const int d = h->cfg.d_model, F = h->cfg.d_ff;
   if (!aligned16(dx) || !aligned16(dwg) || !aligned16(dwu) || !aligned16(dwd)) return LMOE_ERR_INVALID_ARG;

@@ -1,6 +1,6 @@
 """Sizes near 2^31, which the C calls' ints still hold: taken or refused, on the stand-in
 for the CUDA runtime.  Rows of the products are counted in ints, tiles of 256 at a time, so
-that their handles refuse sizes over 2^30; the norms take every T."""
+that they refuse sizes over 2^30; the norms take every T."""
 import ctypes
 
 import pytest
@@ -20,14 +20,25 @@ def b():
 
 
 @pytest.mark.parametrize("training", [0, 1])
-@pytest.mark.parametrize("size", [dict(max_tokens=MOST + 1), dict(max_tokens=LAST), dict(d_in=MOST + 8),
-                                  dict(d_in=LAST - 7), dict(d_out=MOST + 8), dict(d_out=LAST - 7)])
-def test_products_over_2_30_are_refused(tmp_path_factory, b, size, training):
+@pytest.mark.parametrize("size", [dict(d_in=MOST + 8), dict(d_in=LAST - 7), dict(d_out=MOST + 8),
+                                  dict(d_out=LAST - 7)])
+def test_products_wider_than_2_30_are_refused(tmp_path_factory, b, size, training):
     lib = _fake_block.load(tmp_path_factory)
     c = b.LmoeLinearConfig(**(dict(d_in=8, d_out=8, act=0, max_tokens=1, training=training) | size))
     h = ctypes.c_void_p()
     assert lib.lmoe_linear_create(ctypes.byref(c), A, None, None, ctypes.byref(h)) == b.LMOE_ERR_UNSUPPORTED
     assert not h.value
+
+
+@pytest.mark.parametrize("T", [MOST + 1, LAST])
+def test_products_of_more_than_2_30_rows_are_refused(tmp_path_factory, b, T):
+    lib = _fake_block.load(tmp_path_factory)
+    c, h = b.LmoeLinearConfig(d_in=8, d_out=8, act=0, max_tokens=T, training=0), ctypes.c_void_p()
+    assert lib.lmoe_linear_create(ctypes.byref(c), A, None, None, ctypes.byref(h)) == b.LMOE_OK
+    n = lib.fake_launches()
+    assert lib.lmoe_linear_forward(h, A, 8, T, None, 8, 0, A, A, None) == b.LMOE_ERR_UNSUPPORTED
+    assert lib.lmoe_linear_selftest_timeout(h, A, T, A, None) == b.LMOE_ERR_UNSUPPORTED
+    assert lib.fake_launches() == n and lib.lmoe_linear_destroy(h) == b.LMOE_OK
 
 
 @pytest.mark.parametrize("size", [dict(max_tokens=MOST), dict(d_in=MOST), dict(d_out=MOST)])
@@ -41,9 +52,8 @@ def test_products_of_2_30_run(tmp_path_factory, b, size):
 
 
 @pytest.mark.parametrize("mx", [0, 1])
-@pytest.mark.parametrize("size", [dict(max_tokens=MOST + 1), dict(max_tokens=LAST), dict(d_model=MOST + 32),
-                                  dict(d_ff=LAST - 31)])
-def test_blocks_over_2_30_are_refused(tmp_path_factory, b, size, mx):
+@pytest.mark.parametrize("size", [dict(d_model=MOST + 32), dict(d_ff=LAST - 31)])
+def test_blocks_wider_than_2_30_are_refused(tmp_path_factory, b, size, mx):
     lib = _fake_cuda.load(tmp_path_factory)
     c = b.LmoeFfnConfig(**(dict(d_model=32, d_ff=32, act=0, situ_beta=4.0, situ_linear_beta=25.0, wfmt=mx,
                                 max_tokens=1, training=0) | size))
