@@ -74,8 +74,8 @@ LMOE_API lmoe_status lmoe_gated_add_norm(const lmoe_gated_norm_args* args, void*
  *   dgate: CHANNEL fp32 [d], the sum over rows of s n gH; TOKEN bf16 [T][d], packed,
  *          s n gH; NONE: not written, may be NULL
  * dr may be gh (ldgh = d), dy may be go (ldgo = d) or y (ldy = d).  The sums over
- * rows are added in an order that depends on T, d and the types only.  T = 0 writes
- * zero sums.  workspace: lmoe_gated_add_norm_backward_workspace bytes, contents
+ * rows are added in an order that depends on T, d, the types and which of gate and gh
+ * there are, in fp32, T / 152 of them one after the other.  T = 0 writes zero sums.  workspace: lmoe_gated_add_norm_backward_workspace bytes, contents
  * irrelevant.  A bounded wait that runs out leaves NaN in its rows and in the sums.
  * Errors as above. */
 LMOE_API lmoe_status lmoe_gated_add_norm_backward_workspace(int T, int d, size_t* bytes);
@@ -138,7 +138,7 @@ LMOE_API lmoe_status lmoe_linear_forward(lmoe_linear_handle h, const void* x_bf1
  *   dx = dz W bf16 [T][d_in],  dw = dz^T x bf16 [d_out][d_in],  dbias = sum of dz over
  *   rows, fp32 [d_out]
  * overwritten; any of the three may be NULL and is then not computed.  dz is rounded to
- * bf16 for the products (not for dbias).  The gradients may not overlap an input, the
+ * bf16 for the products, also where it is an fp32 dy itself (not for dbias).  The gradients may not overlap an input, the
  * weight or one another.  The same inputs and the same gradients asked for give the
  * same bits.  T = 0 writes zero dw and dbias. */
 LMOE_API lmoe_status lmoe_linear_backward(lmoe_linear_handle h, const void* x_bf16, int64_t ldx, const void* dy,

@@ -6,9 +6,9 @@
 // HBM bounds it: 28 bytes a value with fp32 states, a master and a bf16 gradient,
 // about 10 with MXFP8 states and no master.  A CTA takes a chunk of one or several times
 // 2048 values of one tensor; a thread holds eight consecutive values, four lanes a block
-// of 32 with its scales.  All arithmetic is fp32.  Measured on 132 million values: 529 us
-// with masters and fp32 states (7.0 TB/s), 417 us for bf16 weights; with MXFP8 states 327
-// us with masters (6.5 TB/s), 273 us for bf16 weights (4.9 TB/s), which what is left of
+// of 32 with its scales.  All arithmetic is fp32.  Measured on 132 million values: 534 us
+// with masters and fp32 states (6.9 TB/s), 416 us for bf16 weights; with MXFP8 states 326
+// us with masters (6.5 TB/s), 265 us for bf16 weights (5.0 TB/s), which what is left of
 // the decoding, mixing and encoding, about 65 instructions a value, bounds.
 //
 // Roundings: a bf16 weight to nearest beside an fp32 master; without one, and for
@@ -400,8 +400,8 @@ __device__ __forceinline__ void work(const AdamParams& p, const Factors& f, int 
     }
   } else if constexpr (MX) {
     // Much arithmetic for few bytes: the next values are on their way meanwhile, by copies
-    // into shared memory that each thread makes for itself (with loads alone 304 us
-    // instead of 273 us; with the next ones in registers 323 us).
+    // into shared memory that each thread makes for itself (bf16 weights: with loads
+    // alone 366 us instead of 264 us).
     uint32_t ms, vs, ms1 = 0, vs1 = 0;
     fetch(c, 0, staged[0], ms, vs);
     copies_end_group();
@@ -454,9 +454,9 @@ uint32_t adamw_mix(uint32_t x) { return mix(x); }
 // CTAs are handed out by the hardware, one chunk each: with CTAs that stay and take every
 // n-th chunk 132 million values with fp32 states and masters take 570 us and more instead
 // of 529 us.  MXFP8 states want chunks long enough that the step's factors and the first
-// fetch do not count (1, 4, 8 and 16 vectors: 391, 293, 273 and 273 us), fp32 states
-// one or two (bf16 weights 439 and 417 us; with masters 529 and 533 us); few values come
-// first in giving each SM several chunks.
+// fetch do not count (1, 4, 8 and 16 vectors: 377, 281, 264 and 263 us, with masters 421,
+// 328, 327 and 336 us), fp32 states one or two (bf16 weights 439 and 417 us; with masters
+// 529 and 533 us); few values come first in giving each SM several chunks.
 int adamw_vectors(int64_t values, bool mx) {
   const int64_t v = values / kAdamVector / (152 * 16), most = mx ? 8 : 2;
   return static_cast<int>(v < 1 ? 1 : v > most ? most : v);
